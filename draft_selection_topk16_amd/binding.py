@@ -30,6 +30,9 @@ EXPORTED = (
     "dflash2_topk", "dflash2_lmhead_topk",
     "dflash2_project", "dflash2_pair_scores", "dflash2_viterbi", "dflash2_walk",
     "dflash2_sample_walk", "dflash2_philox_uniforms", "dflash2_philox_uniforms_next",
+    "dflash2_select_sample_rows", "dflash2_draft_rows",
+    "dflash2_kv_append", "dflash2_paged_attention", "dflash2_paged_attention_workspace",
+    "dflash2_verify", "dflash2_verify_workspace",
     "dflash2_conv2", "dflash2_device_error",
     "dflash2_plan_override",
     "dflash2_release",
@@ -51,6 +54,21 @@ class Dims(ctypes.Structure):
                 ("d", ctypes.c_int32), ("r", ctypes.c_int32), ("dtype", ctypes.c_int)]
 
 
+class PagedKv(ctypes.Structure):
+    """df2_paged_kv."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_cache", "v_cache", "block_table", "ctx_len", "tok_start")]
+                + [(n, ctypes.c_int64) for n in ("page_stride", "table_stride")]
+                + [(n, ctypes.c_int32) for n in ("B", "N", "Hq", "Hkv", "D", "page_size", "num_pages",
+                                                 "table_width")]
+                + [("dtype", ctypes.c_int)])
+
+
+class VerifyDims(ctypes.Structure):
+    """df2_verify_dims."""
+    _fields_ = [("B", ctypes.c_int32), ("P", ctypes.c_int32), ("V", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("kind", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -65,7 +83,7 @@ def load() -> ctypes.CDLL:
             "(the selector has no fallback path)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, u32p = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_uint32)
-    dp = ctypes.POINTER(Dims)
+    dp, kvp, vdp = ctypes.POINTER(Dims), ctypes.POINTER(PagedKv), ctypes.POINTER(VerifyDims)
     sig = {
         "dflash2_select": [dp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp],
         "dflash2_select_walk": [dp, vp, vp, vp, vp, vp, vp, i32, ctypes.c_int, vp, vp, vp],
@@ -83,6 +101,13 @@ def load() -> ctypes.CDLL:
         "dflash2_philox_uniforms": [ctypes.c_uint64, ctypes.c_uint64, ctypes.c_int64, vp, vp],
         "dflash2_philox_uniforms_next": [ctypes.c_uint64, vp, ctypes.c_int64, vp, vp],
         "dflash2_device_error": [vp, u32p],
+        "dflash2_select_sample_rows": [dp, vp, vp, vp, vp, vp, vp, i32, ctypes.c_float, vp, vp, vp, vp,
+                                       vp, vp, vp],
+        "dflash2_draft_rows": [vp, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp],
+        "dflash2_kv_append": [kvp, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, vp, i32, i32, vp, i64, vp],
+        "dflash2_paged_attention": [kvp, vp, i64, ctypes.c_float, i32, i32, i32, vp, i64, vp, ctypes.c_size_t,
+                                    vp],
+        "dflash2_verify": [vdp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
         "dflash2_plan_override": [ctypes.c_int, i32],
         "dflash2_release": [],
     }
@@ -90,6 +115,9 @@ def load() -> ctypes.CDLL:
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = ctypes.c_int
+    for name, args in {"dflash2_paged_attention_workspace": [kvp, i32], "dflash2_verify_workspace": [vdp]}.items():
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = ctypes.c_size_t
     for name in ("dflash2_status_string",):
         getattr(lib, name).argtypes = [ctypes.c_int]
         getattr(lib, name).restype = ctypes.c_char_p
@@ -149,15 +177,19 @@ class PreparedSelect:
     `u` in place between launches to draw again).  Calling it enqueues one
     launch on the stream that was current when it was prepared.
     walk: "viterbi", "greedy" or "sample" (then u [B, P] float32 uniforms and
-    the temperature; the draws' probabilities land in self.out_q)."""
+    the temperature; the draws' probabilities land in self.out_q, and with
+    rows=True the candidates and the distributions they were drawn from in
+    self.out_cand and self.out_rows)."""
 
     def __init__(self, logits: torch.Tensor, hidden: torch.Tensor, A: torch.Tensor,
                  Bt: torch.Tensor, W: torch.Tensor, prev: torch.Tensor, K: int,
                  out_path: Optional[torch.Tensor] = None,
                  out_score: Optional[torch.Tensor] = None, walk: str = "viterbi",
-                 u: Optional[torch.Tensor] = None, temperature: float = 1.0):
+                 u: Optional[torch.Tensor] = None, temperature: float = 1.0, rows: bool = False):
         lib = load()
         sample = walk == "sample"
+        if rows and not sample:
+            raise ValueError("rows come with the sampling walk")
         wcode = 0 if sample else _walk_code(walk)
         B, P, V = logits.shape
         d = hidden.shape[-1]
@@ -176,7 +208,7 @@ class PreparedSelect:
         if out_score is None:
             out_score = torch.empty((B,), dtype=torch.float32, device=logits.device)
         self.out_path, self.out_score = out_path, out_score
-        self.out_q = None
+        self.out_q = self.out_cand = self.out_rows = None
         self._keep = (logits, hidden, A, Bt, W, prev)
         self._dims = Dims(B, P, V, d, r, dt)
         head = (ctypes.byref(self._dims), _dev(logits, "logits"), _dev(hidden, "hidden"),
@@ -186,9 +218,15 @@ class PreparedSelect:
             self.out_q = torch.empty((B, P), dtype=torch.float32, device=logits.device)
             self._keep += (u,)
             self._fn = lib.dflash2_select_sample
+            more = ()
+            if rows:
+                self._fn = lib.dflash2_select_sample_rows
+                self.out_cand = torch.empty((B, P, int(K)), dtype=torch.int32, device=logits.device)
+                self.out_rows = torch.empty((B, P, int(K)), dtype=torch.float32, device=logits.device)
+                more = (_dev(self.out_cand, "out_cand"), _dev(self.out_rows, "out_rows"))
             self._args = head + (float(temperature), _dev(u, "u"), _dev(out_path, "out_path"),
-                                 _dev(self.out_q, "out_q"), _dev(out_score, "out_score"),
-                                 _stream(logits.device))
+                                 _dev(self.out_q, "out_q"), _dev(out_score, "out_score")) + more + (
+                                 _stream(logits.device),)
         else:
             self._fn = lib.dflash2_select_walk
             self._args = head + (wcode, _dev(out_path, "out_path"), _dev(out_score, "out_score"),
@@ -211,14 +249,17 @@ def select(logits: torch.Tensor, hidden: torch.Tensor, A: torch.Tensor, Bt: torc
 
 def select_sample(logits: torch.Tensor, hidden: torch.Tensor, A: torch.Tensor, Bt: torch.Tensor,
                   W: torch.Tensor, prev: torch.Tensor, K: int, u: torch.Tensor,
-                  temperature: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                  temperature: float = 1.0, rows: bool = False) -> Tuple[torch.Tensor, ...]:
     """Sampling walk in one select call: (path [B, P] int32, q [B, P] float32 =
     each drawn token's probability, score [B] float32); u [B, P] float32
-    uniforms in [0, 1)."""
+    uniforms in [0, 1).  With rows=True also (cand [B, P, K] int32, prob
+    [B, P, K] float32): each position's candidates and the distribution its
+    token was drawn from, as `verify` takes them."""
     call = PreparedSelect(logits, hidden, A, Bt, W, prev, K, walk="sample", u=u,
-                          temperature=temperature)
+                          temperature=temperature, rows=rows)
     path, score = call()
-    return path, call.out_q, score
+    out = path, call.out_q, score
+    return out + (call.out_cand, call.out_rows) if rows else out
 
 
 def topk(logits: torch.Tensor, K: int) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -315,6 +356,22 @@ def sample_walk(S: torch.Tensor, cand: torch.Tensor, u: torch.Tensor,
                                    float(temperature), _dev(path, "path"), _dev(q, "q"),
                                    _dev(score, "score"), _stream(S.device)))
     return path, q, score
+
+
+def draft_rows(S: torch.Tensor, cand: torch.Tensor, path: torch.Tensor,
+               temperature: float = 1.0) -> torch.Tensor:
+    """The distributions [B, P, K] float32 over cand [B, P, K] that the tokens of
+    path [B, P] were drawn from by the sampling walk over S [B, P, K, K]."""
+    lib = load()
+    B, P, K = cand.shape
+    if S.shape != (B, P, K, K) or path.shape != (B, P):
+        raise ValueError("inconsistent shapes")
+    if S.dtype != torch.float32 or cand.dtype != torch.int32 or path.dtype != torch.int32:
+        raise TypeError("S must be float32, cand and path int32")
+    rows = torch.empty((B, P, K), dtype=torch.float32, device=S.device)
+    _check(lib.dflash2_draft_rows(_dev(S, "S"), _dev(cand, "cand"), _dev(path, "path"), B, P, K,
+                                  float(temperature), _dev(rows, "rows"), _stream(S.device)))
+    return rows
 
 
 def philox_uniforms(seed: int, offset: int, n: int, device=None,

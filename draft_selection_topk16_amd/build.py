@@ -11,7 +11,7 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "dflash2.hip")
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("dflash2.hip", "target.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdflash2.so")
 ARCH = "gfx950"
@@ -26,7 +26,7 @@ def hipcc() -> str:
 
 def compile_flags():
     return [
-        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+        f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
         "-I", INCLUDE, "-I", os.path.join(PKG, "csrc"),
         # never emit packed fp32 arithmetic
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -35,17 +35,32 @@ def compile_flags():
 
 
 def build(verbose: bool = False) -> str:
-    """Compile the HIP library; always recompiles."""
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + compile_flags() + [SRC, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
+    """Compile the HIP library (its sources side by side, then one link);
+    always recompiles."""
+    tag = ".tmp%d" % os.getpid()
+    objs = [src + tag + ".o" for src in SOURCES]
+    cmds = [[hipcc()] + compile_flags() + ["-c", src, "-o", obj] for src, obj in zip(SOURCES, objs)]
+    link = [hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared"] + objs + ["-o", LIB + tag]
+    try:
+        if verbose:
+            for cmd in cmds:
+                print(" ".join(cmd), flush=True)
+        running = [subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for cmd in cmds]
+        said = [p.communicate()[0] for p in running]
+        if all(p.returncode == 0 for p in running):
+            if verbose:
+                print(" ".join(link), flush=True)
+            res = subprocess.run(link, capture_output=True, text=True)
+            if res.returncode == 0:
+                os.replace(LIB + tag, LIB)
+                return LIB
+            said.append(res.stdout + res.stderr)
+        sys.stderr.write("".join(said))
         raise RuntimeError("hipcc failed building libdflash2.so")
-    os.replace(tmp, LIB)
-    return LIB
+    finally:
+        for f in objs + [LIB + tag]:
+            if os.path.exists(f):
+                os.remove(f)
 
 
 if __name__ == "__main__":

@@ -1069,6 +1069,29 @@ void launch_gate(const Plan& pl, hipStream_t stream) {
 }  // namespace
 
 // ----------------------------------------------------------------------------
+// What the library's other translation units use (host.hpp).
+// ----------------------------------------------------------------------------
+#include "host.hpp"
+
+namespace df2 {
+namespace host {
+
+df2_status fail_with(df2_status s, const std::string& msg) { return fail(s, msg); }
+df2_status hip_failed(hipError_t e, const char* what) { return hip_fail(e, what); }
+void clear_error() { g_last_error.clear(); }
+int compute_units() { return cu_count(); }
+
+df2_status device_flag_word(uint32_t** word) {
+    void* base = nullptr;
+    const df2_status st = static_scratch(&base);
+    *word = reinterpret_cast<uint32_t*>(base);
+    return st;
+}
+
+}  // namespace host
+}  // namespace df2
+
+// ----------------------------------------------------------------------------
 // C ABI
 // ----------------------------------------------------------------------------
 extern "C" {
@@ -1090,15 +1113,25 @@ const char* dflash2_last_error(void) { return g_last_error.c_str(); }
 
 }  // extern "C"
 
+// The sampling walk's draft distributions: a kernel of its own (drafts.hpp).
+#include "drafts.hpp"
+
 namespace {
 
+df2_status launch_draft_rows(const DraftArgs& a, int B, hipStream_t stream) {
+    return launch_checked(
+        [&] { hipLaunchKernelGGL(k_draft_rows, dim3((unsigned)((int64_t)B * a.P)), dim3(64), 0, stream, a); },
+        "draft rows launch");
+}
+
 // The fused selector with any walk; the sampling walk also takes u, 1 / tau
-// and out_q (checked by the caller).
+// and out_q (checked by the caller), and may return the candidates and the
+// distributions it drew from.
 df2_status select_common(const df2_dims* dims, const void* logits, const void* hidden,
                          const void* A_tab, const void* B_tab, const void* W_H,
                          const int32_t* prev_tok, int32_t K, int walk, const float* u, float inv_tau,
                          int32_t* out_path, float* out_q, float* out_score, hipStream_t stream,
-                         bool noalloc = false) {
+                         bool noalloc = false, int32_t* out_cand = nullptr, float* out_rows = nullptr) {
     df2_status st = check_dims(dims, true);
     if (st != DF2_OK) return st;
     if ((st = check_k(K, dims->V)) != DF2_OK) return st;
@@ -1173,7 +1206,7 @@ df2_status select_common(const df2_dims* dims, const void* logits, const void* h
         note_layout(stream, pl.counter_bytes);
     }
     bind_scratch(pl, base, rows, dims->B);
-    return launch_checked([&] {
+    st = launch_checked([&] {
         if (noalloc) {
             // the counters (all words after the device flag word) start at
             // zero; the previous call may have left data there
@@ -1183,6 +1216,10 @@ df2_status select_common(const df2_dims* dims, const void* logits, const void* h
         }
         launch_select(pl, stream);
     }, "dflash2_select launch");
+    if (st != DF2_OK || !out_rows) return st;
+    // the pair scores and candidates are still in the scratch, in stream order
+    return launch_draft_rows(DraftArgs{p.Sb, p.cand, out_path, out_cand, out_rows, p.P, p.K, inv_tau},
+                             dims->B, stream);
 }
 
 // 1 / tau for the sampling walk, or an error for a temperature that is not
@@ -1227,6 +1264,27 @@ df2_status dflash2_select_sample(const df2_dims* dims, const void* logits, const
     }
     return select_common(dims, logits, hidden, A_tab, B_tab, W_H, prev_tok, K, kWalkSample, u,
                          inv_tau, out_path, out_q, out_score, stream);
+}
+
+df2_status dflash2_select_sample_rows(const df2_dims* dims, const void* logits, const void* hidden,
+                                      const void* A_tab, const void* B_tab, const void* W_H,
+                                      const int32_t* prev_tok, int32_t K, float temperature,
+                                      const float* u, int32_t* out_path, float* out_q,
+                                      float* out_score, int32_t* out_cand, float* out_rows,
+                                           hipStream_t stream) {
+    g_last_error.clear();
+    float inv_tau = 0.f;
+    df2_status st = sample_inv_tau(temperature, &inv_tau);
+    if (st != DF2_OK) return st;
+    if (dims && dims->B > 0) {
+        if (!u || !out_q || !out_cand || !out_rows) return fail(DF2_EINVAL, "NULL pointer argument");
+        if (((uintptr_t)u & 3u) || ((uintptr_t)out_q & 3u))
+            return fail(DF2_EINVAL, "u and out_q must be 4-byte aligned");
+        if (((uintptr_t)out_cand & 3u) || ((uintptr_t)out_rows & 3u))
+            return fail(DF2_EINVAL, "out_cand and out_rows must be 4-byte aligned");
+    }
+    return select_common(dims, logits, hidden, A_tab, B_tab, W_H, prev_tok, K, kWalkSample, u,
+                         inv_tau, out_path, out_q, out_score, stream, false, out_cand, out_rows);
 }
 
 df2_status dflash2_select(const df2_dims* dims, const void* logits, const void* hidden,
@@ -1415,6 +1473,24 @@ df2_status dflash2_sample_walk(const float* S, const int32_t* cand_idx, const fl
     }
     return walk_common(S, cand_idx, B, P, K, kWalkSample, u, inv_tau, out_path, out_q, out_score,
                        stream);
+}
+
+df2_status dflash2_draft_rows(const float* S, const int32_t* cand_idx, const int32_t* path, int32_t B,
+                              int32_t P, int32_t K, float temperature, float* out_rows,
+                              hipStream_t stream) {
+    g_last_error.clear();
+    float inv_tau = 0.f;
+    df2_status st = sample_inv_tau(temperature, &inv_tau);
+    if (st != DF2_OK) return st;
+    if (B < 0) return fail(DF2_EINVAL, "B < 0");
+    if (P < 1 || P > kMaxP) return fail(DF2_EINVAL, "P must be in [1, 64]");
+    if (K < 1 || K > kMaxK) return fail(DF2_EINVAL, "K must be in [1, 64]");
+    if (B == 0) return DF2_OK;
+    if ((int64_t)B * P > 0x7FFFFFFF) return fail(DF2_EUNSUPPORTED, "too many rows");
+    if (!S || !cand_idx || !path || !out_rows) return fail(DF2_EINVAL, "NULL pointer argument");
+    if (((uintptr_t)S & 3u) || ((uintptr_t)cand_idx & 3u) || ((uintptr_t)path & 3u) || ((uintptr_t)out_rows & 3u))
+        return fail(DF2_EINVAL, "arguments must be 4-byte aligned");
+    return launch_draft_rows(DraftArgs{S, cand_idx, path, nullptr, out_rows, P, K, inv_tau}, B, stream);
 }
 
 namespace {

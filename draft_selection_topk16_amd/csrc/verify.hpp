@@ -1,0 +1,505 @@
+// Verification of drafted tokens against the target's rows, from given
+// uniforms ("DFlash 2: Keep Drafting Parallel", section "A Lightweight Path
+// Selector": rejection sampling restores the exact target distribution).
+//
+// Row t of a sequence holds the target's logits after its first t drafted
+// tokens.  With weights w(v) = exp((x(v) - max) / temperature), or the given
+// probabilities themselves, p(v) = w(v) / Z, Z = sum w:
+//   * draft t is accepted while u_t q_t(d_t) < p_t(d_t), q_t(d) the draft's
+//     probability of d;
+//   * at the first row a where it is not, the next token comes from
+//     max(p_a - q_a, 0), which only differs from p_a at the K candidates;
+//   * with every draft accepted, from p_a, a = the number of drafts:
+//     the first v whose running sum exceeds u_P times the whole sum.
+//
+// Launch 1 reads every row once: (max, sum) of each segment in fp32, a maximum
+// per lane with rescaling, so one pass does.  Launch 2 works on the one row a
+// that the draw needs, whose place the partial sums decide: its weights in
+// fp64, because the drawn index must not depend on how sums were rounded (151
+// thousand boundaries stand an fp32 rounding apart from a uniform now and
+// then); each workgroup sums a segment, and the last to finish picks the
+// segment, then a lane's run of it, then the token.
+#pragma once
+
+#include "common.hpp"
+
+namespace df2 {
+
+constexpr uint32_t kFlagDraft = 32u;    // a drafted token outside [0, V)
+constexpr uint32_t kFlagNoMass = 64u;   // a target row without weight
+constexpr int kVerifySegs = 64;         // most segments of a row
+
+enum VerifyKind { kVerifyLogits = 0, kVerifyProbs = 1, kVerifyArgmax = 2 };
+
+struct VerifyArgs {
+    const void* target;         // [B, P + 1, V]
+    const int32_t* path;        // [B, P]
+    const int32_t* cand;        // [B, P, K]
+    const float* prob;          // [B, P, K]
+    const int32_t* n_draft;     // [B] or NULL
+    const float* u;             // [B, P + 1]
+    int32_t* out_tok;           // [B, P + 1]
+    int32_t* out_len;           // [B]
+    float* out_prob;            // [B, P + 1]
+    uint64_t* part;             // [B * (P + 1), nseg] (max, sum) or best word of a segment
+    double* seg;                // [B, nseg2] fp64 sums of the drawn row's segments
+    uint32_t* cnt;              // [B] arrivals, zeroed by launch 1
+    uint32_t* err;
+    int B, P, V, K;
+    int nseg, nseg2;
+    float c;                    // log2(e) / temperature
+    double c64;
+};
+
+// Elements of a row split over segments: whole 16-byte vectors where they are
+// aligned, the elements before the first and behind the last one to the first
+// and last segment.
+template <bool BF16>
+struct RowCut {
+    static constexpr int kE = BF16 ? 8 : 4, kSz = BF16 ? 2 : 4;
+    int head, nv, V;
+    __device__ __forceinline__ RowCut(const char* row, int V_) : V(V_) {
+        const int off = (int)((uintptr_t)row & 15u);
+        head = min(V_, off ? (16 - off) / kSz : 0);
+        nv = (V_ - head) / kE;
+    }
+    __device__ __forceinline__ int first_vec(int s, int nseg) const { return (int)((int64_t)nv * s / nseg); }
+    __device__ __forceinline__ int first(int s, int nseg) const {
+        return s == 0 ? 0 : (s == nseg ? V : head + first_vec(s, nseg) * kE);
+    }
+};
+
+template <bool BF16>
+__device__ __forceinline__ float row_value(const char* row, int v) {
+    if constexpr (BF16) return bf16_lo(reinterpret_cast<const uint16_t*>(row)[v]);
+    else return reinterpret_cast<const float*>(row)[v];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack16(u32x4_t w, float (&x)[BF16 ? 8 : 4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+            x[2 * i] = bf16_lo(w[i]);
+            x[2 * i + 1] = bf16_hi(w[i]);
+        } else {
+            x[i] = __uint_as_float(w[i]);
+        }
+    }
+}
+
+// 2^y in fp64 for y <= 0: whole part by exponent, the rest by its series (the
+// first term left out is below 2 10^-13).
+__device__ __forceinline__ double exp2_64(double y) {
+    if (y < -1000.0) return 0.0;
+    const double n = rint(y), f = (y - n) * 0.69314718055994531;
+    double s = 1.0 / 3628800.0;
+    s = fma(s, f, 1.0 / 362880.0);
+    s = fma(s, f, 1.0 / 40320.0);
+    s = fma(s, f, 1.0 / 5040.0);
+    s = fma(s, f, 1.0 / 720.0);
+    s = fma(s, f, 1.0 / 120.0);
+    s = fma(s, f, 1.0 / 24.0);
+    s = fma(s, f, 1.0 / 6.0);
+    s = fma(s, f, 0.5);
+    s = fma(s, f, 1.0);
+    s = fma(s, f, 1.0);
+    return ldexp(s, (int)n);
+}
+
+// A value's weight; m: the row's maximum (logits).
+template <int KIND>
+__device__ __forceinline__ double weight64(float x, float m, double c64) {
+    if constexpr (KIND == kVerifyProbs) return fmax((double)x, 0.0);
+    return exp2_64(((double)x - (double)m) * c64);
+}
+
+// Running (max, sum) of weights.
+struct Lse {
+    float m, s;
+};
+template <int KIND>
+__device__ __forceinline__ Lse lse_join(Lse a, Lse b, float c) {
+    if constexpr (KIND == kVerifyProbs) return {0.f, a.s + b.s};
+    const float m = fmaxf(a.m, b.m);
+    if (m == -INFINITY) return {m, 0.f};
+    return {m, a.s * __builtin_amdgcn_exp2f((a.m - m) * c) + b.s * __builtin_amdgcn_exp2f((b.m - m) * c)};
+}
+
+// Launch 1: one workgroup a segment of a row.
+template <bool BF16, int KIND>
+__global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
+    constexpr int E = RowCut<BF16>::kE, SZ = RowCut<BF16>::kSz, U = 4;
+    __shared__ uint64_t red[kWaves];
+    const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
+    const int64_t row = blockIdx.x / a.nseg;
+    const int seg = (int)(blockIdx.x % a.nseg);
+    if (seg == 0 && tid == 0 && row % (a.P + 1) == 0) a.cnt[row / (a.P + 1)] = 0;
+    const char* rp = reinterpret_cast<const char*>(a.target) + (size_t)row * a.V * SZ;
+    const RowCut<BF16> cut(rp, a.V);
+    const int v0 = cut.first_vec(seg, a.nseg), v1 = cut.first_vec(seg + 1, a.nseg);
+    const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(rp + (size_t)cut.head * SZ);
+
+    Lse acc = {KIND == kVerifyProbs ? 0.f : -INFINITY, 0.f};
+    uint64_t best = 0;
+    auto take = [&](const float* x, int n, int at) {
+        if constexpr (KIND == kVerifyArgmax) {
+            for (int i = 0; i < n; ++i) {
+                const uint64_t word = cand_word(key_f32(__float_as_uint(x[i])), (uint32_t)(at + i));
+                best = word > best ? word : best;
+            }
+        } else if constexpr (KIND == kVerifyProbs) {
+            for (int i = 0; i < n; ++i) acc.s += fmaxf(x[i], 0.f);
+        } else {
+            float m = x[0];
+            for (int i = 1; i < n; ++i) m = fmaxf(m, x[i]);
+            if (m > acc.m) {
+                acc.s *= __builtin_amdgcn_exp2f((acc.m - m) * a.c);
+                acc.m = m;
+            }
+            // the difference first: the product's rounding is then relative to it
+            const float mm = acc.m == -INFINITY ? 0.f : acc.m;
+            for (int i = 0; i < n; ++i) acc.s += __builtin_amdgcn_exp2f((x[i] - mm) * a.c);
+        }
+    };
+    for (int v = v0 + tid; v < v1; v += kWG * U) {
+        u32x4_t ld[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            ld[i] = __builtin_nontemporal_load(vp + min(v + i * kWG, v1 - 1));
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (v + i * kWG < v1) {
+                float x[E];
+                unpack16<BF16>(ld[i], x);
+                take(x, E, cut.head + (v + i * kWG) * E);
+            }
+        }
+    }
+    if (seg == 0 && tid < cut.head) {
+        const float x[1] = {row_value<BF16>(rp, tid)};
+        take(x, 1, tid);
+    }
+    const int tail = cut.head + cut.nv * E + tid;
+    if (seg == a.nseg - 1 && tail < a.V) {
+        const float x[1] = {row_value<BF16>(rp, tail)};
+        take(x, 1, tail);
+    }
+    if constexpr (KIND == kVerifyArgmax) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            const uint64_t y = __shfl_xor((unsigned long long)best, o);
+            best = y > best ? y : best;
+        }
+    } else {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            const Lse y = {__shfl_xor(acc.m, o), __shfl_xor(acc.s, o)};
+            acc = lse_join<KIND>(acc, y, a.c);
+        }
+        best = ((uint64_t)__float_as_uint(acc.m) << 32) | __float_as_uint(acc.s);
+    }
+    if (lane == 0) red[w] = best;
+    __syncthreads();
+    if (tid == 0) {
+        uint64_t out = red[0];
+        for (int i = 1; i < kWaves; ++i) {
+            if constexpr (KIND == kVerifyArgmax) {
+                out = red[i] > out ? red[i] : out;
+            } else {
+                const Lse y = lse_join<KIND>({__uint_as_float((uint32_t)(out >> 32)), __uint_as_float((uint32_t)out)},
+                                             {__uint_as_float((uint32_t)(red[i] >> 32)), __uint_as_float((uint32_t)red[i])}, a.c);
+                out = ((uint64_t)__float_as_uint(y.m) << 32) | __float_as_uint(y.s);
+            }
+        }
+        a.part[row * a.nseg + seg] = out;
+    }
+}
+
+struct VerifyLds {
+    float m[72], s[72];         // maximum and sum of each row (P + 1 <= 65)
+    float odds[72];             // p of each draft
+    int cid[64];                // candidates of the drawn row and what they lose
+    double cut[64];
+    double lane_sum[kWG];
+    int taken, nd, pick;
+    uint32_t flag;
+    double z, target;
+    int seg;
+};
+
+// One wave finds the first of n <= 256 values whose running sum exceeds
+// `target` and takes the sum before it off `target`.  A target that rounding
+// put at or past the whole becomes the last bit of it.  Every lane calls; the
+// result is the same in all of them.
+__device__ __forceinline__ int find_prefix(const double* sum, int n, double& target) {
+    const int lane = lane_id();
+    double x[4], own = 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[j] = 4 * lane + j < n ? sum[4 * lane + j] : 0.0;
+        own += x[j];
+    }
+    double incl = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double up = __shfl_up(incl, o);
+        incl += lane >= o ? up : 0.0;
+    }
+    const double whole = __shfl(incl, 63);
+    if (!(target < whole)) target = whole * (1.0 - 0x1p-40);
+    const uint64_t some = __ballot(own > 0.0), hit = __ballot(own > 0.0 && target < incl);
+    if (!some) return 0;
+    const int f = hit ? __builtin_ctzll(hit) : 63 - __builtin_clzll(some);
+    double run = f > 0 ? __shfl(incl, f - 1) : 0.0;
+    int at = -1, last = 0;
+    double before = run;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const double y = __shfl(x[j], f);
+        if (at < 0 && y > 0.0) {
+            last = 4 * f + j;
+            before = run;
+            if (target < run + y) at = last;
+        }
+        run += y;
+    }
+    target -= before;
+    return at >= 0 ? at : last;
+}
+
+// Launch 2 (sampling): nseg2 workgroups a sequence.
+template <bool BF16, int KIND>
+__global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
+    constexpr int E = RowCut<BF16>::kE, SZ = RowCut<BF16>::kSz;
+    __shared__ VerifyLds sm;
+    const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
+    const int b = (int)(blockIdx.x / a.nseg2), seg = (int)(blockIdx.x % a.nseg2);
+    const int P = a.P, R = P + 1, K = a.K;
+    const int64_t row0 = (int64_t)b * R;
+
+    // 1. Every row's maximum and sum from its segments.
+    for (int t = w; t < R; t += kWaves) {
+        Lse acc = {KIND == kVerifyProbs ? 0.f : -INFINITY, 0.f};
+        if (lane < a.nseg) {
+            const uint64_t x = a.part[(row0 + t) * a.nseg + lane];
+            acc = {__uint_as_float((uint32_t)(x >> 32)), __uint_as_float((uint32_t)x)};
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            const Lse y = {__shfl_xor(acc.m, o), __shfl_xor(acc.s, o)};
+            acc = lse_join<KIND>(acc, y, a.c);
+        }
+        if (lane == 0) {
+            sm.m[t] = acc.m;
+            sm.s[t] = acc.s;
+        }
+    }
+    __syncthreads();
+
+    // 2. Which drafts are accepted: lane t of wave 0 takes draft t.
+    if (w == 0) {
+        const int nd = a.n_draft ? min(max(a.n_draft[b], 0), P) : P;
+        bool yes = false;
+        if (lane < P) {
+            const int32_t d = a.path[(int64_t)b * P + lane];
+            double p = 0.0;
+            if ((unsigned)d < (unsigned)a.V) {
+                const char* rp = reinterpret_cast<const char*>(a.target) + (size_t)(row0 + lane) * a.V * SZ;
+                if (sm.s[lane] > 0.f)
+                    p = weight64<KIND>(row_value<BF16>(rp, d), sm.m[lane], a.c64) / (double)sm.s[lane];
+            } else if (lane < nd) {
+                atomicOr(a.err, kFlagDraft);
+            }
+            double q = 0.0;
+            for (int k = 0; k < K; ++k) {
+                const int64_t at = ((int64_t)b * P + lane) * K + k;
+                q += a.cand[at] == d ? (double)a.prob[at] : 0.0;
+            }
+            float u = a.u[row0 + lane];
+            u = (u >= 0.f) ? fminf(u, 0x1.fffffep-1f) : 0.f;
+            yes = lane < nd && (double)u * q < p;
+            sm.odds[lane] = (float)p;
+        }
+        const uint64_t ok = __ballot(yes);
+        const int taken = ~ok ? __builtin_ctzll(~ok) : 64;
+        if (lane == 0) {
+            sm.taken = min(taken, nd);
+            sm.nd = nd;
+        }
+    }
+    __syncthreads();
+    const int t = sm.taken;
+    const bool refused = t < sm.nd;
+    const float m = sm.m[t];
+    const char* rp = reinterpret_cast<const char*>(a.target) + (size_t)(row0 + t) * a.V * SZ;
+    const RowCut<BF16> cut(rp, a.V);
+
+    // 3. This segment of row t in fp64.
+    const bool mass = sm.s[t] > 0.f;
+    {
+        const int v0 = cut.first_vec(seg, a.nseg2), v1 = cut.first_vec(seg + 1, a.nseg2);
+        const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(rp + (size_t)cut.head * SZ);
+        double s = 0.0;
+        for (int v = v0 + tid; v < v1; v += kWG) {
+            float x[E];
+            unpack16<BF16>(vp[v], x);
+#pragma unroll
+            for (int i = 0; i < E; ++i) s += weight64<KIND>(x[i], m, a.c64);
+        }
+        if (seg == 0 && tid < cut.head) s += weight64<KIND>(row_value<BF16>(rp, tid), m, a.c64);
+        const int tail = cut.head + cut.nv * E + tid;
+        if (seg == a.nseg2 - 1 && tail < a.V) s += weight64<KIND>(row_value<BF16>(rp, tail), m, a.c64);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+        if (lane == 0) sm.lane_sum[w] = s;
+        __syncthreads();
+        if (tid == 0) xstore(a.seg + (int64_t)b * a.nseg2 + seg, sm.lane_sum[0] + sm.lane_sum[1] + sm.lane_sum[2] + sm.lane_sum[3]);
+    }
+    if (!block_arrive_last(&a.cnt[b], (uint32_t)a.nseg2, &sm.flag)) return;
+
+    // 4. The last workgroup draws.  Segment sums and what the candidates lose:
+    // min(w, q Z) each.
+    if (tid < a.nseg2) sm.lane_sum[tid] = xload(a.seg + (int64_t)b * a.nseg2 + tid);
+    __syncthreads();
+    if (w == 0) {
+        double z = lane < a.nseg2 ? sm.lane_sum[lane] : 0.0;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o);
+        if (lane == 0) sm.z = z;
+    }
+    __syncthreads();
+    if (tid < K) {
+        int id = -1;
+        float q = 0.f;
+        double loss = 0.0;
+        if (refused) {
+            const int64_t at = ((int64_t)b * P + t) * K + tid;
+            id = a.cand[at];
+            q = a.prob[at];
+            if ((unsigned)id >= (unsigned)a.V) {
+                atomicOr(a.err, 2u);
+                id = -1;
+            } else {
+                loss = fmin(weight64<KIND>(row_value<BF16>(rp, id), m, a.c64), fmax((double)q * sm.z, 0.0));
+            }
+        }
+        sm.cid[tid] = id;
+        sm.cut[tid] = loss;
+    }
+    __syncthreads();
+    auto loss_in = [&](int e0, int e1) {
+        double x = 0.0;
+        for (int k = 0; k < K; ++k) x += (sm.cid[k] >= e0 && sm.cid[k] < e1) ? sm.cut[k] : 0.0;
+        return x;
+    };
+    if (tid < a.nseg2) {
+        const double s = sm.lane_sum[tid] - loss_in(cut.first(tid, a.nseg2), cut.first(tid + 1, a.nseg2));
+        sm.lane_sum[tid] = s > 0.0 ? s : 0.0;
+    }
+    __syncthreads();
+    if (w == 0) {
+        double whole = lane < a.nseg2 ? sm.lane_sum[lane] : 0.0;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) whole += __shfl_xor(whole, o);
+        float u = a.u[row0 + P];
+        u = (u >= 0.f) ? fminf(u, 0x1.fffffep-1f) : 0.f;
+        double target = (double)u * whole;
+        const int at = find_prefix(sm.lane_sum, a.nseg2, target);
+        if (lane == 0) {
+            sm.seg = at;
+            sm.target = target;
+        }
+    }
+    __syncthreads();
+    // a run of the segment for each lane
+    const int e0 = cut.first(sm.seg, a.nseg2), e1 = cut.first(sm.seg + 1, a.nseg2);
+    const int len = (e1 - e0 + kWG - 1) / kWG;
+    {
+        const int i0 = min(e0 + tid * len, e1), i1 = min(i0 + len, e1);
+        double s = 0.0;
+        for (int i = i0; i < i1; ++i) s += weight64<KIND>(row_value<BF16>(rp, i), m, a.c64);
+        s -= loss_in(i0, i1);
+        sm.lane_sum[tid] = s > 0.0 ? s : 0.0;
+    }
+    __syncthreads();
+    if (w == 0) {
+        double target = sm.target;
+        const int at = find_prefix(sm.lane_sum, kWG, target);
+        const int i0 = min(e0 + at * len, e1), i1 = min(i0 + len, e1);
+        double run = 0.0;
+        int pick = -1, last = -1;
+        for (int c0 = i0; c0 < i1 && pick < 0; c0 += 64) {
+            const int i = c0 + lane;
+            double x = 0.0;
+            if (i < i1) {
+                x = weight64<KIND>(row_value<BF16>(rp, i), m, a.c64) - loss_in(i, i + 1);
+                x = x > 0.0 ? x : 0.0;
+            }
+            double incl = x;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const double up = __shfl_up(incl, o);
+                incl += lane >= o ? up : 0.0;
+            }
+            const uint64_t some = __ballot(x > 0.0);
+            const uint64_t hit = __ballot(x > 0.0 && target < run + incl);
+            if (hit) pick = c0 + __builtin_ctzll(hit);
+            if (some) last = c0 + 63 - __builtin_clzll(some);
+            run += __shfl(incl, 63);
+        }
+        if (pick < 0) pick = last;
+        const bool ok = mass && pick >= 0 && pick < a.V;
+        if (!ok) {
+            pick = 0;
+            if (lane == 0) atomicOr(a.err, kFlagNoMass);
+        }
+        if (lane == 0) {
+            sm.pick = pick;
+            sm.odds[t] = ok ? (float)(weight64<KIND>(row_value<BF16>(rp, pick), m, a.c64) / sm.z) : 0.f;
+            a.out_len[b] = t + 1;
+        }
+    }
+    __syncthreads();
+    if (tid < R) {
+        a.out_tok[row0 + tid] = tid < t ? a.path[(int64_t)b * P + tid] : (tid == t ? sm.pick : -1);
+        a.out_prob[row0 + tid] = tid <= t ? sm.odds[tid] : 0.f;
+    }
+}
+
+// Launch 2 at temperature 0: a draft is accepted while it is its row's best
+// token; the next token is the best of the row after the last accepted one.
+template <bool BF16>
+__global__ __launch_bounds__(kWG) void k_verify_best(VerifyArgs a) {
+    __shared__ int best[72];
+    const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
+    const int b = (int)blockIdx.x, P = a.P, R = P + 1;
+    const int64_t row0 = (int64_t)b * R;
+    for (int t = w; t < R; t += kWaves) {
+        uint64_t x = lane < a.nseg ? a.part[(row0 + t) * a.nseg + lane] : 0;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            const uint64_t y = __shfl_xor((unsigned long long)x, o);
+            x = y > x ? y : x;
+        }
+        if (lane == 0) best[t] = (int)cand_index(x);
+    }
+    __syncthreads();
+    if (w != 0) return;
+    const int nd = a.n_draft ? min(max(a.n_draft[b], 0), P) : P;
+    bool yes = false;
+    if (lane < P) {
+        const int32_t d = a.path[(int64_t)b * P + lane];
+        if ((unsigned)d >= (unsigned)a.V && lane < nd) atomicOr(a.err, kFlagDraft);
+        yes = lane < nd && d == best[lane];
+    }
+    const uint64_t ok = __ballot(yes);
+    const int t = min(~ok ? __builtin_ctzll(~ok) : 64, nd);
+    if (lane == 0) a.out_len[b] = t + 1;
+    for (int i = lane; i < R; i += 64) {
+        a.out_tok[row0 + i] = i <= t ? best[i] : -1;
+        a.out_prob[row0 + i] = i <= t ? 1.f : 0.f;
+    }
+}
+
+}  // namespace df2

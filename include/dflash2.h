@@ -188,6 +188,23 @@ df2_status dflash2_select_sample(const df2_dims* dims, const void* logits,
                                  float* out_score, hipStream_t stream);
 
 /*
+ * dflash2_select_sample that also returns what each token was drawn from, as
+ * dflash2_verify takes it (one small launch more):
+ *   out_cand [B, P, K] int32  candidates of each position, best first
+ *   out_rows [B, P, K] float  q_t over them; the entry of the drawn token is
+ *                             out_q bit for bit
+ * Other arguments as for dflash2_select_sample.
+ */
+df2_status dflash2_select_sample_rows(const df2_dims* dims, const void* logits,
+                                      const void* hidden, const void* A_tab,
+                                      const void* B_tab, const void* W_H,
+                                      const int32_t* prev_tok, int32_t K,
+                                      float temperature, const float* u,
+                                      int32_t* out_path, float* out_q,
+                                      float* out_score, int32_t* out_cand,
+                                      float* out_rows, hipStream_t stream);
+
+/*
  * dflash2_select that allocates nothing, for callers that cannot allocate
  * device memory (code under HIP graph capture, tight serving loops,
  * harnesses that forbid it).  Same arguments, arithmetic and results as
@@ -317,6 +334,18 @@ df2_status dflash2_sample_walk(const float* S, const int32_t* cand_idx,
                                hipStream_t stream);
 
 /*
+ * The distributions that a path's tokens were drawn from, over given scores
+ * (see dflash2_select_sample_rows): out_rows[b][t] is the softmax over
+ * temperature of S[b][t][i], i the rank of path[b][t - 1] in cand_idx[b][t - 1]
+ * (row 0 at t == 0, and for a token that is no candidate).
+ *   S [B, P, K, K] float, cand_idx [B, P, K] int32, path [B, P] int32,
+ *   out_rows [B, P, K] float
+ */
+df2_status dflash2_draft_rows(const float* S, const int32_t* cand_idx, const int32_t* path,
+                              int32_t B, int32_t P, int32_t K, float temperature,
+                              float* out_rows, hipStream_t stream);
+
+/*
  * Uniforms for the sampling walk, drawn on the device from a counter-based
  * generator (same section: sampling draws from the same scores, one uniform
  * per draft position), so a serving loop need not bring them from the host.
@@ -378,13 +407,160 @@ df2_status dflash2_conv2(const void* x, const void* x_prev, const void* base,
                          df2_dtype dtype, void* out, hipStream_t stream);
 
 /*
+ * The target's side of a draft-verify cycle.  The target runs the last
+ * verified token and the drafted ones as one block: their keys and values are
+ * appended to a paged cache, they attend over it, and its output rows decide
+ * which drafts stand.
+ *
+ * A paged cache of one layer and the new tokens of a batch:
+ *   k_cache, v_cache  pages of [Hkv, page_size, D] elements each, page p at
+ *                     element p * page_stride; 16-byte aligned
+ *   block_table  [B, table_width] int32, rows table_stride apart: the pages of
+ *                each sequence in order of position
+ *   ctx_len      [B] int32    tokens the cache holds before the new ones
+ *   tok_start    [B + 1] int32, ascending: sequence b's new tokens are rows
+ *                tok_start[b] .. tok_start[b + 1] - 1 of the N token rows (any
+ *                count, zero too); new token j has position ctx_len[b] + j
+ *   B, N         sequences, token rows (0: nothing is enqueued).  Rows that no
+ *                sequence owns are neither read nor written.
+ *   Hq, Hkv, D   query heads, key/value heads (Hq a multiple of Hkv; query
+ *                head i reads key/value head i / (Hq / Hkv)), head size 64, 128 or 256
+ *   page_size    a power of two up to 65536
+ *   num_pages    pages in the cache; a page id outside [0, num_pages) raises
+ *                device flag bit 3: nothing is written there, and reads take
+ *                page 0 instead
+ *   table_width  pages a sequence may have (table_width * page_size <= 2^30);
+ *                with ctx_len + new tokens beyond them, flag bit 4 is raised
+ *                and ctx_len taken as if the last new token had the last place
+ * Token rows of queries, keys, values and outputs hold their heads one after
+ * the other ([heads, D]); their stride from token to token is given in
+ * elements, a multiple of 16 bytes, so that they may be parts of one row.
+ * These entry points keep no scratch: workspace belongs to the caller, its
+ * contents need not survive between calls, and calls that share one must be
+ * ordered.  They allocate nothing, enqueue kernels only and can be captured.
+ */
+typedef struct df2_paged_kv {
+    void* k_cache;
+    void* v_cache;
+    const int32_t* block_table;
+    const int32_t* ctx_len;
+    const int32_t* tok_start;
+    int64_t page_stride, table_stride;
+    int32_t B, N, Hq, Hkv, D, page_size, num_pages, table_width;
+    df2_dtype dtype;
+} df2_paged_kv;
+
+/*
+ * Appends the new tokens' keys and values to the cache, normed and rotated,
+ * and norms and rotates their queries:
+ *     y = x * rsqrt(mean(x^2) + eps) * w            (norm of each head)
+ *     (a, b) -> (a cos - b sin, b cos + a sin)      angle = position * rope_freq[i]
+ *   q       token rows of Hq heads, or NULL with out_q (keys and values only)
+ *   k, v    token rows of Hkv heads; v is copied as it is
+ *   q_norm, k_norm [D] (dtype) weights, or NULL: no norm; 16-byte aligned
+ *   rope_freq [rot / 2] double  radians a position; rot: leading elements of a
+ *           head that are rotated, a multiple of 16 (0: none, rope_freq unused)
+ *   interleaved  pair i is elements (i, i + rot / 2) if 0, else (2i, 2i + 1)
+ *   out_q   token rows of Hq heads; may be q itself with q's stride
+ * fp32 arithmetic (angles reduced in fp64), one rounding at the store.  A
+ * token with a negative position is not written to the cache.
+ */
+df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_stride,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const void* q_norm, const void* k_norm, float eps,
+                             const double* rope_freq, int32_t rot, int32_t interleaved,
+                             void* out_q, int64_t out_q_stride, hipStream_t stream);
+
+/*
+ * Attention of the new tokens over their sequences' cached positions
+ * 0 .. ctx_len + n - 1 (n new tokens, whose keys and values are in the cache):
+ *     out = softmax(scale * q k^T) v
+ *   causal  new token t sees positions up to its own; 0: all of them (the
+ *           drafter's block)
+ *   window  0, or how many positions back from its own a token sees (its own
+ *           counts); a token whose position is negative sees none and gets 0
+ *   scale   positive and finite
+ *   max_len an upper estimate of ctx_len + n over the batch for the launch
+ *           plan, 0: table_width * page_size; results do not depend on its truth
+ *   q, out  token rows of Hq heads (dtype); out must not overlap q
+ *   workspace  dflash2_paged_attention_workspace(kv, max_len) bytes (0: may be
+ *           NULL), 16-byte aligned
+ * Scores, softmax statistics and sums are fp32; bf16 probabilities are
+ * rounded to bf16 for the second product.  Keys and values that a token of
+ * the batch sees must be finite; whatever else stands in the pages is not
+ * used.
+ */
+size_t dflash2_paged_attention_workspace(const df2_paged_kv* kv, int32_t max_len);
+df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_t q_stride,
+                                   float scale, int32_t causal, int32_t window,
+                                   int32_t max_len, void* out, int64_t out_stride,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* What the rows given to dflash2_verify hold. */
+typedef enum { DF2_TARGET_LOGITS = 0, DF2_TARGET_PROBS = 1 } df2_target_kind;
+
+/*
+ * Sizes of a verification: B sequences (0 enqueues nothing), P drafted
+ * positions (1 .. 64), vocabulary V (<= 2^29), K candidates a position
+ * (1 .. min(V, 64)); dtype and kind of the target rows.
+ */
+typedef struct df2_verify_dims {
+    int32_t B, P, V, K;
+    df2_dtype dtype;
+    df2_target_kind kind;
+} df2_verify_dims;
+
+/*
+ * Verification of drafted tokens against the target (same section: rejection
+ * sampling restores the exact target distribution), from given uniforms.
+ * With p_t the target's distribution after t drafted tokens (softmax of row t
+ * over temperature, or row t over its sum) and q_t the draft's, which is
+ * cand_prob on the candidates and 0 elsewhere:
+ *     draft t is accepted while u[b][t] * q_t(path_t) < p_t(path_t);
+ *     at the first t where it is not, the next token is drawn from
+ *     max(p_t - q_t, 0); with all accepted, from the row behind the last;
+ *     a draw takes the first v whose running sum exceeds u[b][P] * (whole sum).
+ *   target    [B, P + 1, V] (dtype)
+ *   path      [B, P] int32    drafted tokens (an id outside [0, V) is refused
+ *                             and raises flag bit 5)
+ *   cand_idx  [B, P, K] int32, distinct in a row, cand_prob [B, P, K] float:
+ *             as dflash2_select_sample_rows returns them, or for a path chosen
+ *             without sampling K = 1, the path itself with probability 1
+ *   n_draft   [B] int32  drafts in use of each sequence (clamped to [0, P]),
+ *             or NULL: P
+ *   temperature  >= 0, finite; 0: a draft is accepted while it is the largest
+ *             of its row (ties: lower id), and the next token is the largest;
+ *             then cand_idx, cand_prob and u may be NULL.  With
+ *             DF2_TARGET_PROBS only its being 0 matters.
+ *   u         [B, P + 1] float, clamped into [0, 1)
+ *   out_tok   [B, P + 1] int32  accepted drafts, the next token, then -1
+ *   out_len   [B] int32         tokens that count: accepted drafts + 1
+ *   out_prob  [B, P + 1] float  p of each such token (1 at temperature 0), then 0
+ *   workspace dflash2_verify_workspace(dims) bytes, 16-byte aligned
+ * Row sums are fp32 of fp32 weights; the row that a token is drawn from is
+ * summed in fp64, so that the token does not depend on how sums are rounded.
+ * -inf logits have weight 0; other non-finite values are outside the
+ * contract.  Where no token is left to draw (a row without weight, or
+ * candidates' probabilities that add to more than 1), flag bit 6 is raised and
+ * the token is 0 with probability 0.
+ */
+size_t dflash2_verify_workspace(const df2_verify_dims* dims);
+df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const int32_t* path,
+                          const int32_t* cand_idx, const float* cand_prob,
+                          const int32_t* n_draft, float temperature, const float* u,
+                          int32_t* out_tok, int32_t* out_len, float* out_prob,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Waits for `stream`, then reports and clears the device-side flags of its
  * scratch buffer and of the current device's no-allocation scratch: *flags
  * receives a bit mask (bit 0: a prev_tok outside
  * [0, V) was replaced by 0; bit 1: a cand_idx entry outside [0, V) was
  * replaced by 0; bit 2: a row merge of dflash2_select gave up waiting for
  * its gate rows (launches 1 or 2 only), which only a fault elsewhere can
- * cause, and its scores are then unreliable).  A raised flag can leave a late gate arrival
+ * cause, and its scores are then unreliable; bits 3 to 6: the paged operators
+ * and dflash2_verify, see there; theirs are kept once a device and reported
+ * on any of its streams).  A raised flag can leave a late gate arrival
  * counted in the stream's scratch, so after reporting one the next call on
  * that stream clears all its arrival counters before it launches.  Returns
  * DF2_OK, or DF2_EHIP.
