@@ -44,6 +44,7 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // Device flags of the paged operators (see dflash2_device_error).
 constexpr uint32_t kFlagPage = 8u;      // a page id outside the cache
+constexpr int kPageIds = 1024;          // page ids that a workgroup holds at a time
 constexpr uint32_t kFlagLength = 16u;   // a position outside the page table
 
 // The paged cache and the new tokens, as the kernels read them.
@@ -64,12 +65,14 @@ struct AttnArgs {
     const void* k;
     const void* v;
     void* out;
-    float* part;            // [nsplit, N * Hq, D] unnormalised outputs of a split
-    float* stat;            // [nsplit, N * Hq, 2] its maximum (log2 units) and sum
+    float* part;            // [2 * wgs, bm, D] unnormalised outputs of parts of a block
+    float* stat;            // [2 * wgs, bm, 2] their maximum (log2 units) and sum
+    int32_t* split;         // [wgs, 8] the block that a workgroup's beginning cuts first
     int64_t q_stride, out_stride;
     int G, causal, window;
-    int bm;                 // rows of a block
-    int split_keys, nsplit; // keys of a split, and the most splits (the last takes what is left)
+    int bm, kt, gk;         // rows of a block, keys of a tile, keys its start is a multiple of
+    int wgs, whole;         // workgroups of the launch; 1: each takes a whole block
+    double inv_g;           // 1 / G
     float c;                // scale * log2(e)
 };
 
@@ -91,35 +94,154 @@ __device__ __forceinline__ int seq_ctx(const PagedKv& kv, int b, int n) {
     return ctx;
 }
 
-// The sequence and the block of BM rows that block x of the launch takes: the
-// blocks of all sequences stand in a row, and a wave finds the sequence by
-// scanning the counts, 64 sequences at a time.  Later blocks of a sequence
-// see more keys and come first.
-template <int BM>
-__device__ __forceinline__ bool find_block(const PagedKv& kv, int G, int x, int& b, int& r0, int& s0,
-                                           int& n) {
-    const int lane = lane_id();
+// ----------------------------------------------------------------------------
+// How the work is cut.  The blocks of rows of all sequences stand in a row, each
+// as many tiles long as its keys make (one at least), once for every key/value
+// head; the workgroups, as many as are resident at once, take equal stretches
+// of that line.  So every workgroup streams as many keys as the next whatever
+// the lengths of the sequences, and starts once.  A block that falls to one
+// workgroup is written at once; of one that lies across a boundary, each
+// workgroup leaves its part, and k_attend_join adds them up.  A workgroup has at
+// most two such parts: where its stretch begins and where it ends.
+// With many more blocks than workgroups (long chunks) each workgroup takes one
+// whole block instead (`whole`: a block counts as one tile of the line): blocks
+// of a head then run side by side and share its keys in the L2.
+// Lengths are in device memory, so each wave finds its place itself, a lane to
+// a sequence.
+// ----------------------------------------------------------------------------
+__device__ __forceinline__ int div_g(const AttnArgs& a, int r) {
+    int t = (int)((double)r * a.inv_g);
+    t -= t * a.G > r;
+    return t + ((t + 1) * a.G <= r);
+}
+
+// Block j of a sequence: its rows' tokens and the keys that they see.
+struct BlockKeys {
+    int t_lo, t_hi, begin, end, origin, tiles;
+};
+__device__ __forceinline__ BlockKeys block_keys(const AttnArgs& a, int ctx, int n, int j) {
+    BlockKeys k;
+    k.t_lo = div_g(a, j * a.bm);
+    k.t_hi = div_g(a, min((j + 1) * a.bm, n * a.G) - 1);
+    k.end = max(a.causal ? ctx + k.t_hi + 1 : ctx + n, 0);
+    k.begin = a.window ? max(ctx + k.t_lo + 1 - a.window, 0) : 0;
+    k.origin = k.begin & ~(a.gk - 1);
+    k.tiles = max((int)((unsigned)(k.end - k.origin + a.kt - 1) / (unsigned)a.kt), 1);
+    return k;
+}
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);     // within 16 lanes: shifts by 1, 2, 4, 8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);     // lane 15 to the next 16, 47 likewise
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);     // lane 31 to the upper half
+    return x;
+}
+
+// Sequences of more blocks than this are gone through by the whole wave, a lane to
+// a block; others by their lane.
+constexpr int kLaneBlocks = 4;
+
+// A lane's sequence: its tokens, blocks and length on the line.
+struct LaneSeq {
+    int s0, n, ctx, blocks, tiles;
+};
+__device__ __forceinline__ LaneSeq lane_seq(const AttnArgs& a, int c0) {
+    LaneSeq q = {0, 0, 0, 0, 0};
+    const int lane = lane_id(), i = c0 + lane;
+    if (i < a.kv.B) {
+        seq_tokens(a.kv, i, q.s0, q.n);
+        q.ctx = seq_ctx(a.kv, i, q.n);
+        q.blocks = (int)((unsigned)(q.n * a.G + a.bm - 1) / (unsigned)a.bm);
+    }
+    if (a.whole) {
+        q.tiles = q.blocks;
+        return q;
+    }
+    if (q.blocks <= kLaneBlocks)
+        for (int j = 0; j < q.blocks; ++j) q.tiles += block_keys(a, q.ctx, q.n, j).tiles;
+    for (uint64_t big = __ballot(q.blocks > kLaneBlocks); big; big &= big - 1) {
+        const int f = __builtin_ctzll(big);
+        const int ctx = __builtin_amdgcn_readlane(q.ctx, f), n = __builtin_amdgcn_readlane(q.n, f);
+        const int blocks = __builtin_amdgcn_readlane(q.blocks, f);
+        int sum = 0;
+        for (int j = lane; j < blocks; j += 64) sum += block_keys(a, ctx, n, j).tiles;
+        sum = __builtin_amdgcn_readlane(wave_scan(sum), 63);
+        if (lane == f) q.tiles = sum;
+    }
+    return q;
+}
+
+// The stretches: `each` tiles and one more in the first `more` of them.
+struct Cut {
+    int head_tiles, wgs, each, more;
+    __device__ __forceinline__ int first(int i) const { return i * each + min(i, more); }
+    // the workgroup that has tile g
+    __device__ __forceinline__ int owner(int g) const {
+        const int longer = more * (each + 1);
+        return g < longer ? (int)((unsigned)g / (unsigned)(each + 1))
+                          : more + (int)((unsigned)(g - longer) / (unsigned)each);
+    }
+};
+__device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
+    Cut c;
+    c.head_tiles = 0;
+    for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
+        q = lane_seq(a, c0);
+        c.head_tiles += __builtin_amdgcn_readlane(wave_scan(q.tiles), 63);
+    }
+    const int all = c.head_tiles * a.kv.Hkv;
+    c.wgs = min(a.wgs, all);
+    c.each = c.wgs > 0 ? (int)((unsigned)all / (unsigned)c.wgs) : 0;
+    c.more = all - c.each * c.wgs;
+    return c;
+}
+
+// A block of rows; first: where it begins on the line of its head.
+struct Place {
+    int b, s0, n, ctx, blocks, j, first;
+    BlockKeys k;
+};
+// The block that has tile g of a head.  q: the lanes' sequences if there are no
+// more than 64.
+__device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, int g, Place& p) {
     int before = 0;
-    for (int c0 = 0; c0 < kv.B; c0 += 64) {
-        const int i = min(c0 + lane, kv.B - 1);
-        int si, ni;
-        seq_tokens(kv, i, si, ni);
-        const int nb = (c0 + lane < kv.B) ? (ni * G + BM - 1) / BM : 0;
-        int incl = nb;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int up = __shfl_up(incl, o);
-            incl += lane >= o ? up : 0;
-        }
-        const uint64_t hit = __ballot(before + incl > x);
+    for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
+        if (a.kv.B > 64) q = lane_seq(a, c0);
+        const int incl = wave_scan(q.tiles);
+        const uint64_t hit = __ballot(before + incl > g);
         if (hit) {
             const int f = __builtin_ctzll(hit);
-            b = c0 + f;
-            s0 = __builtin_amdgcn_readlane(si, f);
-            n = __builtin_amdgcn_readlane(ni, f);
-            const int nbf = __builtin_amdgcn_readlane(nb, f);
-            const int at = x - before - (__builtin_amdgcn_readlane(incl, f) - nbf);
-            r0 = (nbf - 1 - at) * BM;
+            p.b = c0 + f;
+            p.s0 = __builtin_amdgcn_readlane(q.s0, f);
+            p.n = __builtin_amdgcn_readlane(q.n, f);
+            p.ctx = __builtin_amdgcn_readlane(q.ctx, f);
+            p.blocks = __builtin_amdgcn_readlane(q.blocks, f);
+            p.first = before + __builtin_amdgcn_readlane(incl - q.tiles, f);
+            p.j = 0;
+            if (a.whole) {
+                // a later block sees more keys: it goes first
+                p.j = p.blocks - 1 - (g - p.first);
+                p.first = g;
+            } else if (p.blocks > 1) {
+                for (int j0 = 0; j0 < p.blocks; j0 += 64) {
+                    const int j = j0 + lane_id();
+                    const int own = j < p.blocks ? block_keys(a, p.ctx, p.n, j).tiles : 0;
+                    const int sum = wave_scan(own);
+                    const uint64_t here = __ballot(p.first + sum > g);
+                    if (here) {
+                        const int l = __builtin_ctzll(here);
+                        p.j = j0 + l;
+                        p.first += __builtin_amdgcn_readlane(sum - own, l);
+                        break;
+                    }
+                    p.first += __builtin_amdgcn_readlane(sum, 63);
+                }
+            }
+            p.k = block_keys(a, p.ctx, p.n, p.j);
             return true;
         }
         before += __builtin_amdgcn_readlane(incl, 63);
@@ -127,14 +249,10 @@ __device__ __forceinline__ bool find_block(const PagedKv& kv, int G, int x, int&
     return false;
 }
 
-// Splits of a block that sees `keys` keys.
-__device__ __forceinline__ int split_count(const AttnArgs& a, int keys) {
-    return min(max(1, (keys + a.split_keys - 1) / a.split_keys), a.nsplit);
-}
-
 // 16 bytes a lane from memory to LDS: lane l's go to base + 16 l, base the
 // same in the wave.  The compiler does not see the write: whoever reads it
-// waits for the vector-memory counter and meets a barrier first.
+// waits for the vector-memory counter and meets a barrier first.  (Nothing else
+// here uses m0, which the compiler reserves.)
 __device__ __forceinline__ void load_to_lds(const void* src, uint32_t lds_base) {
     asm volatile(
         "s_mov_b32 m0, %0\n\t"
@@ -142,7 +260,52 @@ __device__ __forceinline__ void load_to_lds(const void* src, uint32_t lds_base) 
         "global_load_lds_dwordx4 %1, off"
         :
         : "s"(lds_base), "v"(src)
-        : "memory", "m0");
+        : "memory");
+}
+
+// Waits until no more than the loads of min(ahead, A) stages, L each, are in
+// flight and this wave's LDS reads are done, then meets the workgroup.
+template <int A, int L>
+__device__ __forceinline__ void wait_and_meet(int ahead) {
+    if (A == 0 || ahead >= A)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(A * L) : "memory");
+    else
+        wait_and_meet<A == 0 ? 0 : A - 1, L>(ahead);
+}
+
+// G such loads, 1 KB apart in memory (but for the lanes' offsets) and in LDS, from
+// a scalar address: the instruction's offset counts for both.
+template <int G>
+__device__ __forceinline__ void load_to_lds(const void* base, const uint32_t* off, uint32_t lds_base) {
+    static_assert(G == 1 || G == 2 || G == 4, "loads in a group");
+    if constexpr (G == 1)
+        asm volatile(
+            "s_mov_b32 m0, %0\n\t"
+            "s_nop 0\n\t"
+            "global_load_lds_dwordx4 %1, %2"
+            :
+            : "s"(lds_base), "v"(off[0]), "s"(base)
+            : "memory");
+    else if constexpr (G == 2)
+        asm volatile(
+            "s_mov_b32 m0, %0\n\t"
+            "s_nop 0\n\t"
+            "global_load_lds_dwordx4 %1, %3\n\t"
+            "global_load_lds_dwordx4 %2, %3 offset:1024"
+            :
+            : "s"(lds_base), "v"(off[0]), "v"(off[1]), "s"(base)
+            : "memory");
+    else
+        asm volatile(
+            "s_mov_b32 m0, %0\n\t"
+            "s_nop 0\n\t"
+            "global_load_lds_dwordx4 %1, %5\n\t"
+            "global_load_lds_dwordx4 %2, %5 offset:1024\n\t"
+            "global_load_lds_dwordx4 %3, %5 offset:2048\n\t"
+            "global_load_lds_dwordx4 %4, %5 offset:3072"
+            :
+            : "s"(lds_base), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base)
+            : "memory");
 }
 
 // A value of the lane 32 away.
@@ -167,21 +330,34 @@ struct AttnTile {
 };
 
 // WR waves of 32 rows, WK groups of them on different keys, KS times 32 keys
-// a wave in each tile.
-template <bool BF16, int D, int WR, int WK, int KS>
+// a wave in each tile, NS stages of tiles in LDS.
+template <bool BF16, int D, int WR, int WK, int KS, int NS>
+__global__ void k_attend(AttnArgs a);
+
+template <bool BF16, int D, int WR, int WK, int KS, int NS>
 struct AttnShape {
     using Tile = AttnTile<BF16, D>;
+    static constexpr auto kernel() { return &k_attend<BF16, D, WR, WK, KS, NS>; }
     static constexpr int kWaves = WR * WK;
     static constexpr int kThreads = 64 * kWaves;
     static constexpr int BM = 32 * WR;
     static constexpr int KT = 32 * WK * KS;
     static constexpr int kTileBytes = KT * Tile::kRow;       // of K, and of V
     static constexpr int kStage = 2 * kTileBytes;
-    static constexpr int kLoads = kTileBytes / (1024 * kWaves);
+    static constexpr int kStages = NS;
+    static constexpr int kLoads = kTileBytes / (1024 * kWaves);     // of a wave for K, and for V
+    static constexpr int kRows = KT / kWaves;                       // keys that they bring
+    static constexpr int kGroup = kLoads % 4 == 0 && Tile::kRow >= 256 ? 4 : kLoads % 2 == 0 ? 2 : 1;
+    static constexpr int kGroupKeys = kGroup * (64 / Tile::kChunks);
+    // loads that may be in flight while the oldest stage is complete
+    static constexpr int kAhead = (NS - 2) * 2 * kLoads;
     static constexpr int kMergeBytes = WK > 1 ? kWaves * 32 * D * 4 + kWaves * 256 : 0;
-    static constexpr int kLds = 2 * kStage > kMergeBytes ? 2 * kStage : kMergeBytes;
+    static constexpr int kLds = NS * kStage > kMergeBytes ? NS * kStage : kMergeBytes;   // tiles, or the merge
+    static constexpr int kAllLds = kLds + 4 * kPageIds;
     static_assert(kTileBytes % (1024 * kWaves) == 0, "every wave brings whole loads");
-    static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
+    static_assert(kAhead < 64, "the counter of loads in flight");
+    static_assert(kAllLds <= 160 * 1024, "LDS of a compute unit");
+    static_assert(KT <= kPageIds / 2, "a tile's pages fit the list");
 };
 
 // Four consecutive output values of one row.
@@ -198,9 +374,9 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float (&x)[4
     }
 }
 
-template <bool BF16, int D, int WR, int WK, int KS>
-__global__ __launch_bounds__(64 * WR * WK) void k_attend(AttnArgs a) {
-    using Shape = AttnShape<BF16, D, WR, WK, KS>;
+template <bool BF16, int D, int WR, int WK, int KS, int NS>
+__global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) void k_attend(AttnArgs a) {
+    using Shape = AttnShape<BF16, D, WR, WK, KS, NS>;
     using Tile = AttnTile<BF16, D>;
     constexpr int RB = Tile::kRow, CH = Tile::kChunks, KT = Shape::KT, BM = Shape::BM;
     constexpr int NL = Shape::kLoads, DB = D / 32;
@@ -211,27 +387,62 @@ __global__ __launch_bounds__(64 * WR * WK) void k_attend(AttnArgs a) {
     const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
     const int wr = w % WR, wk = w / WR;
     const int half = lane >> 5, col = lane & 31;
-    // neighbouring workgroups take different heads: with eight of them, each
-    // XCD keeps one head's keys in its L2
-    const int lin = blockIdx.x;
-    const int h = lin % kv.Hkv, split = (lin / kv.Hkv) % a.nsplit;
-    int b, r0, s0, n;
-    if (!find_block<BM>(kv, a.G, lin / kv.Hkv / a.nsplit, b, r0, s0, n)) return;
-    const int M = n * a.G;
-    const int ctx = seq_ctx(kv, b, n);
-
-    // The keys that some row of the block sees, and this split's share of them.
-    const int t_lo = r0 / a.G, t_hi = (min(r0 + BM, M) - 1) / a.G;
-    const int end = max(a.causal ? ctx + t_hi + 1 : ctx + n, 0);
-    const int begin = a.window ? max(ctx + t_lo + 1 - a.window, 0) : 0;
-    const int nsplit = split_count(a, end - begin);
-    if (split >= nsplit) return;
-    const int klo = begin + split * a.split_keys;
-    const int khi = split == nsplit - 1 ? end : klo + a.split_keys;
+    // A stretch of the line.  Workgroups go to the eight XCDs in turn; those of one
+    // XCD take neighbouring stretches.  Whole blocks: neighbouring workgroups take
+    // different heads, so that with eight of them an XCD keeps one head's keys.
+    LaneSeq seqs;
+    const Cut cut = cut_work(a, seqs);
+    int wg = blockIdx.x;
+    if (!a.whole && cut.wgs % 8 == 0 && cut.wgs == (int)gridDim.x)
+        wg = (int)(blockIdx.x % 8) * (cut.wgs / 8) + (int)(blockIdx.x / 8);
+    int32_t* split = a.split + 8 * wg;
+    if (wg >= cut.wgs) {
+        if (!a.whole && threadIdx.x == 0) split[0] = -1;
+        return;
+    }
+    int g = cut.first(wg), h = 0;
+    const int start = g, stop = cut.first(wg + 1);
+    Place at;
+    at.j = at.blocks = 0;
+    while (g < stop) {
+    if (a.whole) {
+        h = g % kv.Hkv;
+        if (!find_place(a, seqs, g / kv.Hkv, at)) return;
+        at.first = g - h * cut.head_tiles;      // the block is the whole stretch
+    } else if (at.j + 1 < at.blocks) {
+        at.first += at.k.tiles;         // the next block of the sequence
+        ++at.j;
+        at.k = block_keys(a, at.ctx, at.n, at.j);
+    } else {
+        h = (int)((unsigned)g / (unsigned)cut.head_tiles);
+        if (!find_place(a, seqs, g - h * cut.head_tiles, at)) return;
+    }
+    // the same in every lane; said so, they live in scalar registers
+    const auto uni = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    const int b = uni(at.b), s0 = uni(at.s0), n = uni(at.n), ctx = uni(at.ctx), r0 = uni(at.j) * BM;
+    const int M = n * a.G, head_kv = uni(h), tiles = uni(at.k.tiles);
+    const int first = uni(h * cut.head_tiles + at.first);
+    const int tile0 = a.whole ? 0 : uni(g) - first;
+    const int tile1 = a.whole ? tiles : min(tiles, stop - first);
+    const bool whole = tile0 == 0 && tile1 == tiles;
+    if (!a.whole && g == start && threadIdx.x == 0) {
+        // the first boundary inside a block tells the join about the block
+        const bool cuts = tile0 > 0 && cut.first(wg - 1) <= first;
+        split[0] = cuts ? cut.owner(first + tiles - 1) : -1;
+        split[1] = head_kv;
+        split[2] = s0;
+        split[3] = r0;
+        split[4] = M;
+    }
+    g += a.whole ? 1 : tile1 - tile0;
+    const int t_lo = uni(at.k.t_lo), t_hi = uni(at.k.t_hi);
+    const int origin = uni(at.k.origin);
+    const int klo = max(uni(at.k.begin), origin + tile0 * KT);
+    const int khi = min(uni(at.k.end), origin + tile1 * KT);
 
     // This lane's row: row col of the wave's 32 (the last row again past the end).
     const int r = r0 + wr * 32 + col;
-    const int rc = min(r, M - 1), t = rc / a.G, head = h * a.G + rc % a.G;
+    const int rc = min(r, M - 1), t = div_g(a, rc), head = head_kv * a.G + rc - t * a.G;
     const int lim = a.causal ? ctx + t + 1 : khi;                 // first key it does not see
     const int low = a.window ? ctx + t + 1 - a.window : 0;        // first key it sees
 
@@ -253,50 +464,93 @@ __global__ __launch_bounds__(64 * WR * WK) void k_attend(AttnArgs a) {
     float m = -INFINITY, l = 0.f;       // l: this lane's half of the row's sum
 
     // Loads of a tile: load i of wave w covers 1 KB of the K tile and the same
-    // of the V tile.
-    const int row0 = (w * NL * 64 + lane) / CH;
-    const int chunk = lane % CH;
-    const int64_t head_off = (int64_t)h << kv.page_shift;
+    // of the V tile, RI keys.  Page ids wait in LDS, kPageIds at a time: read
+    // from memory tile by tile, each would have to wait for the loads in flight.
+    // Loads go in groups of GL, one page each: tiles start at multiples of the
+    // group's keys, so in a whole tile (and pages no smaller than a group) a
+    // group's address is one scalar, and the lanes' offsets are the same in every
+    // tile.  Other tiles (the ends of the stretch, whose keys outside it are
+    // replaced by its first or last; small pages) make each lane's address.
+    constexpr int RW = Shape::kRows, RI = 64 / CH;      // keys of a wave, of a load
+    constexpr int GL = Shape::kGroup, GK = GL * RI;     // loads and keys of a group
+    int32_t* ids = reinterpret_cast<int32_t*>(lds + Shape::kLds);
+    const int64_t head_off = (int64_t)head_kv << kv.page_shift;
     const int32_t* table = kv.table + (int64_t)b * kv.table_stride;
-    auto page_ids = [&](int k0, int (&id)[NL]) {
+    const int page_mask = (1 << kv.page_shift) - 1;
+    const bool one_page = page_mask >= GK - 1;
+    uint32_t at_k[NL], at_v[NL];        // within RI keys, chunks permuted by row
 #pragma unroll
-        for (int i = 0; i < NL; ++i) id[i] = table[min(k0 + row0 + i * (64 / CH), khi - 1) >> kv.page_shift];
-    };
-    uint32_t bad = 0;
-    auto load_tile = [&](int k0, int stage, const int (&id)[NL]) {
+    for (int i = 0; i < NL; ++i) {
+        const int row = w * RW + i * RI + lane / CH;
+        at_k[i] = (lane / CH) * RB + ((lane % CH) ^ Tile::swz_k(row)) * 16;
+        at_v[i] = (lane / CH) * RB + ((lane % CH) ^ Tile::swz_v(row)) * 16;
+    }
+    auto load_tile = [&](int k0, int stage, int page0) {
+        const uint32_t to = lds0 + stage * Shape::kStage + w * NL * 1024;
+        // all ids first: the loads are not reordered with LDS reads, which would
+        // then wait one by one
+        int id[NL];
+        if (one_page && k0 >= klo && k0 + KT <= khi) {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int row = row0 + i * (64 / CH);
-            const int key = min(k0 + row, khi - 1);
-            const bool ok = (unsigned)id[i] < (unsigned)kv.num_pages;
-            bad |= ok ? 0u : 1u;
-            const int64_t off = ((int64_t)(ok ? id[i] : 0) * kv.page_stride +
-                                 (head_off + (key & ((1 << kv.page_shift) - 1))) * D) * Tile::kEsz;
-            const uint32_t at = lds0 + stage * Shape::kStage + (w * NL + i) * 1024;
-            load_to_lds(reinterpret_cast<const char*>(a.k) + off + (chunk ^ Tile::swz_k(row)) * 16, at);
-            load_to_lds(reinterpret_cast<const char*>(a.v) + off + (chunk ^ Tile::swz_v(row)) * 16,
-                        at + Shape::kTileBytes);
+            for (int i = 0; i < NL; i += GL) id[i] = ids[((k0 + w * RW + i * RI) >> kv.page_shift) - page0];
+#pragma unroll
+            for (int i = 0; i < NL; i += GL) {
+                const int key = k0 + w * RW + i * RI;
+                const int64_t off = ((int64_t)__builtin_amdgcn_readfirstlane(id[i]) * kv.page_stride +
+                                     (head_off + (key & page_mask)) * D) * Tile::kEsz;
+                load_to_lds<GL>(reinterpret_cast<const char*>(a.k) + off, at_k + i, to + i * 1024);
+                load_to_lds<GL>(reinterpret_cast<const char*>(a.v) + off, at_v + i, to + i * 1024 + Shape::kTileBytes);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                id[i] = ids[(min(max(k0 + w * RW + i * RI + lane / CH, klo), khi - 1) >> kv.page_shift) - page0];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int key = min(max(k0 + w * RW + i * RI + lane / CH, klo), khi - 1);
+                const int64_t off = ((int64_t)id[i] * kv.page_stride + (head_off + (key & page_mask)) * D) * Tile::kEsz;
+                load_to_lds(reinterpret_cast<const char*>(a.k) + off + at_k[i] % RB, to + i * 1024);
+                load_to_lds(reinterpret_cast<const char*>(a.v) + off + at_v[i] % RB, to + i * 1024 + Shape::kTileBytes);
+            }
         }
     };
 
-    const int ntile = max((khi - klo + KT - 1) / KT, 0);
-    if (ntile > 0) {
-        int ids[NL];
-        page_ids(klo, ids);
-        load_tile(klo, 0, ids);
-        page_ids(klo + KT, ids);
-        for (int it = 0; it < ntile; ++it) {
-            const int k0 = klo + it * KT;
-            const int stage = it & 1;
-            drain_stores();             // vmcnt(0): this wave's part of the tile is in LDS
-            __syncthreads();            // everyone's is, and nobody reads the other stage any more
-            if (it + 1 < ntile) {
-                load_tile(k0 + KT, stage ^ 1, ids);
-                page_ids(k0 + 2 * KT, ids);
+    for (int k_win = origin + tile0 * KT; k_win < khi;) {
+        // the tiles whose pages fit the list, and their pages
+        const int page0 = max(k_win, klo) >> kv.page_shift;
+        const int64_t reach = ((int64_t)(page0 + kPageIds) << kv.page_shift) - k_win;
+        const int ntile = (int)min(reach / KT, (int64_t)((khi - k_win + KT - 1) / KT));
+        const int last_page = min(khi - 1, k_win + ntile * KT - 1) >> kv.page_shift;
+        __syncthreads();
+        for (int i = threadIdx.x; i <= last_page - page0; i += Shape::kThreads) {
+            int id = table[page0 + i];
+            if ((unsigned)id >= (unsigned)kv.num_pages) {
+                atomicOr(kv.err, kFlagPage);
+                id = 0;
             }
-            const int kw = k0 + wk * KS * 32;          // this wave's first key
+            ids[i] = id;
+        }
+        __syncthreads();
+        // The query rows have arrived before the first tile's loads go out: a wait
+        // for them inside the loop would be one for all loads in flight.
+#pragma unroll
+        for (int q = 0; q < QN; ++q) asm volatile("" : "+v"(qf[q]));
+        // A ring of NS stages, NS - 1 of them in flight or waiting.
+#pragma unroll
+        for (int i = 0; i < NS - 1; ++i)
+            if (i < ntile) load_tile(k_win + i * KT, i, page0);
+        int stage = 0;
+        for (int it = 0; it < ntile; ++it) {
+            const int k0 = k_win + it * KT;
+            // this wave's part of the oldest stage is in LDS; then everyone's is,
+            // and nobody reads the stage before it any more
+            wait_and_meet<NS - 2, 2 * NL>(ntile - 1 - it);
+            if (it + NS - 1 < ntile)
+                load_tile(k0 + (NS - 1) * KT, stage == 0 ? NS - 1 : stage - 1, page0);
             const unsigned char* kt = lds + stage * Shape::kStage;
             const unsigned char* vt = kt + Shape::kTileBytes;
+            stage = stage == NS - 1 ? 0 : stage + 1;
+            const int kw = k0 + wk * KS * 32;          // this wave's first key
 
             f32x16_t s[KS];
 #pragma unroll
@@ -325,14 +579,14 @@ __global__ __launch_bounds__(64 * WR * WK) void k_attend(AttnArgs a) {
             // whole need none).
             const int first_lim = a.causal ? ctx + t_lo + 1 : khi;
             const int last_low = a.window ? ctx + t_hi + 1 - a.window : 0;
-            if (k0 + KT > min(first_lim, khi) || k0 < last_low) {
-                const int top = min(lim, khi);
+            if (k0 + KT > min(first_lim, khi) || k0 < max(last_low, klo)) {
+                const int top = min(lim, khi), bottom = max(low, klo);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int v = 0; v < 16; ++v) {
                         const int key = kw + ks * 32 + 8 * (v / 4) + 4 * half + v % 4;
-                        s[ks][v] = (key < top && key >= low) ? s[ks][v] : -INFINITY;
+                        s[ks][v] = (key < top && key >= bottom) ? s[ks][v] : -INFINITY;
                     }
             }
             float mx = s[0][0];
@@ -404,7 +658,7 @@ __global__ __launch_bounds__(64 * WR * WK) void k_attend(AttnArgs a) {
                 }
             }
         }
-        if (bad) atomicOr(kv.err, kFlagPage);
+        k_win += ntile * KT;
     }
     l += other_half(l);
 
@@ -437,7 +691,7 @@ __global__ __launch_bounds__(64 * WR * WK) void k_attend(AttnArgs a) {
                         (f32x4_t){o[d][4 * v] * f, o[d][4 * v + 1] * f, o[d][4 * v + 2] * f, o[d][4 * v + 3] * f};
         }
         __syncthreads();
-        if (wk > 0) return;
+        if (wk > 0) continue;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -455,22 +709,21 @@ __global__ __launch_bounds__(64 * WR * WK) void k_attend(AttnArgs a) {
         m = mg;
         l = lg;
     }
-    if (r >= M) return;
-    const int64_t grow = (int64_t)(s0 + t) * kv.Hq + head;
-    if (nsplit == 1) {
+    if (r >= M) continue;
+    if (whole) {
         // a row that sees nothing gives zeros
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        const int64_t at = (int64_t)(s0 + t) * a.out_stride + (int64_t)head * D;
+        const int64_t to = (int64_t)(s0 + t) * a.out_stride + (int64_t)head * D;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 const float y[4] = {o[d][4 * v] * inv, o[d][4 * v + 1] * inv, o[d][4 * v + 2] * inv,
                                     o[d][4 * v + 3] * inv};
-                store4<BF16>(a.out, at + 32 * d + 8 * v + 4 * half, y);
+                store4<BF16>(a.out, to + 32 * d + 8 * v + 4 * half, y);
             }
     } else {
-        const int64_t prow = (int64_t)split * kv.N * kv.Hq + grow;
+        const int64_t prow = (int64_t)(2 * wg + (tile0 == 0 ? 1 : 0)) * BM + wr * 32 + col;
         if (half == 0) {
             a.stat[2 * prow] = m;
             a.stat[2 * prow + 1] = l;
@@ -483,55 +736,90 @@ __global__ __launch_bounds__(64 * WR * WK) void k_attend(AttnArgs a) {
                 store4<false>(a.part, prow * D + 32 * d + 8 * v + 4 * half, y);
             }
     }
+    }
 }
 
-// Joins the splits of each row: sum_s 2^(m_s - m) (o_s, l_s).  A group of D / 4
-// lanes takes a row; rows of sequences whose keys made one split are done
-// already.
+// Joins the parts of the blocks that lie across workgroups:
+//     sum_s 2^(m_s - m) (o_s, l_s)
+// over the parts s of a row.  Four workgroups for each boundary of stretches, of
+// which the first inside a block does the block; D / 4 lanes take a row, or
+// with many parts all of the workgroup, part by part, and meet in LDS.
 template <bool BF16, int D>
 __global__ __launch_bounds__(256) void k_attend_join(AttnArgs a) {
-    constexpr int L = D / 4;
-    const PagedKv& kv = a.kv;
-    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
-    const int d = (threadIdx.x % L) * 4;
-    if (row >= (int64_t)kv.N * kv.Hq) return;
-    const int tok = (int)(row / kv.Hq), head = (int)(row % kv.Hq);
-    // the token's sequence: the last one that starts at or before it
-    int lo = 0, hi = kv.B;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (kv.start[mid + 1] > tok) hi = mid;
-        else lo = mid + 1;
-    }
-    if (lo >= kv.B || tok < kv.start[lo] || tok < 0) return;
-    int s0, n;
-    seq_tokens(kv, lo, s0, n);
-    const int ctx = seq_ctx(kv, lo, n);
-    // the block's keys, as k_attend saw them
-    const int M = n * a.G, r0 = ((tok - s0) * a.G + head % a.G) / a.bm * a.bm;
-    const int t_lo = r0 / a.G, t_hi = (min(r0 + a.bm, M) - 1) / a.G;
-    const int end = max(a.causal ? ctx + t_hi + 1 : ctx + n, 0);
-    const int begin = a.window ? max(ctx + t_lo + 1 - a.window, 0) : 0;
-    const int nsplit = split_count(a, end - begin);
-    if (nsplit == 1) return;
-    const int64_t rows = (int64_t)kv.N * kv.Hq;
-    float m = -INFINITY;
-    for (int s = 0; s < nsplit; ++s) m = fmaxf(m, a.stat[2 * (s * rows + row)]);
-    float l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < nsplit; ++s) {
-        const int64_t at = s * rows + row;
-        const float ms = a.stat[2 * at];
-        if (ms == -INFINITY) continue;          // a split of which the row sees nothing
-        const float f = __builtin_amdgcn_exp2f(ms - m);
-        l += f * a.stat[2 * at + 1];
-        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(a.part + at * D + d);
+    constexpr int L = D / 4, NG = 256 / L;
+    constexpr int kMany = 16;           // parts from which the workgroup takes a row at a time
+    __shared__ f32x4_t lds_y[256];
+    __shared__ float lds_m[NG], lds_l[NG];
+    const int quarter = blockIdx.x % 4, boundary = 1 + blockIdx.x / 4;
+    const int32_t* split = a.split + 8 * boundary;
+    const int w0 = boundary - 1, w1 = split[0], h = split[1], s0 = split[2], r0 = split[3], M = split[4];
+    if (w1 < 0) return;
+    const int group = threadIdx.x / L, d = (threadIdx.x % L) * 4;
+    const bool many = w1 - w0 >= kMany;
+    const int rows = a.bm / 4;
+    const int step = many ? 1 : NG, first_part = many ? group : 0, part_step = many ? NG : 1;
+    for (int i0 = quarter * rows; i0 < (quarter + 1) * rows && r0 + i0 < M; i0 += step) {
+        const int i = i0 + (many ? 0 : group), r = r0 + i;
+        const bool live = i < (quarter + 1) * rows && r < M;
+        float m = -INFINITY, l = 0.f;
+        f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+        if (live) {
+            for (int w = w0 + first_part; w <= w1; w += 4 * part_step) {
+                float pm[4], pl[4];
+                f32x4_t py[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] += f * x[e];
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+                for (int x = 0; x < 4; ++x) {
+                    const int p = min(w + x * part_step, w1);
+                    const int64_t row = (int64_t)(2 * p + (p == w0 ? 1 : 0)) * a.bm + i;
+                    pm[x] = w + x * part_step <= w1 ? a.stat[2 * row] : -INFINITY;
+                    pl[x] = a.stat[2 * row + 1];
+                    py[x] = *reinterpret_cast<const f32x4_t*>(a.part + row * D + d);
+                }
+                float mn = m;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] *= inv;
-    store4<BF16>(a.out, (int64_t)tok * a.out_stride + (int64_t)head * D + d, y);
+                for (int x = 0; x < 4; ++x) mn = fmaxf(mn, pm[x]);
+                if (mn == -INFINITY) continue;      // parts of which the row sees nothing
+                const float f = __builtin_amdgcn_exp2f(m - mn);
+                m = mn;
+                l *= f;
+                y *= f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (pm[x] == -INFINITY) continue;
+                    const float e = __builtin_amdgcn_exp2f(pm[x] - mn);
+                    l += e * pl[x];
+                    y += e * py[x];
+                }
+            }
+        }
+        if (many) {
+            __syncthreads();
+            lds_y[threadIdx.x] = y;
+            if (threadIdx.x % L == 0) {
+                lds_m[group] = m;
+                lds_l[group] = l;
+            }
+            __syncthreads();
+            if (group > 0) continue;
+            float mn = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < NG; ++x) mn = fmaxf(mn, lds_m[x]);
+            l = 0.f;
+            y = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < NG; ++x) {
+                if (lds_m[x] == -INFINITY) continue;
+                const float e = __builtin_amdgcn_exp2f(lds_m[x] - mn);
+                l += e * lds_l[x];
+                y += e * lds_y[x * L + threadIdx.x];
+            }
+        }
+        if (!live) continue;
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const int t = div_g(a, r), head = h * a.G + r - t * a.G;
+        const float out[4] = {y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv};
+        store4<BF16>(a.out, (int64_t)(s0 + t) * a.out_stride + (int64_t)head * D + d, out);
+    }
 }
 
 }  // namespace df2

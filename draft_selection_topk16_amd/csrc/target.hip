@@ -98,11 +98,10 @@ df2_status check_rows(const df2_paged_kv* kv, const void* p, int64_t stride, int
 // ----------------------------------------------------------------------------
 struct AttnPlan {
     int wr = 1;                 // waves of 32 rows in a block
-    int bm = 32, kt = 32;       // rows of a block, keys of a tile
-    int per_cu = 1;             // resident workgroups of a compute unit
-    int64_t blocks = 0;         // most blocks of rows
-    int split_keys = 0, nsplit = 1;
-    size_t bytes = 0;           // workspace
+    int bm = 32, kt = 32, gk = 16;
+    int wgs = 1, whole = 0;
+    bool fits = true;           // 32-bit tile numbers
+    size_t part = 0, bytes = 0; // workspace: the parts' outputs, all of it
 };
 
 // The kernels there are: rows (WR waves of 32), key groups, 32-key steps.
@@ -110,25 +109,25 @@ template <bool BF16, int D, typename F>
 auto with_shape(int wr, F&& f) {
     constexpr int RB = AttnTile<BF16, D>::kRow;
     if constexpr (RB == 128) {
-        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 2>());
-        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2>());
-        return f(AttnShape<BF16, D, 8, 1, 2>());
+        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 2, 2>());
+        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2>());
+        return f(AttnShape<BF16, D, 8, 1, 2, 2>());
     } else if constexpr (RB == 256 && BF16) {
-        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1>());
-        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2>());
-        return f(AttnShape<BF16, D, 8, 1, 2>());
+        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2>());
+        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2>());
+        return f(AttnShape<BF16, D, 8, 1, 2, 2>());
     } else if constexpr (RB == 256) {
-        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1>());
-        return f(AttnShape<BF16, D, 4, 1, 1>());
+        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2>());
+        return f(AttnShape<BF16, D, 4, 1, 1, 2>());
     } else if constexpr (RB == 512) {
-        if (wr == 1) return f(AttnShape<BF16, D, 1, 2, 1>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1>());
-        return f(AttnShape<BF16, D, 4, 1, 1>());
+        if (wr == 1) return f(AttnShape<BF16, D, 1, 2, 1, 2>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2>());
+        return f(AttnShape<BF16, D, 4, 1, 1, 2>());
     } else {
-        return f(AttnShape<BF16, D, 4, 1, 1>());
+        return f(AttnShape<BF16, D, 4, 1, 1, 2>());
     }
 }
 
@@ -145,32 +144,37 @@ auto with_type(const df2_paged_kv* kv, F&& f) {
     return f(integral_constant<bool, false>(), integral_constant<int, 256>());
 }
 
-// Blocks of as many rows as a sequence has on average; keys split until there
-// are about three workgroups for every place on the device, which evens out
-// sequences of different lengths.
+// Blocks of as many rows as a sequence has on average, and as many workgroups as
+// are resident at once (fewer where max_len says that there are fewer tiles).
 AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
     AttnPlan pl;
     const int64_t rows = (int64_t)kv->N * (kv->Hq / kv->Hkv);
-    const int64_t each = (rows + kv->B - 1) / kv->B;
+    const int64_t seqs = std::min(kv->B, kv->N);
+    const int64_t each = (rows + seqs - 1) / seqs;
     pl.wr = each <= 32 ? 1 : each <= 64 ? 2 : each <= 128 ? 4 : 8;
+    int per_cu = 1;
     with_type(kv, [&](auto bf16, auto d) {
         return with_shape<decltype(bf16)::value, decltype(d)::value>(pl.wr, [&](auto shape) {
             using S = decltype(shape);
             pl.bm = S::BM;
             pl.kt = S::KT;
-            pl.per_cu = std::max(1, std::min(160 * 1024 / S::kLds, 8 / S::kWaves));
+            pl.gk = S::kGroupKeys;
+            per_cu = std::max(1, std::min(160 * 1024 / S::kAllLds, 8 / S::kWaves));
             return 0;
         });
     });
-    pl.blocks = rows / pl.bm + std::min(kv->B, kv->N);      // one more in each sequence that has tokens
-    const int64_t likely = std::max<int64_t>((rows + pl.bm - 1) / pl.bm, std::min(kv->B, kv->N));
-    const int64_t units = likely * kv->Hkv;
-    const int64_t want = std::max<int64_t>(1, 3 * (int64_t)compute_units() * pl.per_cu / units);
-    const int64_t keys = (max_len + want - 1) / want;
-    const int64_t least = 2 * pl.kt;
-    pl.split_keys = (int)std::max<int64_t>(least, (keys + pl.kt - 1) / pl.kt * pl.kt);
-    pl.nsplit = (int)std::max<int64_t>(1, (max_len + pl.split_keys - 1) / pl.split_keys);
-    if (pl.nsplit > 1) pl.bytes = (size_t)pl.nsplit * kv->N * kv->Hq * (kv->D + 2) * sizeof(float);
+    const int64_t blocks = rows / pl.bm + seqs;     // one more in each sequence that has tokens
+    const int64_t resident = (int64_t)compute_units() * per_cu;
+    const auto tiles = [&](int64_t len) { return (len + pl.gk + pl.kt - 1) / pl.kt; };
+    pl.fits = blocks * kv->Hkv * tiles((int64_t)kv->table_width * kv->page_size) < (1LL << 31);
+    pl.whole = pl.wr == 8 && rows / pl.bm * kv->Hkv >= 2 * resident;
+    if (pl.whole) {
+        pl.wgs = (int)std::min<int64_t>(blocks * kv->Hkv, 0x7FFFFFFF);
+        return pl;
+    }
+    pl.wgs = (int)std::min(resident, blocks * kv->Hkv * tiles(max_len));
+    pl.part = (size_t)2 * pl.wgs * pl.bm * kv->D;
+    pl.bytes = pl.wgs > 1 ? (pl.part + (size_t)(4 * pl.bm + 8) * pl.wgs) * sizeof(float) : 0;
     return pl;
 }
 
@@ -184,12 +188,10 @@ df2_status plan_length(const df2_paged_kv* kv, int32_t max_len, int* out) {
 
 template <bool BF16, int D>
 df2_status launch_attend(const AttnPlan& pl, const AttnArgs& a, hipStream_t stream) {
-    const int64_t grid = pl.blocks * a.kv.Hkv * pl.nsplit;
-    if (grid > 0x7FFFFFFF) return fail_with(DF2_EUNSUPPORTED, "problem too large");
     const df2_status st = with_shape<BF16, D>(pl.wr, [&](auto shape) {
         using S = decltype(shape);
-        constexpr auto* fn = &k_attend<BF16, D, S::BM / 32, S::kWaves / (S::BM / 32), S::KT / 32 / (S::kWaves / (S::BM / 32))>;
-        if (S::kLds > 65536) {
+        constexpr auto fn = S::kernel();
+        if (S::kAllLds > 65536) {
             static std::mutex mu;
             static std::map<int, hipError_t> done;      // per device
             int dev = 0;
@@ -198,15 +200,14 @@ df2_status launch_attend(const AttnPlan& pl, const AttnArgs& a, hipStream_t stre
             auto it = done.find(dev);
             if (it == done.end())
                 it = done.emplace(dev, hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                                           hipFuncAttributeMaxDynamicSharedMemorySize, S::kLds)).first;
+                                                           hipFuncAttributeMaxDynamicSharedMemorySize, S::kAllLds)).first;
             if (it->second != hipSuccess) return hip_failed(it->second, "hipFuncSetAttribute (attention)");
         }
-        hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, stream, a);
+        hipLaunchKernelGGL(fn, dim3((unsigned)pl.wgs), dim3(S::kThreads), S::kAllLds, stream, a);
         return launched("dflash2_paged_attention launch");
     });
-    if (st != DF2_OK || pl.nsplit == 1) return st;
-    const int64_t rows = (int64_t)a.kv.N * a.kv.Hq, per = 256 / (D / 4);
-    hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, stream, a);
+    if (st != DF2_OK || pl.wgs == 1 || pl.whole) return st;
+    hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)(4 * (pl.wgs - 1))), dim3(256), 0, stream, a);
     return launched("dflash2_paged_attention join launch");
 }
 
@@ -240,6 +241,7 @@ df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_
     if ((st = check_rows(kv, q, q_stride, kv->Hq, "q")) != DF2_OK) return st;
     if ((st = check_rows(kv, out, out_stride, kv->Hq, "out")) != DF2_OK) return st;
     const AttnPlan pl = plan_attend(kv, len);
+    if (!pl.fits) return fail_with(DF2_EUNSUPPORTED, "too many tiles (N, Hkv and the page table's width)");
     if (pl.bytes > 0) {
         if (!workspace || workspace_bytes < pl.bytes)
             return fail_with(DF2_EINVAL, "workspace of " + std::to_string(workspace ? workspace_bytes : 0) +
@@ -252,15 +254,19 @@ df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_
     a.v = kv->v_cache;
     a.out = out;
     a.part = reinterpret_cast<float*>(workspace);
-    a.stat = a.part + (size_t)pl.nsplit * kv->N * kv->Hq * kv->D;
+    a.stat = a.part + pl.part;
+    a.split = reinterpret_cast<int32_t*>(a.stat + (size_t)4 * pl.wgs * pl.bm);
     a.q_stride = q_stride;
     a.out_stride = out_stride;
     a.G = kv->Hq / kv->Hkv;
     a.causal = causal ? 1 : 0;
     a.window = window;
     a.bm = pl.bm;
-    a.split_keys = pl.split_keys;
-    a.nsplit = pl.nsplit;
+    a.kt = pl.kt;
+    a.gk = pl.gk;
+    a.wgs = pl.wgs;
+    a.whole = pl.whole;
+    a.inv_g = 1.0 / a.G;
     a.c = (float)((double)scale * 1.4426950408889634);
     return with_type(kv, [&](auto bf16, auto d) {
         return launch_attend<decltype(bf16)::value, decltype(d)::value>(pl, a, stream);

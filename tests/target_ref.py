@@ -62,30 +62,34 @@ def attention_ref(c, scale, causal=True, window=0):
         j = torch.arange(L)
         k = kc[table[b, j // page], :, j % page].double()       # [L, Hkv, D]
         v = vc[table[b, j // page], :, j % page].double()
-        for t in range(n):
-            pos = cb + t
-            see = j <= pos if causal else torch.ones_like(j, dtype=torch.bool)
-            if window:
-                see = see & (j > pos - window)
-            if pos < 0:
-                see = torch.zeros_like(see)
-            for head in range(Hq):
-                r = start[b] + t
-                if not bool(see.any()):
-                    out[r, head] = 0.0
-                    continue
-                kk, vv, x = k[see, head // G], v[see, head // G], q[r, head]
-                s = kk @ x * scale
-                p = torch.exp(s - s.max())
-                o = p @ vv / p.sum()
-                A = p @ vv.abs() / p.sum()
-                smax = float((kk.abs() @ x.abs()).max()) * scale
-                amax = float((s.max() - s).max()) + float(s.abs().max())
-                d = 2 * (D + 2) * U * smax + 2 * U * amax + 4 * U + len(s) * U
-                if dtype == torch.bfloat16:
-                    d += h
-                out[r, head] = o
-                bound[r, head] = (d * A + h * o.abs()) * (1 + 2 * h)
+        if n == 0:
+            continue
+        rows = slice(start[b], start[b] + n)
+        pos = cb + torch.arange(n)[:, None]
+        see = (j <= pos) if causal else (j < L).expand(n, L)
+        if window:
+            see = see & (j > pos - window)
+        see = see & (pos >= 0)
+        some = see.any(-1)
+        if L == 0 or not bool(some.any()):
+            out[rows] = 0.0
+            continue
+        for head in range(Hq):
+            kk, vv, x = k[:, head // G], v[:, head // G], q[rows, head]
+            kk, vv = torch.nan_to_num(kk), torch.nan_to_num(vv)
+            s = torch.where(see, x @ kk.T * scale, -float("inf"))
+            top = torch.where(some, s.amax(-1), 0.0)[:, None]
+            p = torch.exp(s - top)
+            total = p.sum(-1, keepdim=True).clamp(min=1e-300)
+            o, A = p @ vv / total, p @ vv.abs() / total
+            smax = torch.where(see, x.abs() @ kk.abs().T * scale, 0.0).amax(-1, keepdim=True)
+            low = torch.where(see, s, float("inf")).amin(-1, keepdim=True)
+            amax = torch.where(some[:, None], top - low, 0.0) + torch.where(see, s.abs(), 0.0).amax(-1, keepdim=True)
+            d = 2 * (D + 2) * U * smax + 2 * U * amax + 4 * U + see.sum(-1, keepdim=True) * U
+            if dtype == torch.bfloat16:
+                d = d + h
+            out[rows, head] = o
+            bound[rows, head] = (d * A + h * o.abs()) * (1 + 2 * h)
     return out, bound
 
 

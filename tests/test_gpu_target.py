@@ -51,6 +51,8 @@ ATTENTION = [
     ("block8_g8", BF, 128, 16, 2, 16, [8, 8], [63, 640], True, 0),
     ("block16_g7", BF, 64, 7, 1, 64, [16, 9], [33, 95], True, 0),
     ("chunk", BF, 128, 4, 1, 16, [150, 0, 97], [201, 9, 0], True, 0),
+    ("chunk_many_blocks", BF, 128, 32, 8, 16, [3000, 1111, 2], [40, 300, 7], True, 0),
+    ("chunk_many_blocks_window", BF, 64, 32, 8, 16, [4100, 300], [0, 900], True, 500),
     ("chunk_64", BF, 64, 2, 1, 32, [333], [100], True, 0),
     ("chunk_256", BF, 256, 2, 1, 16, [70, 3], [45, 31], True, 0),
     ("decode_256", BF, 256, 8, 2, 64, [1, 2], [200, 77], True, 0),

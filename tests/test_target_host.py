@@ -74,7 +74,9 @@ def test_attention_workspace(lib):
     long = kv(table_width=4096, table_stride=4096)
     need = lib.dflash2_paged_attention_workspace(ctypes.byref(long), 0)
     assert need > 0 and need % 4 == 0
-    assert lib.dflash2_paged_attention_workspace(ctypes.byref(kv()), 16) == 0
+    one = kv(B=1, N=1, Hq=1, Hkv=1, page_stride=16 * 128)
+    assert lib.dflash2_paged_attention_workspace(ctypes.byref(one), 1) < need
+    assert lib.dflash2_paged_attention_workspace(ctypes.byref(kv(N=0)), 16) == 0
     assert lib.dflash2_paged_attention_workspace(ctypes.byref(kv(D=77)), 0) == 0
     assert lib.dflash2_paged_attention_workspace(None, 0) == 0
     assert attend(lib, long, max_len=0, ws=None, n=need) == EINVAL
