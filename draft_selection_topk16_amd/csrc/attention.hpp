@@ -252,16 +252,23 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, int g, 
 // 16 bytes a lane from memory to LDS: lane l's go to base + 16 l, base the
 // same in the wave.  The compiler does not see the write: whoever reads it
 // waits for the vector-memory counter and meets a barrier first.  (Nothing else
-// here uses m0, which the compiler reserves.)
+// here uses m0, which the compiler reserves.)  ONCE: bytes that nobody reads
+// again (non-temporal): contexts of 131 thousand tokens, 282 us without and 252 us
+// with it.
+#define DF2_TO_LDS(NT)                             \
+    asm volatile(                                  \
+        "s_mov_b32 m0, %0\n\t"                     \
+        "s_nop 0\n\t"                              \
+        "global_load_lds_dwordx4 %1, off" NT       \
+        :                                          \
+        : "s"(lds_base), "v"(src)                  \
+        : "memory")
+template <bool ONCE>
 __device__ __forceinline__ void load_to_lds(const void* src, uint32_t lds_base) {
-    asm volatile(
-        "s_mov_b32 m0, %0\n\t"
-        "s_nop 0\n\t"
-        "global_load_lds_dwordx4 %1, off"
-        :
-        : "s"(lds_base), "v"(src)
-        : "memory");
+    if constexpr (ONCE) DF2_TO_LDS(" nt");
+    else DF2_TO_LDS("");
 }
+#undef DF2_TO_LDS
 
 // Waits until no more than the loads of min(ahead, A) stages, L each, are in
 // flight and this wave's LDS reads are done, then meets the workgroup.
@@ -273,40 +280,82 @@ __device__ __forceinline__ void wait_and_meet(int ahead) {
         wait_and_meet<A == 0 ? 0 : A - 1, L>(ahead);
 }
 
+// N products of which each takes one operand from LDS: read(u) brings product u's,
+// mul(u, operand) does it.  Operands are read four at a time, a group ahead of the
+// products that run meanwhile.  (Left to itself the compiler saves registers:
+// it reads each operand just before its product and waits for it.)
+template <int N, typename Read, typename Mul>
+__device__ __forceinline__ void run_products(Read read, Mul mul) {
+    constexpr int G = 4;
+    static_assert(N % G == 0, "whole groups");
+    u32x4_t f[2][G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) f[0][i] = read(i);
+#pragma unroll
+    for (int g = 0; g < N / G; ++g) {
+        if (g + 1 < N / G) {
+#pragma unroll
+            for (int i = 0; i < G; ++i) f[(g + 1) & 1][i] = read((g + 1) * G + i);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < G; ++i) mul(g * G + i, f[g & 1][i]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 // G such loads, 1 KB apart in memory (but for the lanes' offsets) and in LDS, from
 // a scalar address: the instruction's offset counts for both.
-template <int G>
+#define DF2_TO_LDS_1(NT)                                    \
+    asm volatile(                                           \
+        "s_mov_b32 m0, %0\n\t"                              \
+        "s_nop 0\n\t"                                       \
+        "global_load_lds_dwordx4 %1, %2" NT                 \
+        :                                                   \
+        : "s"(lds_base), "v"(off[0]), "s"(base)             \
+        : "memory")
+#define DF2_TO_LDS_2(NT)                                    \
+    asm volatile(                                           \
+        "s_mov_b32 m0, %0\n\t"                              \
+        "s_nop 0\n\t"                                       \
+        "global_load_lds_dwordx4 %1, %3" NT "\n\t"          \
+        "global_load_lds_dwordx4 %2, %3 offset:1024" NT     \
+        :                                                   \
+        : "s"(lds_base), "v"(off[0]), "v"(off[1]), "s"(base) \
+        : "memory")
+#define DF2_TO_LDS_4(NT)                                    \
+    asm volatile(                                           \
+        "s_mov_b32 m0, %0\n\t"                              \
+        "s_nop 0\n\t"                                       \
+        "global_load_lds_dwordx4 %1, %5" NT "\n\t"          \
+        "global_load_lds_dwordx4 %2, %5 offset:1024" NT "\n\t" \
+        "global_load_lds_dwordx4 %3, %5 offset:2048" NT "\n\t" \
+        "global_load_lds_dwordx4 %4, %5 offset:3072" NT     \
+        :                                                   \
+        : "s"(lds_base), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base) \
+        : "memory")
+template <int G, bool ONCE>
 __device__ __forceinline__ void load_to_lds(const void* base, const uint32_t* off, uint32_t lds_base) {
     static_assert(G == 1 || G == 2 || G == 4, "loads in a group");
-    if constexpr (G == 1)
-        asm volatile(
-            "s_mov_b32 m0, %0\n\t"
-            "s_nop 0\n\t"
-            "global_load_lds_dwordx4 %1, %2"
-            :
-            : "s"(lds_base), "v"(off[0]), "s"(base)
-            : "memory");
-    else if constexpr (G == 2)
-        asm volatile(
-            "s_mov_b32 m0, %0\n\t"
-            "s_nop 0\n\t"
-            "global_load_lds_dwordx4 %1, %3\n\t"
-            "global_load_lds_dwordx4 %2, %3 offset:1024"
-            :
-            : "s"(lds_base), "v"(off[0]), "v"(off[1]), "s"(base)
-            : "memory");
-    else
-        asm volatile(
-            "s_mov_b32 m0, %0\n\t"
-            "s_nop 0\n\t"
-            "global_load_lds_dwordx4 %1, %5\n\t"
-            "global_load_lds_dwordx4 %2, %5 offset:1024\n\t"
-            "global_load_lds_dwordx4 %3, %5 offset:2048\n\t"
-            "global_load_lds_dwordx4 %4, %5 offset:3072"
-            :
-            : "s"(lds_base), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base)
-            : "memory");
+    // the same in the wave, also where the compiler cannot see it
+    const uint64_t addr = (uint64_t)base;
+    base = reinterpret_cast<const void*>(
+        ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(addr >> 32)) << 32) |
+        (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)addr));
+    if constexpr (G == 1) {
+        if constexpr (ONCE) DF2_TO_LDS_1(" nt");
+        else DF2_TO_LDS_1("");
+    } else if constexpr (G == 2) {
+        if constexpr (ONCE) DF2_TO_LDS_2(" nt");
+        else DF2_TO_LDS_2("");
+    } else {
+        if constexpr (ONCE) DF2_TO_LDS_4(" nt");
+        else DF2_TO_LDS_4("");
+    }
 }
+#undef DF2_TO_LDS_1
+#undef DF2_TO_LDS_2
+#undef DF2_TO_LDS_4
 
 // A value of the lane 32 away.
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
@@ -472,6 +521,7 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
     // tile.  Other tiles (the ends of the stretch, whose keys outside it are
     // replaced by its first or last; small pages) make each lane's address.
     constexpr int RW = Shape::kRows, RI = 64 / CH;      // keys of a wave, of a load
+    constexpr bool kOnce = WR <= 4;     // one block has all rows of a sequence, mostly
     constexpr int GL = Shape::kGroup, GK = GL * RI;     // loads and keys of a group
     int32_t* ids = reinterpret_cast<int32_t*>(lds + Shape::kLds);
     const int64_t head_off = (int64_t)head_kv << kv.page_shift;
@@ -485,8 +535,8 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
         at_k[i] = (lane / CH) * RB + ((lane % CH) ^ Tile::swz_k(row)) * 16;
         at_v[i] = (lane / CH) * RB + ((lane % CH) ^ Tile::swz_v(row)) * 16;
     }
-    auto load_tile = [&](int k0, int stage, int page0) {
-        const uint32_t to = lds0 + stage * Shape::kStage + w * NL * 1024;
+    auto load_tile = [&](const void* cache, int k0, uint32_t to, int page0, const uint32_t (&at)[NL]) {
+        to += w * NL * 1024;
         // all ids first: the loads are not reordered with LDS reads, which would
         // then wait one by one
         int id[NL];
@@ -498,8 +548,7 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
                 const int key = k0 + w * RW + i * RI;
                 const int64_t off = ((int64_t)__builtin_amdgcn_readfirstlane(id[i]) * kv.page_stride +
                                      (head_off + (key & page_mask)) * D) * Tile::kEsz;
-                load_to_lds<GL>(reinterpret_cast<const char*>(a.k) + off, at_k + i, to + i * 1024);
-                load_to_lds<GL>(reinterpret_cast<const char*>(a.v) + off, at_v + i, to + i * 1024 + Shape::kTileBytes);
+                load_to_lds<GL, kOnce>(reinterpret_cast<const char*>(cache) + off, at + i, to + i * 1024);
             }
         } else {
 #pragma unroll
@@ -509,9 +558,147 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
             for (int i = 0; i < NL; ++i) {
                 const int key = min(max(k0 + w * RW + i * RI + lane / CH, klo), khi - 1);
                 const int64_t off = ((int64_t)id[i] * kv.page_stride + (head_off + (key & page_mask)) * D) * Tile::kEsz;
-                load_to_lds(reinterpret_cast<const char*>(a.k) + off + at_k[i] % RB, to + i * 1024);
-                load_to_lds(reinterpret_cast<const char*>(a.v) + off + at_v[i] % RB, to + i * 1024 + Shape::kTileBytes);
+                load_to_lds<kOnce>(reinterpret_cast<const char*>(cache) + off + at[i] % RB, to + i * 1024);
             }
+        }
+    };
+    auto load_k = [&](int k0, int slot, int page0) {
+        load_tile(a.k, k0, lds0 + slot * Shape::kTileBytes, page0, at_k);
+    };
+    auto load_v = [&](int k0, int slot, int page0) {
+        load_tile(a.v, k0, lds0 + (NS + slot) * Shape::kTileBytes, page0, at_v);
+    };
+
+    // The first product of a tile, the scores of its keys for this wave's rows:
+    // product u = q * KS + ks takes chunk q of sub-tile ks (neighbouring products
+    // add to different sums).
+    f32x16_t s[KS];
+    constexpr int NQ = KS * QN;
+    const int k_row = wk * KS * 32 + col;
+    const uint32_t k_at = k_row * RB + (half ^ Tile::swz_k(k_row)) * 16;     // 32 rows on: the same permutation
+    auto key_operand = [&](int slot, int u) {
+        return *reinterpret_cast<const u32x4_t*>(lds + slot * Shape::kTileBytes + (u % KS) * 32 * RB +
+                                                 (k_at ^ (uint32_t)(u / KS * 32)));
+    };
+    auto key_product = [&](int u, u32x4_t kf, f32x16_t (&x)[KS]) {
+        const int q = u / KS, ks = u % KS;
+        if (q == 0) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) x[ks][v] = 0.f;
+        }
+        if constexpr (BF16) {
+            x[ks] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf), as_bf16x8(qf[q]), x[ks], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[ks] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(kf[e]), __uint_as_float(qf[q][e]), x[ks],
+                                                            0, 0, 0);
+        }
+    };
+    auto scores = [&](int slot, f32x16_t (&x)[KS]) {
+        run_products<NQ>([&](int u) { return key_operand(slot, u); },
+                         [&](int u, u32x4_t f) { key_product(u, f, x); });
+    };
+    // Masks the keys that a row does not see (tiles that every row sees whole need
+    // none) and returns the row's maximum in units of log2.
+    const int first_lim = min(a.causal ? ctx + t_lo + 1 : khi, khi);
+    const int last_low = max(a.window ? ctx + t_hi + 1 - a.window : 0, klo);
+    const int top = min(lim, khi), bottom = max(low, klo);
+    auto mask_and_max = [&](int k0, f32x16_t (&x)[KS]) {
+        if (k0 + KT > first_lim || k0 < last_low) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int key = k0 + (wk * KS + ks) * 32 + 8 * (v / 4) + 4 * half + v % 4;
+                    x[ks][v] = (key < top && key >= bottom) ? x[ks][v] : -INFINITY;
+                }
+        }
+        float mx = x[0][0];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) mx = fmaxf(mx, x[ks][v]);
+        return fmaxf(mx, other_half(mx)) * a.c;
+    };
+
+    // exp2 of the scores over the row's maximum, into the row's sum and packed for
+    // the second product: bf16 (one rounding, relative 2^-9 at most a value; the sum
+    // keeps the fp32 values), or as they are.
+    constexpr int PN = BF16 ? 8 : 16;
+    auto weights = [&](const f32x16_t (&x)[KS], uint32_t (&p)[KS][PN]) {
+        const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            float e[16];
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                e[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[ks][v], a.c, -ms));
+                l += e[v];
+            }
+#pragma unroll
+            for (int v = 0; v < PN; ++v) {
+                if constexpr (BF16)
+                    p[ks][v] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
+                        (f32x2_t){e[2 * v], e[2 * v + 1]}, bf16x2_t));
+                else
+                    p[ks][v] = __float_as_uint(e[v]);
+            }
+        }
+    };
+    // The maximum moves only where it grew by more than 2^8, so that most tiles
+    // need no rescaling: p stays below 2^8, and p / sum is the same.
+    auto move_max = [&](float mx) {
+        if (__any(mx > m + 8.f)) {
+            const float mn = fmaxf(m, mx);
+            const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) o[d][v] *= f;
+        }
+    };
+    // The second product of a tile.  bf16: product u = (ks * 2 + j) * DB + d takes
+    // 16 keys and 32 of the columns.
+    constexpr int NV = KS * 2 * DB;
+    const int v_row = wk * KS * 32 + 4 * half + ((lane & 15) >> 2);
+    const int v_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    auto value_operand = [&](int slot, int u) {
+        typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+        const int d = u % DB, keys = u / DB * 16;       // 16 rows on: the same permutation
+        const unsigned char* from = lds + (NS + slot) * Shape::kTileBytes + keys * RB + v_row * RB + (lane & 1) * 8 +
+                                    ((4 * d + v_chunk) ^ Tile::swz_v(v_row)) * 16;
+        const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)from);
+        const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + 8 * RB));
+        return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    auto value_product = [&](int u, u32x4_t vf, const uint32_t (&p)[KS][PN]) {
+        const int d = u % DB, j = u / DB;
+        const uint32_t* w4 = &p[j / 2][(j & 1) * 4];
+        const u32x4_t pf = {w4[0], w4[1], w4[2], w4[3]};
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vf), as_bf16x8(pf), o[d], 0, 0, 0);
+    };
+    auto add_values = [&](int slot, const uint32_t (&p)[KS][PN]) {
+        if constexpr (BF16) {
+            run_products<NV>([&](int u) { return value_operand(slot, u); },
+                             [&](int u, u32x4_t f) { value_product(u, f, p); });
+        } else {
+            const unsigned char* vt = lds + (NS + slot) * Shape::kTileBytes;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int row = (wk * KS + ks) * 32 + 8 * (v / 4) + 4 * half + v % 4;
+                    const int f = Tile::swz_v(row);
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        const float vf = *reinterpret_cast<const float*>(
+                            vt + row * RB + ((8 * d + (col >> 2)) ^ f) * 16 + (col & 3) * 4);
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, __uint_as_float(p[ks][v]), o[d], 0, 0, 0);
+                    }
+                }
         }
     };
 
@@ -535,128 +722,30 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
         // for them inside the loop would be one for all loads in flight.
 #pragma unroll
         for (int q = 0; q < QN; ++q) asm volatile("" : "+v"(qf[q]));
-        // A ring of NS stages, NS - 1 of them in flight or waiting.
+        uint32_t p[KS][PN];
+        // A ring of NS tiles, NS - 1 of them in flight or waiting.
 #pragma unroll
         for (int i = 0; i < NS - 1; ++i)
-            if (i < ntile) load_tile(k_win + i * KT, i, page0);
-        int stage = 0;
+            if (i < ntile) {
+                load_k(k_win + i * KT, i, page0);
+                load_v(k_win + i * KT, i, page0);
+            }
+        int slot = 0;
         for (int it = 0; it < ntile; ++it) {
             const int k0 = k_win + it * KT;
-            // this wave's part of the oldest stage is in LDS; then everyone's is,
-            // and nobody reads the stage before it any more
+            // this wave's part of the oldest tile is in LDS; then everyone's is,
+            // and nobody reads the tile before it any more
             wait_and_meet<NS - 2, 2 * NL>(ntile - 1 - it);
-            if (it + NS - 1 < ntile)
-                load_tile(k0 + (NS - 1) * KT, stage == 0 ? NS - 1 : stage - 1, page0);
-            const unsigned char* kt = lds + stage * Shape::kStage;
-            const unsigned char* vt = kt + Shape::kTileBytes;
-            stage = stage == NS - 1 ? 0 : stage + 1;
-            const int kw = k0 + wk * KS * 32;          // this wave's first key
-
-            f32x16_t s[KS];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const int row = (wk * KS + ks) * 32 + col;
-                const unsigned char* kp = kt + row * RB;
-                const int c0 = (half ^ Tile::swz_k(row)) * 16;
-                f32x16_t acc;
-#pragma unroll
-                for (int v = 0; v < 16; ++v) acc[v] = 0.f;
-#pragma unroll
-                for (int q = 0; q < QN; ++q) {
-                    const u32x4_t kf = *reinterpret_cast<const u32x4_t*>(kp + (c0 ^ (q * 32)));
-                    if constexpr (BF16) {
-                        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf), as_bf16x8(qf[q]), acc, 0, 0, 0);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(kf[e]), __uint_as_float(qf[q][e]),
-                                                                      acc, 0, 0, 0);
-                    }
-                }
-                s[ks] = acc;
+            if (it + NS - 1 < ntile) {
+                const int free = slot == 0 ? NS - 1 : slot - 1;
+                load_k(k0 + (NS - 1) * KT, free, page0);
+                load_v(k0 + (NS - 1) * KT, free, page0);
             }
-            // Mask the keys that a row does not see (tiles that every row sees
-            // whole need none).
-            const int first_lim = a.causal ? ctx + t_lo + 1 : khi;
-            const int last_low = a.window ? ctx + t_hi + 1 - a.window : 0;
-            if (k0 + KT > min(first_lim, khi) || k0 < max(last_low, klo)) {
-                const int top = min(lim, khi), bottom = max(low, klo);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const int key = kw + ks * 32 + 8 * (v / 4) + 4 * half + v % 4;
-                        s[ks][v] = (key < top && key >= bottom) ? s[ks][v] : -INFINITY;
-                    }
-            }
-            float mx = s[0][0];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[ks][v]);
-            mx = fmaxf(mx, other_half(mx)) * a.c;
-            // The maximum moves only where it grew by more than 2^8, so that most
-            // tiles need no rescaling: p stays below 2^8, and p / sum is the same.
-            if (__any(mx > m + 8.f)) {
-                const float mn = fmaxf(m, mx);
-                const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-                m = mn;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) o[d][v] *= f;
-            }
-            const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                float p[16];
-#pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    p[v] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[ks][v], a.c, -ms));
-                    l += p[v];
-                }
-                const int krow = (wk * KS + ks) * 32;
-                if constexpr (BF16) {
-                    // P enters the product in bf16 (one rounding, relative 2^-9 at
-                    // most a value); the sum keeps the fp32 values
-                    const int i = lane & 15, g = lane >> 4;
-                    const int tr_key = 4 * (g >> 1) + (i >> 2);
-                    const int tr_chunk = 2 * (g & 1) + ((i & 3) >> 1);
-                    const unsigned char* vp = vt + (krow + tr_key) * RB + (i & 1) * 8;
-                    const int f = Tile::swz_v(krow + tr_key);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        u32x4_t pf;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            pf[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
-                                (f32x2_t){p[8 * j + 2 * e], p[8 * j + 2 * e + 1]}, bf16x2_t));
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
-                            const unsigned char* at = vp + 16 * j * RB + (((4 * d + tr_chunk) ^ f) * 16);
-                            const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-                            const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * RB));
-                            const s16x8_t vf = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, vf), as_bf16x8(pf),
-                                                                          o[d], 0, 0, 0);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int v = 0; v < 16; ++v) {
-                        const int row = krow + 8 * (v / 4) + 4 * half + v % 4;
-                        const int f = Tile::swz_v(row);
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            const float vf = *reinterpret_cast<const float*>(
-                                vt + row * RB + ((8 * d + (col >> 2)) ^ f) * 16 + (col & 3) * 4);
-                            o[d] = __builtin_amdgcn_mfma_f32_32x32x2f32(vf, p[v], o[d], 0, 0, 0);
-                        }
-                    }
-                }
-            }
+            scores(slot, s);
+            move_max(mask_and_max(k0, s));
+            weights(s, p);
+            add_values(slot, p);
+            slot = slot == NS - 1 ? 0 : slot + 1;
         }
         k_win += ntile * KT;
     }
@@ -741,37 +830,38 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
 
 // Joins the parts of the blocks that lie across workgroups:
 //     sum_s 2^(m_s - m) (o_s, l_s)
-// over the parts s of a row.  Four workgroups for each boundary of stretches, of
-// which the first inside a block does the block; D / 4 lanes take a row, or
-// with many parts all of the workgroup, part by part, and meet in LDS.
+// over the parts s of a row.  Sixteen workgroups for each boundary of stretches, of
+// which the first inside a block does the block.  D / 4 lanes take a row, or
+// several such groups the row's parts in turn (few rows, perhaps many parts),
+// which then meet in LDS.
+constexpr int kJoinWgs = 16;
 template <bool BF16, int D>
 __global__ __launch_bounds__(256) void k_attend_join(AttnArgs a) {
     constexpr int L = D / 4, NG = 256 / L;
-    constexpr int kMany = 16;           // parts from which the workgroup takes a row at a time
     __shared__ f32x4_t lds_y[256];
     __shared__ float lds_m[NG], lds_l[NG];
-    const int quarter = blockIdx.x % 4, boundary = 1 + blockIdx.x / 4;
+    const int slice = blockIdx.x % kJoinWgs, boundary = 1 + blockIdx.x / kJoinWgs;
     const int32_t* split = a.split + 8 * boundary;
     const int w0 = boundary - 1, w1 = split[0], h = split[1], s0 = split[2], r0 = split[3], M = split[4];
     if (w1 < 0) return;
     const int group = threadIdx.x / L, d = (threadIdx.x % L) * 4;
-    const bool many = w1 - w0 >= kMany;
-    const int rows = a.bm / 4;
-    const int step = many ? 1 : NG, first_part = many ? group : 0, part_step = many ? NG : 1;
-    for (int i0 = quarter * rows; i0 < (quarter + 1) * rows && r0 + i0 < M; i0 += step) {
-        const int i = i0 + (many ? 0 : group), r = r0 + i;
-        const bool live = i < (quarter + 1) * rows && r < M;
+    const int rows = a.bm / kJoinWgs;                   // of this workgroup: 2 to 16
+    const int share = max(NG / rows, 1);                // groups of a row
+    const int at_once = NG / share;
+    for (int i0 = slice * rows; i0 < (slice + 1) * rows && r0 + i0 < M; i0 += at_once) {
+        const int i = i0 + group / share, r = r0 + i;
+        const bool live = r < M;
         float m = -INFINITY, l = 0.f;
         f32x4_t y = {0.f, 0.f, 0.f, 0.f};
         if (live) {
-            for (int w = w0 + first_part; w <= w1; w += 4 * part_step) {
+            for (int w = w0 + group % share; w <= w1; w += 4 * share) {
                 float pm[4], pl[4];
                 f32x4_t py[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int p = min(w + x * part_step, w1);
+                    const int p = min(w + x * share, w1);
                     const int64_t row = (int64_t)(2 * p + (p == w0 ? 1 : 0)) * a.bm + i;
-                    pm[x] = w + x * part_step <= w1 ? a.stat[2 * row] : -INFINITY;
+                    pm[x] = w + x * share <= w1 ? a.stat[2 * row] : -INFINITY;
                     pl[x] = a.stat[2 * row + 1];
                     py[x] = *reinterpret_cast<const f32x4_t*>(a.part + row * D + d);
                 }
@@ -792,7 +882,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttnArgs a) {
                 }
             }
         }
-        if (many) {
+        if (share > 1) {
             __syncthreads();
             lds_y[threadIdx.x] = y;
             if (threadIdx.x % L == 0) {
@@ -800,18 +890,15 @@ __global__ __launch_bounds__(256) void k_attend_join(AttnArgs a) {
                 lds_l[group] = l;
             }
             __syncthreads();
-            if (group > 0) continue;
-            float mn = -INFINITY;
-#pragma unroll
-            for (int x = 0; x < NG; ++x) mn = fmaxf(mn, lds_m[x]);
-            l = 0.f;
-            y = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int x = 0; x < NG; ++x) {
-                if (lds_m[x] == -INFINITY) continue;
-                const float e = __builtin_amdgcn_exp2f(lds_m[x] - mn);
-                l += e * lds_l[x];
-                y += e * lds_y[x * L + threadIdx.x];
+            if (group % share != 0) continue;
+            for (int x = 1; x < share; ++x) {
+                const float mx = lds_m[group + x];
+                if (mx == -INFINITY) continue;
+                const float mn = fmaxf(m, mx);
+                const float f = __builtin_amdgcn_exp2f(m - mn), e = __builtin_amdgcn_exp2f(mx - mn);
+                m = mn;
+                l = f * l + e * lds_l[group + x];
+                y = f * y + e * lds_y[(group + x) * L + threadIdx.x % L];
             }
         }
         if (!live) continue;

@@ -117,7 +117,7 @@ auto with_shape(int wr, F&& f) {
         if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2>());
         if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2>());
         if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2>());
-        return f(AttnShape<BF16, D, 8, 1, 2, 2>());
+        return f(AttnShape<BF16, D, 8, 1, 4, 2>());
     } else if constexpr (RB == 256) {
         if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2>());
         if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2>());
@@ -207,7 +207,7 @@ df2_status launch_attend(const AttnPlan& pl, const AttnArgs& a, hipStream_t stre
         return launched("dflash2_paged_attention launch");
     });
     if (st != DF2_OK || pl.wgs == 1 || pl.whole) return st;
-    hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)(4 * (pl.wgs - 1))), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)(kJoinWgs * (pl.wgs - 1))), dim3(256), 0, stream, a);
     return launched("dflash2_paged_attention join launch");
 }
 
@@ -339,15 +339,16 @@ struct VerifyPlan {
     size_t off_seg = 0, off_cnt = 0, bytes = 0;
 };
 
-// Segments of a row: about eight workgroups a compute unit over all rows, none
-// under 4 KB; for the one row a sequence's draw reads, two.
+// Segments of a row in launch 1: about eight workgroups a compute unit over all
+// rows, none under 4 KB, a power of two (launch 2 takes several rows a wave).
+// Segments of the one row that a sequence's draw reads: 4096 elements, 16 for
+// each lane.
 VerifyPlan plan_verify(const df2_verify_dims* d) {
     VerifyPlan pl;
     const int64_t rows = (int64_t)d->B * (d->P + 1), cus = compute_units();
     const int64_t row_bytes = (int64_t)d->V * (d->dtype == DF2_BF16 ? 2 : 4);
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kVerifySegs, row_bytes / 4096));
-    pl.nseg = (int)std::max<int64_t>(1, std::min<int64_t>(most, 8 * cus / rows));
-    pl.nseg2 = (int)std::max<int64_t>(1, std::min<int64_t>(most, 2 * cus / d->B));
+    while (pl.nseg < kVerifySegs && 2 * pl.nseg * rows <= 8 * cus && 2 * pl.nseg * 4096 <= row_bytes) pl.nseg *= 2;
+    pl.nseg2 = (int)std::max<int64_t>(1, std::min<int64_t>(kVerifySegs, (d->V + 4095) / 4096));
     pl.off_seg = (size_t)rows * pl.nseg * 8;
     pl.off_cnt = pl.off_seg + (size_t)d->B * pl.nseg2 * 8;
     pl.bytes = (pl.off_cnt + (size_t)d->B * 4 + 15) / 16 * 16;
@@ -443,6 +444,7 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
     a.nseg = pl.nseg;
     a.nseg2 = pl.nseg2;
     a.c = (float)c64;
+    a.c_low = (float)(c64 - (double)a.c);
     a.c64 = c64;
     return dims->dtype == DF2_BF16 ? launch_verify<true>(dims, best, pl, a, stream)
                                    : launch_verify<false>(dims, best, pl, a, stream);

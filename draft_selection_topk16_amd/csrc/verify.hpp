@@ -47,7 +47,7 @@ struct VerifyArgs {
     uint32_t* err;
     int B, P, V, K;
     int nseg, nseg2;
-    float c;                    // log2(e) / temperature
+    float c, c_low;             // log2(e) / temperature, and what fp32 leaves of it
     double c64;
 };
 
@@ -157,9 +157,14 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
                 acc.s *= __builtin_amdgcn_exp2f((acc.m - m) * a.c);
                 acc.m = m;
             }
-            // the difference first: the product's rounding is then relative to it
+            // the difference first, so that the product's rounding is relative to it;
+            // the factor in two parts, or its own rounding would move every weight
+            // the same way
             const float mm = acc.m == -INFINITY ? 0.f : acc.m;
-            for (int i = 0; i < n; ++i) acc.s += __builtin_amdgcn_exp2f((x[i] - mm) * a.c);
+            for (int i = 0; i < n; ++i) {
+                const float d = x[i] - mm;
+                acc.s += __builtin_amdgcn_exp2f(__builtin_fmaf(d, a.c, d * a.c_low));
+            }
         }
     };
     for (int v = v0 + tid; v < v1; v += kWG * U) {
@@ -218,14 +223,14 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
 
 struct VerifyLds {
     float m[72], s[72];         // maximum and sum of each row (P + 1 <= 65)
-    float odds[72];             // p of each draft
-    int cid[64];                // candidates of the drawn row and what they lose
+    uint32_t q[72];             // bits of the draft's probability of each drafted token
+    float odds[72];             // p of each drafted token
+    int cid[64];                // candidates of the drawn row, and what they lose
     double cut[64];
-    double lane_sum[kWG];
-    int taken, nd, pick;
+    double sums[kWG];
+    int taken, nd, pick, seg;
     uint32_t flag;
     double z, target;
-    int seg;
 };
 
 // One wave finds the first of n <= 256 values whose running sum exceeds
@@ -268,32 +273,88 @@ __device__ __forceinline__ int find_prefix(const double* sum, int n, double& tar
     return at >= 0 ? at : last;
 }
 
+// Elements of lane run `i` of a segment (vectors v0 .. v1 - 1 and, in the first and
+// last segment, the row's ends): `len` vectors each, in order.
+template <bool BF16>
+__device__ __forceinline__ int run_first(const RowCut<BF16>& cut, int seg, int nseg, int len, int i) {
+    if (i == 0) return cut.first(seg, nseg);
+    if (i == kWG) return cut.first(seg + 1, nseg);
+    return cut.head + min(cut.first_vec(seg, nseg) + i * len, cut.first_vec(seg + 1, nseg)) * RowCut<BF16>::kE;
+}
+
+// The sum of a run's weights in fp64.
+template <bool BF16, int KIND>
+__device__ __forceinline__ double run_sum(const char* rp, const RowCut<BF16>& cut, int seg, int nseg, int len, int i,
+                                          float m, double c64) {
+    constexpr int E = RowCut<BF16>::kE, SZ = RowCut<BF16>::kSz;
+    const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(rp + (size_t)cut.head * SZ);
+    const int v1 = cut.first_vec(seg + 1, nseg);
+    const int a = min(cut.first_vec(seg, nseg) + i * len, v1), b = min(a + len, v1);
+    double s = 0.0;
+    for (int v = a; v < b; v += 2) {
+        const bool two = v + 1 < b;
+        const u32x4_t w0 = vp[v], w1 = vp[two ? v + 1 : v];
+        float x[E];
+        unpack16<BF16>(w0, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += weight64<KIND>(x[e], m, c64);
+        if (two) {
+            unpack16<BF16>(w1, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) s += weight64<KIND>(x[e], m, c64);
+        }
+    }
+    if (i == 0 && seg == 0)
+        for (int e = 0; e < cut.head; ++e) s += weight64<KIND>(row_value<BF16>(rp, e), m, c64);
+    if (i == kWG - 1 && seg == nseg - 1)
+        for (int e = cut.head + cut.nv * E; e < cut.V; ++e) s += weight64<KIND>(row_value<BF16>(rp, e), m, c64);
+    return s;
+}
+
 // Launch 2 (sampling): nseg2 workgroups a sequence.
 template <bool BF16, int KIND>
 __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
-    constexpr int E = RowCut<BF16>::kE, SZ = RowCut<BF16>::kSz;
+    constexpr int SZ = RowCut<BF16>::kSz;
     __shared__ VerifyLds sm;
     const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
     const int b = (int)(blockIdx.x / a.nseg2), seg = (int)(blockIdx.x % a.nseg2);
     const int P = a.P, R = P + 1, K = a.K;
     const int64_t row0 = (int64_t)b * R;
+    const char* rows = reinterpret_cast<const char*>(a.target) + (size_t)row0 * a.V * SZ;
 
-    // 1. Every row's maximum and sum from its segments.
-    for (int t = w; t < R; t += kWaves) {
+    // 1. Every row's maximum and sum from its segments (a power of two of them: the
+    // lanes of a wave take several rows at once), and the draft's probability of
+    // each drafted token: all of the loads side by side.
+    if (tid < 72) sm.q[tid] = 0;
+    int32_t draft = -1;
+    float at_draft = 0.f;
+    if (w == 0 && lane < P) {
+        draft = a.path[(int64_t)b * P + lane];
+        if ((unsigned)draft < (unsigned)a.V) at_draft = row_value<BF16>(rows + (size_t)lane * a.V * SZ, draft);
+    }
+    for (int x0 = w * 64; x0 < R * a.nseg; x0 += kWG) {
+        const int x = x0 + lane;
         Lse acc = {KIND == kVerifyProbs ? 0.f : -INFINITY, 0.f};
-        if (lane < a.nseg) {
-            const uint64_t x = a.part[(row0 + t) * a.nseg + lane];
-            acc = {__uint_as_float((uint32_t)(x >> 32)), __uint_as_float((uint32_t)x)};
+        if (x < R * a.nseg) {
+            const uint64_t y = a.part[row0 * a.nseg + x];
+            acc = {__uint_as_float((uint32_t)(y >> 32)), __uint_as_float((uint32_t)y)};
         }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
+        for (int o = 1; o < a.nseg; o <<= 1) {
             const Lse y = {__shfl_xor(acc.m, o), __shfl_xor(acc.s, o)};
             acc = lse_join<KIND>(acc, y, a.c);
         }
-        if (lane == 0) {
-            sm.m[t] = acc.m;
-            sm.s[t] = acc.s;
+        if (x < R * a.nseg && x % a.nseg == 0) {
+            sm.m[x / a.nseg] = acc.m;
+            sm.s[x / a.nseg] = acc.s;
         }
+    }
+    __syncthreads();
+    for (int x = tid; x < P * K; x += kWG) {
+        const int t = x / K;
+        const int64_t at = (int64_t)b * P * K + x;
+        // candidates of a row are distinct: one hit at most (the largest otherwise)
+        const float q = a.prob[at];
+        if (a.cand[at] == a.path[(int64_t)b * P + t]) atomicMax(&sm.q[t], __float_as_uint(fmaxf(q, 0.f)));
     }
     __syncthreads();
 
@@ -302,23 +363,15 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         const int nd = a.n_draft ? min(max(a.n_draft[b], 0), P) : P;
         bool yes = false;
         if (lane < P) {
-            const int32_t d = a.path[(int64_t)b * P + lane];
             double p = 0.0;
-            if ((unsigned)d < (unsigned)a.V) {
-                const char* rp = reinterpret_cast<const char*>(a.target) + (size_t)(row0 + lane) * a.V * SZ;
-                if (sm.s[lane] > 0.f)
-                    p = weight64<KIND>(row_value<BF16>(rp, d), sm.m[lane], a.c64) / (double)sm.s[lane];
+            if ((unsigned)draft < (unsigned)a.V) {
+                if (sm.s[lane] > 0.f) p = weight64<KIND>(at_draft, sm.m[lane], a.c64) / (double)sm.s[lane];
             } else if (lane < nd) {
                 atomicOr(a.err, kFlagDraft);
             }
-            double q = 0.0;
-            for (int k = 0; k < K; ++k) {
-                const int64_t at = ((int64_t)b * P + lane) * K + k;
-                q += a.cand[at] == d ? (double)a.prob[at] : 0.0;
-            }
             float u = a.u[row0 + lane];
             u = (u >= 0.f) ? fminf(u, 0x1.fffffep-1f) : 0.f;
-            yes = lane < nd && (double)u * q < p;
+            yes = lane < nd && (double)u * (double)__uint_as_float(sm.q[lane]) < p;
             sm.odds[lane] = (float)p;
         }
         const uint64_t ok = __ballot(yes);
@@ -332,60 +385,45 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
     const int t = sm.taken;
     const bool refused = t < sm.nd;
     const float m = sm.m[t];
-    const char* rp = reinterpret_cast<const char*>(a.target) + (size_t)(row0 + t) * a.V * SZ;
-    const RowCut<BF16> cut(rp, a.V);
-
-    // 3. This segment of row t in fp64.
     const bool mass = sm.s[t] > 0.f;
-    {
-        const int v0 = cut.first_vec(seg, a.nseg2), v1 = cut.first_vec(seg + 1, a.nseg2);
-        const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(rp + (size_t)cut.head * SZ);
-        double s = 0.0;
-        for (int v = v0 + tid; v < v1; v += kWG) {
-            float x[E];
-            unpack16<BF16>(vp[v], x);
+    const char* rp = rows + (size_t)t * a.V * SZ;
+    const RowCut<BF16> cut(rp, a.V);
+    auto run_len = [&](int g) { return (cut.first_vec(g + 1, a.nseg2) - cut.first_vec(g, a.nseg2) + kWG - 1) / kWG; };
+
+    // 3. This segment of row t, a run of it for each lane.
+    double s = run_sum<BF16, KIND>(rp, cut, seg, a.nseg2, run_len(seg), tid, m, a.c64);
 #pragma unroll
-            for (int i = 0; i < E; ++i) s += weight64<KIND>(x[i], m, a.c64);
-        }
-        if (seg == 0 && tid < cut.head) s += weight64<KIND>(row_value<BF16>(rp, tid), m, a.c64);
-        const int tail = cut.head + cut.nv * E + tid;
-        if (seg == a.nseg2 - 1 && tail < a.V) s += weight64<KIND>(row_value<BF16>(rp, tail), m, a.c64);
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-        if (lane == 0) sm.lane_sum[w] = s;
-        __syncthreads();
-        if (tid == 0) xstore(a.seg + (int64_t)b * a.nseg2 + seg, sm.lane_sum[0] + sm.lane_sum[1] + sm.lane_sum[2] + sm.lane_sum[3]);
-    }
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if (lane == 0) sm.sums[w] = s;
+    __syncthreads();
+    if (tid == 0) xstore(a.seg + (int64_t)b * a.nseg2 + seg, sm.sums[0] + sm.sums[1] + sm.sums[2] + sm.sums[3]);
     if (!block_arrive_last(&a.cnt[b], (uint32_t)a.nseg2, &sm.flag)) return;
 
-    // 4. The last workgroup draws.  Segment sums and what the candidates lose:
-    // min(w, q Z) each.
-    if (tid < a.nseg2) sm.lane_sum[tid] = xload(a.seg + (int64_t)b * a.nseg2 + tid);
+    // 4. The last workgroup draws.  What each candidate loses is min(w, q Z).
+    int id = -1;
+    double loss = 0.0;
+    if (tid < a.nseg2) sm.sums[tid] = xload(a.seg + (int64_t)b * a.nseg2 + tid);
+    if (w == 1 && lane < K && refused) {
+        const int64_t at = ((int64_t)b * P + t) * K + lane;
+        id = a.cand[at];
+        loss = (double)fmaxf(a.prob[at], 0.f);
+        if ((unsigned)id >= (unsigned)a.V) {
+            atomicOr(a.err, 2u);
+            id = -1;
+        }
+    }
+    const float at_cand = id >= 0 ? row_value<BF16>(rp, id) : 0.f;
     __syncthreads();
     if (w == 0) {
-        double z = lane < a.nseg2 ? sm.lane_sum[lane] : 0.0;
+        double z = lane < a.nseg2 ? sm.sums[lane] : 0.0;
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o);
         if (lane == 0) sm.z = z;
     }
     __syncthreads();
-    if (tid < K) {
-        int id = -1;
-        float q = 0.f;
-        double loss = 0.0;
-        if (refused) {
-            const int64_t at = ((int64_t)b * P + t) * K + tid;
-            id = a.cand[at];
-            q = a.prob[at];
-            if ((unsigned)id >= (unsigned)a.V) {
-                atomicOr(a.err, 2u);
-                id = -1;
-            } else {
-                loss = fmin(weight64<KIND>(row_value<BF16>(rp, id), m, a.c64), fmax((double)q * sm.z, 0.0));
-            }
-        }
-        sm.cid[tid] = id;
-        sm.cut[tid] = loss;
+    if (w == 1) {
+        sm.cid[lane] = id;
+        sm.cut[lane] = id >= 0 ? fmin(weight64<KIND>(at_cand, m, a.c64), loss * sm.z) : 0.0;
     }
     __syncthreads();
     auto loss_in = [&](int e0, int e1) {
@@ -393,40 +431,38 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         for (int k = 0; k < K; ++k) x += (sm.cid[k] >= e0 && sm.cid[k] < e1) ? sm.cut[k] : 0.0;
         return x;
     };
-    if (tid < a.nseg2) {
-        const double s = sm.lane_sum[tid] - loss_in(cut.first(tid, a.nseg2), cut.first(tid + 1, a.nseg2));
-        sm.lane_sum[tid] = s > 0.0 ? s : 0.0;
-    }
-    __syncthreads();
     if (w == 0) {
-        double whole = lane < a.nseg2 ? sm.lane_sum[lane] : 0.0;
+        double left = 0.0;
+        if (lane < a.nseg2) {
+            left = sm.sums[lane] - loss_in(cut.first(lane, a.nseg2), cut.first(lane + 1, a.nseg2));
+            left = left > 0.0 ? left : 0.0;
+            sm.sums[lane] = left;
+        }
+        double whole = left;
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) whole += __shfl_xor(whole, o);
         float u = a.u[row0 + P];
         u = (u >= 0.f) ? fminf(u, 0x1.fffffep-1f) : 0.f;
         double target = (double)u * whole;
-        const int at = find_prefix(sm.lane_sum, a.nseg2, target);
+        wave_sync();
+        const int at = find_prefix(sm.sums, a.nseg2, target);
         if (lane == 0) {
             sm.seg = at;
             sm.target = target;
         }
     }
     __syncthreads();
-    // a run of the segment for each lane
-    const int e0 = cut.first(sm.seg, a.nseg2), e1 = cut.first(sm.seg + 1, a.nseg2);
-    const int len = (e1 - e0 + kWG - 1) / kWG;
+    const int g = sm.seg, len = run_len(g);
     {
-        const int i0 = min(e0 + tid * len, e1), i1 = min(i0 + len, e1);
-        double s = 0.0;
-        for (int i = i0; i < i1; ++i) s += weight64<KIND>(row_value<BF16>(rp, i), m, a.c64);
-        s -= loss_in(i0, i1);
-        sm.lane_sum[tid] = s > 0.0 ? s : 0.0;
+        double x = run_sum<BF16, KIND>(rp, cut, g, a.nseg2, len, tid, m, a.c64);
+        x -= loss_in(run_first(cut, g, a.nseg2, len, tid), run_first(cut, g, a.nseg2, len, tid + 1));
+        sm.sums[tid] = x > 0.0 ? x : 0.0;
     }
     __syncthreads();
     if (w == 0) {
         double target = sm.target;
-        const int at = find_prefix(sm.lane_sum, kWG, target);
-        const int i0 = min(e0 + at * len, e1), i1 = min(i0 + len, e1);
+        const int at = find_prefix(sm.sums, kWG, target);
+        const int i0 = run_first(cut, g, a.nseg2, len, at), i1 = run_first(cut, g, a.nseg2, len, at + 1);
         double run = 0.0;
         int pick = -1, last = -1;
         for (int c0 = i0; c0 < i1 && pick < 0; c0 += 64) {
