@@ -32,6 +32,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "lanes.hpp"
 
 namespace df2 {
 
@@ -130,17 +131,6 @@ __device__ __forceinline__ BlockKeys block_keys(const AttnArgs& a, int ctx, int 
     return k;
 }
 
-// Sum over the lanes up to this one.
-__device__ __forceinline__ int wave_scan(int x) {
-    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);     // within 16 lanes: shifts by 1, 2, 4, 8
-    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
-    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);     // lane 15 to the next 16, 47 likewise
-    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);     // lane 31 to the upper half
-    return x;
-}
-
 // Sequences of more blocks than this are gone through by the whole wave, a lane to
 // a block; others by their lane.
 constexpr int kLaneBlocks = 4;
@@ -169,7 +159,7 @@ __device__ __forceinline__ LaneSeq lane_seq(const AttnArgs& a, int c0) {
         const int blocks = __builtin_amdgcn_readlane(q.blocks, f);
         int sum = 0;
         for (int j = lane; j < blocks; j += 64) sum += block_keys(a, ctx, n, j).tiles;
-        sum = __builtin_amdgcn_readlane(wave_scan(sum), 63);
+        sum = __builtin_amdgcn_readlane(lanes_scan(sum), 63);
         if (lane == f) q.tiles = sum;
     }
     return q;
@@ -191,7 +181,7 @@ __device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
     c.head_tiles = 0;
     for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
         q = lane_seq(a, c0);
-        c.head_tiles += __builtin_amdgcn_readlane(wave_scan(q.tiles), 63);
+        c.head_tiles += __builtin_amdgcn_readlane(lanes_scan(q.tiles), 63);
     }
     const int all = c.head_tiles * a.kv.Hkv;
     c.wgs = min(a.wgs, all);
@@ -211,7 +201,7 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, int g, 
     int before = 0;
     for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
         if (a.kv.B > 64) q = lane_seq(a, c0);
-        const int incl = wave_scan(q.tiles);
+        const int incl = lanes_scan(q.tiles);
         const uint64_t hit = __ballot(before + incl > g);
         if (hit) {
             const int f = __builtin_ctzll(hit);
@@ -230,7 +220,7 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, int g, 
                 for (int j0 = 0; j0 < p.blocks; j0 += 64) {
                     const int j = j0 + lane_id();
                     const int own = j < p.blocks ? block_keys(a, p.ctx, p.n, j).tiles : 0;
-                    const int sum = wave_scan(own);
+                    const int sum = lanes_scan(own);
                     const uint64_t here = __ballot(p.first + sum > g);
                     if (here) {
                         const int l = __builtin_ctzll(here);
@@ -356,9 +346,6 @@ __device__ __forceinline__ void load_to_lds(const void* base, const uint32_t* of
 #undef DF2_TO_LDS_1
 #undef DF2_TO_LDS_2
 #undef DF2_TO_LDS_4
-
-// A value of the lane 32 away.
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
 
 template <bool BF16, int D>
 struct AttnTile {
@@ -619,7 +606,9 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int v = 0; v < 16; ++v) mx = fmaxf(mx, x[ks][v]);
-        return fmaxf(mx, other_half(mx)) * a.c;
+        float lower, upper;
+        pair_of<32>(mx, lower, upper);
+        return fmaxf(lower, upper) * a.c;
     };
 
     // exp2 of the scores over the row's maximum, into the row's sum and packed for
@@ -749,7 +738,11 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
         }
         k_win += ntile * KT;
     }
-    l += other_half(l);
+    {
+        float lower, upper;
+        pair_of<32>(l, lower, upper);
+        l = lower + upper;
+    }
 
     if constexpr (WK > 1) {
         // The groups' results meet in LDS: statistics first, then each wave's

@@ -335,20 +335,29 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
 namespace {
 
 struct VerifyPlan {
-    int nseg = 1, nseg2 = 1;
+    int nseg = 1, nseg_log = 0, per = 1;
+    int nseg2 = 1, per2 = 1, len2 = 1;
     size_t off_seg = 0, off_cnt = 0, bytes = 0;
 };
 
 // Segments of a row in launch 1: about eight workgroups a compute unit over all
 // rows, none under 4 KB, a power of two (launch 2 takes several rows a wave).
 // Segments of the one row that a sequence's draw reads: 4096 elements, 16 for
-// each lane.
+// each lane, or more where that would be more workgroups than run at once.
 VerifyPlan plan_verify(const df2_verify_dims* d) {
     VerifyPlan pl;
     const int64_t rows = (int64_t)d->B * (d->P + 1), cus = compute_units();
     const int64_t row_bytes = (int64_t)d->V * (d->dtype == DF2_BF16 ? 2 : 4);
-    while (pl.nseg < kVerifySegs && 2 * pl.nseg * rows <= 8 * cus && 2 * pl.nseg * 4096 <= row_bytes) pl.nseg *= 2;
-    pl.nseg2 = (int)std::max<int64_t>(1, std::min<int64_t>(kVerifySegs, (d->V + 4095) / 4096));
+    while (pl.nseg < kVerifySegs && 2 * pl.nseg * rows <= 8 * cus && 2 * pl.nseg * 4096 <= row_bytes) {
+        pl.nseg *= 2;
+        ++pl.nseg_log;
+    }
+    pl.nseg2 = (int)std::max<int64_t>(1, std::min<int64_t>(
+        {kVerifySegs, (d->V + 4095) / 4096, 2 * cus / d->B}));
+    const int vectors = d->V / (d->dtype == DF2_BF16 ? 8 : 4);      // one less in some rows that start unaligned
+    pl.per = std::max(1, (vectors + pl.nseg - 1) / pl.nseg);
+    pl.per2 = std::max(1, (vectors + pl.nseg2 - 1) / pl.nseg2);
+    pl.len2 = (pl.per2 + kWG - 1) / kWG;
     pl.off_seg = (size_t)rows * pl.nseg * 8;
     pl.off_cnt = pl.off_seg + (size_t)d->B * pl.nseg2 * 8;
     pl.bytes = (pl.off_cnt + (size_t)d->B * 4 + 15) / 16 * 16;
@@ -441,8 +450,12 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
     a.P = dims->P;
     a.V = dims->V;
     a.K = dims->K;
-    a.nseg = pl.nseg;
+    a.nseg_log = pl.nseg_log;
+    a.per = pl.per;
     a.nseg2 = pl.nseg2;
+    a.per2 = pl.per2;
+    a.len2 = pl.len2;
+    a.k_inv = (1u << 20) / (uint32_t)dims->K + 1;
     a.c = (float)c64;
     a.c_low = (float)(c64 - (double)a.c);
     a.c64 = c64;

@@ -22,6 +22,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "lanes.hpp"
 
 namespace df2 {
 
@@ -46,26 +47,28 @@ struct VerifyArgs {
     uint32_t* cnt;              // [B] arrivals, zeroed by launch 1
     uint32_t* err;
     int B, P, V, K;
-    int nseg, nseg2;
+    int nseg_log, per;          // launch 1: segments of a row (2^nseg_log), vectors of each
+    int nseg2, per2, len2;      // launch 2: the same, and vectors of a lane's run
+    uint32_t k_inv;             // 2^20 / K + 1: x / K for x < 4096
     float c, c_low;             // log2(e) / temperature, and what fp32 leaves of it
     double c64;
 };
 
-// Elements of a row split over segments: whole 16-byte vectors where they are
-// aligned, the elements before the first and behind the last one to the first
-// and last segment.
+// Elements of a row split over segments of `per` whole 16-byte vectors where they
+// are aligned (the last ones shorter or empty), the elements before the first and
+// behind the last vector to the first and last segment.
 template <bool BF16>
 struct RowCut {
     static constexpr int kE = BF16 ? 8 : 4, kSz = BF16 ? 2 : 4;
-    int head, nv, V;
-    __device__ __forceinline__ RowCut(const char* row, int V_) : V(V_) {
+    int head, nv, V, per, nseg;
+    __device__ __forceinline__ RowCut(const char* row, int V_, int per_, int nseg_) : V(V_), per(per_), nseg(nseg_) {
         const int off = (int)((uintptr_t)row & 15u);
         head = min(V_, off ? (16 - off) / kSz : 0);
         nv = (V_ - head) / kE;
     }
-    __device__ __forceinline__ int first_vec(int s, int nseg) const { return (int)((int64_t)nv * s / nseg); }
-    __device__ __forceinline__ int first(int s, int nseg) const {
-        return s == 0 ? 0 : (s == nseg ? V : head + first_vec(s, nseg) * kE);
+    __device__ __forceinline__ int first_vec(int s) const { return min(s * per, nv); }
+    __device__ __forceinline__ int first(int s) const {
+        return s == 0 ? 0 : (s == nseg ? V : head + first_vec(s) * kE);
     }
 };
 
@@ -88,30 +91,36 @@ __device__ __forceinline__ void unpack16(u32x4_t w, float (&x)[BF16 ? 8 : 4]) {
     }
 }
 
-// 2^y in fp64 for y <= 0: whole part by exponent, the rest by its series (the
-// first term left out is below 2 10^-13).
-__device__ __forceinline__ double exp2_64(double y) {
-    if (y < -1000.0) return 0.0;
-    const double n = rint(y), f = (y - n) * 0.69314718055994531;
-    double s = 1.0 / 3628800.0;
-    s = fma(s, f, 1.0 / 362880.0);
-    s = fma(s, f, 1.0 / 40320.0);
-    s = fma(s, f, 1.0 / 5040.0);
-    s = fma(s, f, 1.0 / 720.0);
-    s = fma(s, f, 1.0 / 120.0);
-    s = fma(s, f, 1.0 / 24.0);
-    s = fma(s, f, 1.0 / 6.0);
-    s = fma(s, f, 0.5);
-    s = fma(s, f, 1.0);
-    s = fma(s, f, 1.0);
-    return ldexp(s, (int)n);
-}
-
-// A value's weight; m: the row's maximum (logits).
+// Weights of a row in fp64.  Logits: 2^y, y = (x - m) log2(e) / temperature, as
+// 2^e * 2^(j / 32) * 2^(f / 32), |f| <= 1/2: the whole part through the exponent
+// field, the 32nds from a table in LDS, the rest by the series of 2^(f / 32), whose
+// first term left out is below 1.3 10^-12.  That is half the fp64 instructions of
+// a series over a whole octave; the pass over a row is bound by them.
+constexpr int kExpTable = 32;
 template <int KIND>
-__device__ __forceinline__ double weight64(float x, float m, double c64) {
-    if constexpr (KIND == kVerifyProbs) return fmax((double)x, 0.0);
-    return exp2_64(((double)x - (double)m) * c64);
+struct Weights {
+    const double* table;        // 2^(j / 32)
+    double m, c32;              // the row's maximum, 32 log2(e) / temperature
+    __device__ __forceinline__ Weights(const double* t, float m_, double c64) : table(t), m(m_), c32(32.0 * c64) {}
+    __device__ __forceinline__ double operator()(float x) const {
+        if constexpr (KIND == kVerifyProbs) return fmax((double)x, 0.0);
+        const double y = ((double)x - m) * c32;         // the difference first: it is exact next to m
+        const double shifted = y + 0x1.8p52;            // its low word is y to the nearest whole
+        const int n = (int)(uint32_t)(uint64_t)__double_as_longlong(shifted);
+        const double f = y - (shifted - 0x1.8p52);
+        constexpr double k = 0.69314718055994531 / kExpTable;
+        double s = k * k * k * k / 24.0;
+        s = fma(s, f, k * k * k / 6.0);
+        s = fma(s, f, k * k / 2.0);
+        s = fma(s, f, k);
+        s = fma(s, f, 1.0);
+        s *= table[n & (kExpTable - 1)];
+        const uint64_t w = (uint64_t)__double_as_longlong(s) + ((uint64_t)(uint32_t)((n >> 5) << 20) << 32);
+        return y > -1000.0 * kExpTable ? __longlong_as_double((long long)w) : 0.0;     // 2^-1000 and less: 0
+    }
+};
+__device__ __forceinline__ void fill_exp_table(double* table) {
+    if (threadIdx.x < kExpTable) table[threadIdx.x] = exp2((double)threadIdx.x / kExpTable);
 }
 
 // Running (max, sum) of weights.
@@ -125,6 +134,14 @@ __device__ __forceinline__ Lse lse_join(Lse a, Lse b, float c) {
     if (m == -INFINITY) return {m, 0.f};
     return {m, a.s * __builtin_amdgcn_exp2f((a.m - m) * c) + b.s * __builtin_amdgcn_exp2f((b.m - m) * c)};
 }
+// The same over groups of N lanes: the maximum first, then the sums at it.
+template <int KIND, int N>
+__device__ __forceinline__ Lse lse_lanes(Lse a, float c) {
+    if constexpr (KIND == kVerifyProbs) return {0.f, lanes_sum<N>(a.s)};
+    const float m = lanes_max<N>(a.m);
+    const float s = m == -INFINITY ? 0.f : a.s * __builtin_amdgcn_exp2f((a.m - m) * c);
+    return {m, lanes_sum<N>(s)};
+}
 
 // Launch 1: one workgroup a segment of a row.
 template <bool BF16, int KIND>
@@ -132,12 +149,12 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
     constexpr int E = RowCut<BF16>::kE, SZ = RowCut<BF16>::kSz, U = 4;
     __shared__ uint64_t red[kWaves];
     const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
-    const int64_t row = blockIdx.x / a.nseg;
-    const int seg = (int)(blockIdx.x % a.nseg);
+    const int64_t row = blockIdx.x >> a.nseg_log;
+    const int nseg = 1 << a.nseg_log, seg = (int)(blockIdx.x & (nseg - 1));
     if (seg == 0 && tid == 0 && row % (a.P + 1) == 0) a.cnt[row / (a.P + 1)] = 0;
     const char* rp = reinterpret_cast<const char*>(a.target) + (size_t)row * a.V * SZ;
-    const RowCut<BF16> cut(rp, a.V);
-    const int v0 = cut.first_vec(seg, a.nseg), v1 = cut.first_vec(seg + 1, a.nseg);
+    const RowCut<BF16> cut(rp, a.V, a.per, nseg);
+    const int v0 = cut.first_vec(seg), v1 = cut.first_vec(seg + 1);
     const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(rp + (size_t)cut.head * SZ);
 
     Lse acc = {KIND == kVerifyProbs ? 0.f : -INFINITY, 0.f};
@@ -186,7 +203,7 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
         take(x, 1, tid);
     }
     const int tail = cut.head + cut.nv * E + tid;
-    if (seg == a.nseg - 1 && tail < a.V) {
+    if (seg == nseg - 1 && tail < a.V) {
         const float x[1] = {row_value<BF16>(rp, tail)};
         take(x, 1, tail);
     }
@@ -197,11 +214,7 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
             best = y > best ? y : best;
         }
     } else {
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const Lse y = {__shfl_xor(acc.m, o), __shfl_xor(acc.s, o)};
-            acc = lse_join<KIND>(acc, y, a.c);
-        }
+        acc = lse_lanes<KIND, 64>(acc, a.c);
         best = ((uint64_t)__float_as_uint(acc.m) << 32) | __float_as_uint(acc.s);
     }
     if (lane == 0) red[w] = best;
@@ -217,7 +230,7 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
                 out = ((uint64_t)__float_as_uint(y.m) << 32) | __float_as_uint(y.s);
             }
         }
-        a.part[row * a.nseg + seg] = out;
+        a.part[row * nseg + seg] = out;
     }
 }
 
@@ -228,6 +241,7 @@ struct VerifyLds {
     int cid[64];                // candidates of the drawn row, and what they lose
     double cut[64];
     double sums[kWG];
+    double table[kExpTable];
     int taken, nd, pick, seg;
     uint32_t flag;
     double z, target;
@@ -245,23 +259,18 @@ __device__ __forceinline__ int find_prefix(const double* sum, int n, double& tar
         x[j] = 4 * lane + j < n ? sum[4 * lane + j] : 0.0;
         own += x[j];
     }
-    double incl = own;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double up = __shfl_up(incl, o);
-        incl += lane >= o ? up : 0.0;
-    }
-    const double whole = __shfl(incl, 63);
+    const double incl = lanes_scan(own);
+    const double whole = lane_value(incl, 63);
     if (!(target < whole)) target = whole * (1.0 - 0x1p-40);
     const uint64_t some = __ballot(own > 0.0), hit = __ballot(own > 0.0 && target < incl);
     if (!some) return 0;
     const int f = hit ? __builtin_ctzll(hit) : 63 - __builtin_clzll(some);
-    double run = f > 0 ? __shfl(incl, f - 1) : 0.0;
+    double run = f > 0 ? lane_value(incl, f - 1) : 0.0;
     int at = -1, last = 0;
     double before = run;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const double y = __shfl(x[j], f);
+        const double y = lane_value(x[j], f);
         if (at < 0 && y > 0.0) {
             last = 4 * f + j;
             before = run;
@@ -273,41 +282,52 @@ __device__ __forceinline__ int find_prefix(const double* sum, int n, double& tar
     return at >= 0 ? at : last;
 }
 
-// Elements of lane run `i` of a segment (vectors v0 .. v1 - 1 and, in the first and
-// last segment, the row's ends): `len` vectors each, in order.
+// First element of run `i` of a segment: its lanes take `len` vectors each, in
+// order, the row's ends go to the first and last run.
 template <bool BF16>
-__device__ __forceinline__ int run_first(const RowCut<BF16>& cut, int seg, int nseg, int len, int i) {
-    if (i == 0) return cut.first(seg, nseg);
-    if (i == kWG) return cut.first(seg + 1, nseg);
-    return cut.head + min(cut.first_vec(seg, nseg) + i * len, cut.first_vec(seg + 1, nseg)) * RowCut<BF16>::kE;
+__device__ __forceinline__ int run_first(const RowCut<BF16>& cut, int seg, int len, int i) {
+    if (i == 0) return cut.first(seg);
+    if (i == kWG) return cut.first(seg + 1);
+    return cut.head + min(cut.first_vec(seg) + i * len, cut.first_vec(seg + 1)) * RowCut<BF16>::kE;
 }
 
-// The sum of a run's weights in fp64.
+// The sum of a thread's share of a segment's weights in fp64: len vectors from
+// `first` on, `step` apart (1: a run of its own, kWG: the workgroup side by side),
+// four at a time with the next four on their way; the row's ends to the first and
+// last thread, as runs have them.
 template <bool BF16, int KIND>
-__device__ __forceinline__ double run_sum(const char* rp, const RowCut<BF16>& cut, int seg, int nseg, int len, int i,
-                                          float m, double c64) {
-    constexpr int E = RowCut<BF16>::kE, SZ = RowCut<BF16>::kSz;
+__device__ __forceinline__ double share_sum(const char* rp, const RowCut<BF16>& cut, int seg, int len, int first,
+                                            int step, const Weights<KIND>& weight) {
+    constexpr int E = RowCut<BF16>::kE, SZ = RowCut<BF16>::kSz, U = 4;
+    const int tid = threadIdx.x;
     const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(rp + (size_t)cut.head * SZ);
-    const int v1 = cut.first_vec(seg + 1, nseg);
-    const int a = min(cut.first_vec(seg, nseg) + i * len, v1), b = min(a + len, v1);
+    const int v1 = cut.first_vec(seg + 1), v0 = cut.first_vec(seg) + first;
     double s = 0.0;
-    for (int v = a; v < b; v += 2) {
-        const bool two = v + 1 < b;
-        const u32x4_t w0 = vp[v], w1 = vp[two ? v + 1 : v];
-        float x[E];
-        unpack16<BF16>(w0, x);
+    if (v0 < v1) {
+        u32x4_t next[U];
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += weight64<KIND>(x[e], m, c64);
-        if (two) {
-            unpack16<BF16>(w1, x);
+        for (int u = 0; u < U; ++u) next[u] = vp[min(v0 + u * step, v1 - 1)];
+        for (int i = 0; i < len; i += U) {
+            u32x4_t now[U];
 #pragma unroll
-            for (int e = 0; e < E; ++e) s += weight64<KIND>(x[e], m, c64);
+            for (int u = 0; u < U; ++u) {
+                now[u] = next[u];
+                next[u] = vp[min(v0 + (i + U + u) * step, v1 - 1)];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i + u >= len || v0 + (i + u) * step >= v1) break;
+                float x[E];
+                unpack16<BF16>(now[u], x);
+#pragma unroll
+                for (int e = 0; e < E; ++e) s += weight(x[e]);
+            }
         }
     }
-    if (i == 0 && seg == 0)
-        for (int e = 0; e < cut.head; ++e) s += weight64<KIND>(row_value<BF16>(rp, e), m, c64);
-    if (i == kWG - 1 && seg == nseg - 1)
-        for (int e = cut.head + cut.nv * E; e < cut.V; ++e) s += weight64<KIND>(row_value<BF16>(rp, e), m, c64);
+    if (tid == 0 && seg == 0)
+        for (int e = 0; e < cut.head; ++e) s += weight(row_value<BF16>(rp, e));
+    if (tid == kWG - 1 && seg == cut.nseg - 1)
+        for (int e = cut.head + cut.nv * E; e < cut.V; ++e) s += weight(row_value<BF16>(rp, e));
     return s;
 }
 
@@ -324,37 +344,57 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
 
     // 1. Every row's maximum and sum from its segments (a power of two of them: the
     // lanes of a wave take several rows at once), and the draft's probability of
-    // each drafted token: all of the loads side by side.
-    if (tid < 72) sm.q[tid] = 0;
+    // each drafted token.  All loads go out before any is used.
+    constexpr int kFirst = 2;               // candidates a thread looks at in the first go
+    int32_t cid[kFirst], cdraft[kFirst];
+    float cq[kFirst];
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) {
+        const int x = min(tid + i * kWG, P * K - 1);
+        cid[i] = a.cand[(int64_t)b * P * K + x];
+        cq[i] = a.prob[(int64_t)b * P * K + x];
+        cdraft[i] = a.path[(int64_t)b * P + (int)((uint32_t)x * a.k_inv >> 20)];
+    }
     int32_t draft = -1;
-    float at_draft = 0.f;
+    float at_draft = 0.f, u_draft = 0.f;
     if (w == 0 && lane < P) {
         draft = a.path[(int64_t)b * P + lane];
+        u_draft = a.u[row0 + lane];
         if ((unsigned)draft < (unsigned)a.V) at_draft = row_value<BF16>(rows + (size_t)lane * a.V * SZ, draft);
     }
-    for (int x0 = w * 64; x0 < R * a.nseg; x0 += kWG) {
+    if (tid < 72) sm.q[tid] = 0;
+    fill_exp_table(sm.table);
+    const int parts = R << a.nseg_log;
+    for (int x0 = w * 64; x0 < parts; x0 += kWG) {
         const int x = x0 + lane;
         Lse acc = {KIND == kVerifyProbs ? 0.f : -INFINITY, 0.f};
-        if (x < R * a.nseg) {
-            const uint64_t y = a.part[row0 * a.nseg + x];
+        if (x < parts) {
+            const uint64_t y = a.part[(row0 << a.nseg_log) + x];
             acc = {__uint_as_float((uint32_t)(y >> 32)), __uint_as_float((uint32_t)y)};
         }
-        for (int o = 1; o < a.nseg; o <<= 1) {
-            const Lse y = {__shfl_xor(acc.m, o), __shfl_xor(acc.s, o)};
-            acc = lse_join<KIND>(acc, y, a.c);
+        switch (a.nseg_log) {
+            case 0: break;
+            case 1: acc = lse_lanes<KIND, 2>(acc, a.c); break;
+            case 2: acc = lse_lanes<KIND, 4>(acc, a.c); break;
+            case 3: acc = lse_lanes<KIND, 8>(acc, a.c); break;
+            case 4: acc = lse_lanes<KIND, 16>(acc, a.c); break;
+            case 5: acc = lse_lanes<KIND, 32>(acc, a.c); break;
+            default: acc = lse_lanes<KIND, 64>(acc, a.c); break;
         }
-        if (x < R * a.nseg && x % a.nseg == 0) {
-            sm.m[x / a.nseg] = acc.m;
-            sm.s[x / a.nseg] = acc.s;
+        if (x < parts && (x & ((1 << a.nseg_log) - 1)) == 0) {
+            sm.m[x >> a.nseg_log] = acc.m;
+            sm.s[x >> a.nseg_log] = acc.s;
         }
     }
     __syncthreads();
-    for (int x = tid; x < P * K; x += kWG) {
-        const int t = x / K;
+    // candidates of a row are distinct: one hit at most (the largest otherwise)
+    for (int x = tid, i = 0; x < P * K; x += kWG, ++i) {
         const int64_t at = (int64_t)b * P * K + x;
-        // candidates of a row are distinct: one hit at most (the largest otherwise)
-        const float q = a.prob[at];
-        if (a.cand[at] == a.path[(int64_t)b * P + t]) atomicMax(&sm.q[t], __float_as_uint(fmaxf(q, 0.f)));
+        const int32_t id = i == 0 ? cid[0] : i == 1 ? cid[1] : a.cand[at];
+        const float q = i == 0 ? cq[0] : i == 1 ? cq[1] : a.prob[at];
+        const int t = (int)((uint32_t)x * a.k_inv >> 20);      // x / K
+        const int32_t d = i == 0 ? cdraft[0] : i == 1 ? cdraft[1] : a.path[(int64_t)b * P + t];
+        if (id == d) atomicMax(&sm.q[t], __float_as_uint(fmaxf(q, 0.f)));
     }
     __syncthreads();
 
@@ -365,12 +405,11 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         if (lane < P) {
             double p = 0.0;
             if ((unsigned)draft < (unsigned)a.V) {
-                if (sm.s[lane] > 0.f) p = weight64<KIND>(at_draft, sm.m[lane], a.c64) / (double)sm.s[lane];
+                if (sm.s[lane] > 0.f) p = Weights<KIND>(sm.table, sm.m[lane], a.c64)(at_draft) / (double)sm.s[lane];
             } else if (lane < nd) {
                 atomicOr(a.err, kFlagDraft);
             }
-            float u = a.u[row0 + lane];
-            u = (u >= 0.f) ? fminf(u, 0x1.fffffep-1f) : 0.f;
+            const float u = (u_draft >= 0.f) ? fminf(u_draft, 0x1.fffffep-1f) : 0.f;
             yes = lane < nd && (double)u * (double)__uint_as_float(sm.q[lane]) < p;
             sm.odds[lane] = (float)p;
         }
@@ -384,105 +423,98 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
     __syncthreads();
     const int t = sm.taken;
     const bool refused = t < sm.nd;
-    const float m = sm.m[t];
+    const Weights<KIND> weight(sm.table, sm.m[t], a.c64);
     const bool mass = sm.s[t] > 0.f;
     const char* rp = rows + (size_t)t * a.V * SZ;
-    const RowCut<BF16> cut(rp, a.V);
-    auto run_len = [&](int g) { return (cut.first_vec(g + 1, a.nseg2) - cut.first_vec(g, a.nseg2) + kWG - 1) / kWG; };
+    const RowCut<BF16> cut(rp, a.V, a.per2, a.nseg2);
+    // The row's candidates, for the workgroup that will draw: on their way while
+    // the segment is summed.
+    int id = -1;
+    float at_cand = 0.f, q_cand = 0.f;
+    if (w == 1 && lane < K && refused) {
+        const int64_t at = ((int64_t)b * P + t) * K + lane;
+        id = a.cand[at];
+        q_cand = fmaxf(a.prob[at], 0.f);
+        if ((unsigned)id < (unsigned)a.V) at_cand = row_value<BF16>(rp, id);
+        else atomicOr(a.err, 2u), id = -1;
+    }
 
-    // 3. This segment of row t, a run of it for each lane.
-    double s = run_sum<BF16, KIND>(rp, cut, seg, a.nseg2, run_len(seg), tid, m, a.c64);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    // 3. This segment of row t.
+    const double s = lanes_sum(share_sum<BF16, KIND>(rp, cut, seg, a.len2, tid, kWG, weight));
     if (lane == 0) sm.sums[w] = s;
     __syncthreads();
     if (tid == 0) xstore(a.seg + (int64_t)b * a.nseg2 + seg, sm.sums[0] + sm.sums[1] + sm.sums[2] + sm.sums[3]);
     if (!block_arrive_last(&a.cnt[b], (uint32_t)a.nseg2, &sm.flag)) return;
 
     // 4. The last workgroup draws.  What each candidate loses is min(w, q Z).
-    int id = -1;
-    double loss = 0.0;
-    if (tid < a.nseg2) sm.sums[tid] = xload(a.seg + (int64_t)b * a.nseg2 + tid);
-    if (w == 1 && lane < K && refused) {
-        const int64_t at = ((int64_t)b * P + t) * K + lane;
-        id = a.cand[at];
-        loss = (double)fmaxf(a.prob[at], 0.f);
-        if ((unsigned)id >= (unsigned)a.V) {
-            atomicOr(a.err, 2u);
-            id = -1;
-        }
-    }
-    const float at_cand = id >= 0 ? row_value<BF16>(rp, id) : 0.f;
-    __syncthreads();
-    if (w == 0) {
-        double z = lane < a.nseg2 ? sm.sums[lane] : 0.0;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) z += __shfl_xor(z, o);
-        if (lane == 0) sm.z = z;
-    }
-    __syncthreads();
+    const double mine = w <= 1 && lane < a.nseg2 ? xload(a.seg + (int64_t)b * a.nseg2 + lane) : 0.0;
+    const double z = lanes_sum(mine);       // in waves 0 and 1
     if (w == 1) {
         sm.cid[lane] = id;
-        sm.cut[lane] = id >= 0 ? fmin(weight64<KIND>(at_cand, m, a.c64), loss * sm.z) : 0.0;
+        sm.cut[lane] = id >= 0 ? fmin(weight(at_cand), (double)q_cand * z) : 0.0;
     }
     __syncthreads();
+    // what the candidates among elements e0 .. e1 - 1 lose (places past K are empty)
     auto loss_in = [&](int e0, int e1) {
         double x = 0.0;
-        for (int k = 0; k < K; ++k) x += (sm.cid[k] >= e0 && sm.cid[k] < e1) ? sm.cut[k] : 0.0;
+        for (int k0 = 0; k0 < K; k0 += 8) {
+            int c[8];
+            double y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                c[k] = sm.cid[k0 + k];
+                y[k] = sm.cut[k0 + k];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x += (c[k] >= e0 && c[k] < e1) ? y[k] : 0.0;
+        }
         return x;
     };
     if (w == 0) {
         double left = 0.0;
         if (lane < a.nseg2) {
-            left = sm.sums[lane] - loss_in(cut.first(lane, a.nseg2), cut.first(lane + 1, a.nseg2));
+            left = mine - loss_in(cut.first(lane), cut.first(lane + 1));
             left = left > 0.0 ? left : 0.0;
             sm.sums[lane] = left;
         }
-        double whole = left;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) whole += __shfl_xor(whole, o);
         float u = a.u[row0 + P];
         u = (u >= 0.f) ? fminf(u, 0x1.fffffep-1f) : 0.f;
-        double target = (double)u * whole;
+        double target = (double)u * lanes_sum(left);
         wave_sync();
         const int at = find_prefix(sm.sums, a.nseg2, target);
         if (lane == 0) {
             sm.seg = at;
             sm.target = target;
+            sm.z = z;
         }
     }
     __syncthreads();
-    const int g = sm.seg, len = run_len(g);
+    const int g = sm.seg, len = a.len2;
     {
-        double x = run_sum<BF16, KIND>(rp, cut, g, a.nseg2, len, tid, m, a.c64);
-        x -= loss_in(run_first(cut, g, a.nseg2, len, tid), run_first(cut, g, a.nseg2, len, tid + 1));
+        double x = share_sum<BF16, KIND>(rp, cut, g, len, tid * len, 1, weight);
+        x -= loss_in(run_first(cut, g, len, tid), run_first(cut, g, len, tid + 1));
         sm.sums[tid] = x > 0.0 ? x : 0.0;
     }
     __syncthreads();
     if (w == 0) {
         double target = sm.target;
         const int at = find_prefix(sm.sums, kWG, target);
-        const int i0 = run_first(cut, g, a.nseg2, len, at), i1 = run_first(cut, g, a.nseg2, len, at + 1);
+        const int i0 = run_first(cut, g, len, at), i1 = run_first(cut, g, len, at + 1);
         double run = 0.0;
         int pick = -1, last = -1;
         for (int c0 = i0; c0 < i1 && pick < 0; c0 += 64) {
             const int i = c0 + lane;
             double x = 0.0;
             if (i < i1) {
-                x = weight64<KIND>(row_value<BF16>(rp, i), m, a.c64) - loss_in(i, i + 1);
+                x = weight(row_value<BF16>(rp, i)) - loss_in(i, i + 1);
                 x = x > 0.0 ? x : 0.0;
             }
-            double incl = x;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const double up = __shfl_up(incl, o);
-                incl += lane >= o ? up : 0.0;
-            }
+            const double incl = lanes_scan(x);
             const uint64_t some = __ballot(x > 0.0);
             const uint64_t hit = __ballot(x > 0.0 && target < run + incl);
             if (hit) pick = c0 + __builtin_ctzll(hit);
             if (some) last = c0 + 63 - __builtin_clzll(some);
-            run += __shfl(incl, 63);
+            run += lane_value(incl, 63);
         }
         if (pick < 0) pick = last;
         const bool ok = mass && pick >= 0 && pick < a.V;
@@ -492,7 +524,7 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         }
         if (lane == 0) {
             sm.pick = pick;
-            sm.odds[t] = ok ? (float)(weight64<KIND>(row_value<BF16>(rp, pick), m, a.c64) / sm.z) : 0.f;
+            sm.odds[t] = ok ? (float)(weight(row_value<BF16>(rp, pick)) / sm.z) : 0.f;
             a.out_len[b] = t + 1;
         }
     }
@@ -512,7 +544,7 @@ __global__ __launch_bounds__(kWG) void k_verify_best(VerifyArgs a) {
     const int b = (int)blockIdx.x, P = a.P, R = P + 1;
     const int64_t row0 = (int64_t)b * R;
     for (int t = w; t < R; t += kWaves) {
-        uint64_t x = lane < a.nseg ? a.part[(row0 + t) * a.nseg + lane] : 0;
+        uint64_t x = lane < (1 << a.nseg_log) ? a.part[((row0 + t) << a.nseg_log) + lane] : 0;
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) {
             const uint64_t y = __shfl_xor((unsigned long long)x, o);
