@@ -85,8 +85,8 @@ __device__ __forceinline__ void seq_tokens(const PagedKv& kv, int b, int& s0, in
 
 // Tokens before the new ones, such that ctx + n stays inside the page table.
 // Below -n no position is left that sees a key, so there it stops.
-__device__ __forceinline__ int seq_ctx(const PagedKv& kv, int b, int n) {
-    const int ctx = max(kv.ctx[b], -n);
+__device__ __forceinline__ int inside_table(const PagedKv& kv, int ctx, int n) {
+    ctx = max(ctx, -n);
     const int64_t cap = (int64_t)kv.table_width << kv.page_shift;
     if ((int64_t)ctx + n > cap) {
         atomicOr(kv.err, kFlagLength);
@@ -144,7 +144,7 @@ __device__ __forceinline__ LaneSeq lane_seq(const AttnArgs& a, int c0) {
     const int lane = lane_id(), i = c0 + lane;
     if (i < a.kv.B) {
         seq_tokens(a.kv, i, q.s0, q.n);
-        q.ctx = seq_ctx(a.kv, i, q.n);
+        q.ctx = inside_table(a.kv, a.kv.ctx[i], q.n);
         q.blocks = (int)((unsigned)(q.n * a.G + a.bm - 1) / (unsigned)a.bm);
     }
     if (a.whole) {

@@ -321,8 +321,17 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
     a.interleaved = interleaved ? 1 : 0;
     a.eps = eps;
     return with_type(kv, [&](auto bf16, auto d) {
-        hipLaunchKernelGGL((k_append<decltype(bf16)::value, decltype(d)::value>), dim3((unsigned)kv->N), dim3(256), 0,
-                           stream, a);
+        constexpr int D = decltype(d)::value, heads = 256 / (D / (decltype(bf16)::value ? 8 : 4));
+        const int units = (q ? kv->Hq : 0) + 2 * kv->Hkv;
+        // four tokens a workgroup from sixteen tokens a compute unit on; below one
+        // token a compute unit, a workgroup for every `heads` heads
+        if (kv->N >= 16 * compute_units())
+            hipLaunchKernelGGL((k_append<decltype(bf16)::value, D, 4>), dim3((unsigned)((kv->N + 3) / 4)), dim3(256), 0,
+                               stream, a);
+        else
+            hipLaunchKernelGGL((k_append<decltype(bf16)::value, D, 1>),
+                               dim3((unsigned)kv->N, kv->N <= compute_units() ? (units + heads - 1) / heads : 1),
+                               dim3(256), 0, stream, a);
         return launched("dflash2_kv_append launch");
     });
 }

@@ -50,7 +50,7 @@ struct VerifyArgs {
     int nseg_log, per;          // launch 1: segments of a row (2^nseg_log), vectors of each
     int nseg2, per2, len2;      // launch 2: the same, and vectors of a lane's run
     uint32_t k_inv;             // 2^20 / K + 1: x / K for x < 4096
-    float c, c_low;             // log2(e) / temperature, and what fp32 leaves of it
+    float c, c_low;             // log2(e) / temperature, and what fp32 leaves of it (Factor)
     double c64;
 };
 
@@ -123,23 +123,36 @@ __device__ __forceinline__ void fill_exp_table(double* table) {
     if (threadIdx.x < kExpTable) table[threadIdx.x] = exp2((double)threadIdx.x / kExpTable);
 }
 
+// log2(e) / temperature as two floats: its rounding to one would move every weight
+// the same way.
+struct Factor {
+    float c, low;
+    // 2^(d * factor): the whole octaves apart, so that the argument's rounding is
+    // that of a fraction also where d is large
+    __device__ __forceinline__ float exp2_of(float d) const {
+        const float y = d * c, n = rintf(y);
+        if (!(y > -1000.f)) return 0.f;
+        return ldexpf(__builtin_amdgcn_exp2f((y - n) + (__builtin_fmaf(d, c, -y) + d * low)), (int)n);
+    }
+};
+
 // Running (max, sum) of weights.
 struct Lse {
     float m, s;
 };
 template <int KIND>
-__device__ __forceinline__ Lse lse_join(Lse a, Lse b, float c) {
+__device__ __forceinline__ Lse lse_join(Lse a, Lse b, Factor c) {
     if constexpr (KIND == kVerifyProbs) return {0.f, a.s + b.s};
     const float m = fmaxf(a.m, b.m);
     if (m == -INFINITY) return {m, 0.f};
-    return {m, a.s * __builtin_amdgcn_exp2f((a.m - m) * c) + b.s * __builtin_amdgcn_exp2f((b.m - m) * c)};
+    return {m, a.s * c.exp2_of(a.m - m) + b.s * c.exp2_of(b.m - m)};
 }
 // The same over groups of N lanes: the maximum first, then the sums at it.
 template <int KIND, int N>
-__device__ __forceinline__ Lse lse_lanes(Lse a, float c) {
+__device__ __forceinline__ Lse lse_lanes(Lse a, Factor c) {
     if constexpr (KIND == kVerifyProbs) return {0.f, lanes_sum<N>(a.s)};
     const float m = lanes_max<N>(a.m);
-    const float s = m == -INFINITY ? 0.f : a.s * __builtin_amdgcn_exp2f((a.m - m) * c);
+    const float s = m == -INFINITY ? 0.f : a.s * c.exp2_of(a.m - m);
     return {m, lanes_sum<N>(s)};
 }
 
@@ -157,6 +170,7 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
     const int v0 = cut.first_vec(seg), v1 = cut.first_vec(seg + 1);
     const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(rp + (size_t)cut.head * SZ);
 
+    const Factor factor = {a.c, a.c_low};
     Lse acc = {KIND == kVerifyProbs ? 0.f : -INFINITY, 0.f};
     uint64_t best = 0;
     auto take = [&](const float* x, int n, int at) {
@@ -171,12 +185,10 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
             float m = x[0];
             for (int i = 1; i < n; ++i) m = fmaxf(m, x[i]);
             if (m > acc.m) {
-                acc.s *= __builtin_amdgcn_exp2f((acc.m - m) * a.c);
+                acc.s = acc.m == -INFINITY ? 0.f : acc.s * factor.exp2_of(acc.m - m);
                 acc.m = m;
             }
-            // the difference first, so that the product's rounding is relative to it;
-            // the factor in two parts, or its own rounding would move every weight
-            // the same way
+            // the difference first: the product's rounding is relative to it
             const float mm = acc.m == -INFINITY ? 0.f : acc.m;
             for (int i = 0; i < n; ++i) {
                 const float d = x[i] - mm;
@@ -214,7 +226,7 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
             best = y > best ? y : best;
         }
     } else {
-        acc = lse_lanes<KIND, 64>(acc, a.c);
+        acc = lse_lanes<KIND, 64>(acc, factor);
         best = ((uint64_t)__float_as_uint(acc.m) << 32) | __float_as_uint(acc.s);
     }
     if (lane == 0) red[w] = best;
@@ -226,7 +238,7 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
                 out = red[i] > out ? red[i] : out;
             } else {
                 const Lse y = lse_join<KIND>({__uint_as_float((uint32_t)(out >> 32)), __uint_as_float((uint32_t)out)},
-                                             {__uint_as_float((uint32_t)(red[i] >> 32)), __uint_as_float((uint32_t)red[i])}, a.c);
+                                             {__uint_as_float((uint32_t)(red[i] >> 32)), __uint_as_float((uint32_t)red[i])}, factor);
                 out = ((uint64_t)__float_as_uint(y.m) << 32) | __float_as_uint(y.s);
             }
         }
@@ -365,6 +377,7 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
     if (tid < 72) sm.q[tid] = 0;
     fill_exp_table(sm.table);
     const int parts = R << a.nseg_log;
+    const Factor factor = {a.c, a.c_low};
     for (int x0 = w * 64; x0 < parts; x0 += kWG) {
         const int x = x0 + lane;
         Lse acc = {KIND == kVerifyProbs ? 0.f : -INFINITY, 0.f};
@@ -374,12 +387,12 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         }
         switch (a.nseg_log) {
             case 0: break;
-            case 1: acc = lse_lanes<KIND, 2>(acc, a.c); break;
-            case 2: acc = lse_lanes<KIND, 4>(acc, a.c); break;
-            case 3: acc = lse_lanes<KIND, 8>(acc, a.c); break;
-            case 4: acc = lse_lanes<KIND, 16>(acc, a.c); break;
-            case 5: acc = lse_lanes<KIND, 32>(acc, a.c); break;
-            default: acc = lse_lanes<KIND, 64>(acc, a.c); break;
+            case 1: acc = lse_lanes<KIND, 2>(acc, factor); break;
+            case 2: acc = lse_lanes<KIND, 4>(acc, factor); break;
+            case 3: acc = lse_lanes<KIND, 8>(acc, factor); break;
+            case 4: acc = lse_lanes<KIND, 16>(acc, factor); break;
+            case 5: acc = lse_lanes<KIND, 32>(acc, factor); break;
+            default: acc = lse_lanes<KIND, 64>(acc, factor); break;
         }
         if (x < parts && (x & ((1 << a.nseg_log) - 1)) == 0) {
             sm.m[x >> a.nseg_log] = acc.m;
