@@ -71,7 +71,7 @@ struct AttnArgs {
     int32_t* split;         // [wgs, 8] the block that a workgroup's beginning cuts first
     int64_t q_stride, out_stride;
     int G, causal, window;
-    int bm, kt, gk;         // rows of a block, keys of a tile, keys its start is a multiple of
+    int bm;                 // rows of a block
     int wgs, whole;         // workgroups of the launch; 1: each takes a whole block
     double inv_g;           // 1 / G
     float c;                // scale * log2(e)
@@ -120,14 +120,15 @@ __device__ __forceinline__ int div_g(const AttnArgs& a, int r) {
 struct BlockKeys {
     int t_lo, t_hi, begin, end, origin, tiles;
 };
+template <typename Shape>
 __device__ __forceinline__ BlockKeys block_keys(const AttnArgs& a, int ctx, int n, int j) {
     BlockKeys k;
-    k.t_lo = div_g(a, j * a.bm);
-    k.t_hi = div_g(a, min((j + 1) * a.bm, n * a.G) - 1);
+    k.t_lo = div_g(a, j * Shape::BM);
+    k.t_hi = div_g(a, min((j + 1) * Shape::BM, n * a.G) - 1);
     k.end = max(a.causal ? ctx + k.t_hi + 1 : ctx + n, 0);
     k.begin = a.window ? max(ctx + k.t_lo + 1 - a.window, 0) : 0;
-    k.origin = k.begin & ~(a.gk - 1);
-    k.tiles = max((int)((unsigned)(k.end - k.origin + a.kt - 1) / (unsigned)a.kt), 1);
+    k.origin = k.begin & ~(Shape::kGroupKeys - 1);
+    k.tiles = max((int)((unsigned)(k.end - k.origin + Shape::KT - 1) / (unsigned)Shape::KT), 1);
     return k;
 }
 
@@ -139,26 +140,27 @@ constexpr int kLaneBlocks = 4;
 struct LaneSeq {
     int s0, n, ctx, blocks, tiles;
 };
+template <typename Shape>
 __device__ __forceinline__ LaneSeq lane_seq(const AttnArgs& a, int c0) {
     LaneSeq q = {0, 0, 0, 0, 0};
     const int lane = lane_id(), i = c0 + lane;
     if (i < a.kv.B) {
         seq_tokens(a.kv, i, q.s0, q.n);
         q.ctx = inside_table(a.kv, a.kv.ctx[i], q.n);
-        q.blocks = (int)((unsigned)(q.n * a.G + a.bm - 1) / (unsigned)a.bm);
+        q.blocks = (int)((unsigned)(q.n * a.G + Shape::BM - 1) / (unsigned)Shape::BM);
     }
     if (a.whole) {
         q.tiles = q.blocks;
         return q;
     }
     if (q.blocks <= kLaneBlocks)
-        for (int j = 0; j < q.blocks; ++j) q.tiles += block_keys(a, q.ctx, q.n, j).tiles;
+        for (int j = 0; j < q.blocks; ++j) q.tiles += block_keys<Shape>(a, q.ctx, q.n, j).tiles;
     for (uint64_t big = __ballot(q.blocks > kLaneBlocks); big; big &= big - 1) {
         const int f = __builtin_ctzll(big);
         const int ctx = __builtin_amdgcn_readlane(q.ctx, f), n = __builtin_amdgcn_readlane(q.n, f);
         const int blocks = __builtin_amdgcn_readlane(q.blocks, f);
         int sum = 0;
-        for (int j = lane; j < blocks; j += 64) sum += block_keys(a, ctx, n, j).tiles;
+        for (int j = lane; j < blocks; j += 64) sum += block_keys<Shape>(a, ctx, n, j).tiles;
         sum = __builtin_amdgcn_readlane(lanes_scan(sum), 63);
         if (lane == f) q.tiles = sum;
     }
@@ -176,11 +178,12 @@ struct Cut {
                           : more + (int)((unsigned)(g - longer) / (unsigned)each);
     }
 };
+template <typename Shape>
 __device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
     Cut c;
     c.head_tiles = 0;
     for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
-        q = lane_seq(a, c0);
+        q = lane_seq<Shape>(a, c0);
         c.head_tiles += __builtin_amdgcn_readlane(lanes_scan(q.tiles), 63);
     }
     const int all = c.head_tiles * a.kv.Hkv;
@@ -197,10 +200,11 @@ struct Place {
 };
 // The block that has tile g of a head.  q: the lanes' sequences if there are no
 // more than 64.
+template <typename Shape>
 __device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, int g, Place& p) {
     int before = 0;
     for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
-        if (a.kv.B > 64) q = lane_seq(a, c0);
+        if (a.kv.B > 64) q = lane_seq<Shape>(a, c0);
         const int incl = lanes_scan(q.tiles);
         const uint64_t hit = __ballot(before + incl > g);
         if (hit) {
@@ -219,7 +223,7 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, int g, 
             } else if (p.blocks > 1) {
                 for (int j0 = 0; j0 < p.blocks; j0 += 64) {
                     const int j = j0 + lane_id();
-                    const int own = j < p.blocks ? block_keys(a, p.ctx, p.n, j).tiles : 0;
+                    const int own = j < p.blocks ? block_keys<Shape>(a, p.ctx, p.n, j).tiles : 0;
                     const int sum = lanes_scan(own);
                     const uint64_t here = __ballot(p.first + sum > g);
                     if (here) {
@@ -231,7 +235,7 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, int g, 
                     p.first += __builtin_amdgcn_readlane(sum, 63);
                 }
             }
-            p.k = block_keys(a, p.ctx, p.n, p.j);
+            p.k = block_keys<Shape>(a, p.ctx, p.n, p.j);
             return true;
         }
         before += __builtin_amdgcn_readlane(incl, 63);
@@ -387,7 +391,7 @@ struct AttnShape {
     static constexpr int kGroupKeys = kGroup * (64 / Tile::kChunks);
     // loads that may be in flight while the oldest stage is complete
     static constexpr int kAhead = (NS - 2) * 2 * kLoads;
-    static constexpr int kMergeBytes = WK > 1 ? kWaves * 32 * D * 4 + kWaves * 256 : 0;
+    static constexpr int kMergeBytes = WK > 1 ? kWaves * (32 * D * 4 + 256) + BM * 8 : 0;
     static constexpr int kLds = NS * kStage > kMergeBytes ? NS * kStage : kMergeBytes;   // tiles, or the merge
     static constexpr int kAllLds = kLds + 4 * kPageIds;
     static_assert(kTileBytes % (1024 * kWaves) == 0, "every wave brings whole loads");
@@ -427,7 +431,7 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
     // XCD take neighbouring stretches.  Whole blocks: neighbouring workgroups take
     // different heads, so that with eight of them an XCD keeps one head's keys.
     LaneSeq seqs;
-    const Cut cut = cut_work(a, seqs);
+    const Cut cut = cut_work<Shape>(a, seqs);
     int wg = blockIdx.x;
     if (!a.whole && cut.wgs % 8 == 0 && cut.wgs == (int)gridDim.x)
         wg = (int)(blockIdx.x % 8) * (cut.wgs / 8) + (int)(blockIdx.x / 8);
@@ -443,15 +447,15 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
     while (g < stop) {
     if (a.whole) {
         h = g % kv.Hkv;
-        if (!find_place(a, seqs, g / kv.Hkv, at)) return;
+        if (!find_place<Shape>(a, seqs, g / kv.Hkv, at)) return;
         at.first = g - h * cut.head_tiles;      // the block is the whole stretch
     } else if (at.j + 1 < at.blocks) {
         at.first += at.k.tiles;         // the next block of the sequence
         ++at.j;
-        at.k = block_keys(a, at.ctx, at.n, at.j);
+        at.k = block_keys<Shape>(a, at.ctx, at.n, at.j);
     } else {
         h = (int)((unsigned)g / (unsigned)cut.head_tiles);
-        if (!find_place(a, seqs, g - h * cut.head_tiles, at)) return;
+        if (!find_place<Shape>(a, seqs, g - h * cut.head_tiles, at)) return;
     }
     // the same in every lane; said so, they live in scalar registers
     const auto uni = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
@@ -744,10 +748,14 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
         l = lower + upper;
     }
 
+    const int part0 = 2 * wg + (tile0 == 0 ? 1 : 0);    // where a part goes
     if constexpr (WK > 1) {
-        // The groups' results meet in LDS: statistics first, then each wave's
-        // output scaled to the common maximum, summed by group 0.
+        // The groups' results meet in LDS: each wave's output scaled to the rows' common
+        // maximum, then summed and written row by row by all threads.  (Short code,
+        // not unrolled: code that runs once costs its fetch, 4 us of it here with
+        // everything in registers.)
         float* st = reinterpret_cast<float*>(lds + Shape::kWaves * 32 * D * 4);
+        float* joint = st + Shape::kWaves * 64;         // of each row of the block: maximum, sum
         __syncthreads();
         if (half == 0) {
             st[w * 64 + col] = m;
@@ -764,33 +772,42 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
         }
         const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mg);
         f32x4_t* mine = reinterpret_cast<f32x4_t*>(lds + w * 32 * D * 4);
-        if (wk > 0) {
-#pragma unroll
-            for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    mine[col * (D / 4) + ((8 * d + 2 * v + half) ^ (col & 15))] =
-                        (f32x4_t){o[d][4 * v] * f, o[d][4 * v + 1] * f, o[d][4 * v + 2] * f, o[d][4 * v + 3] * f};
-        }
-        __syncthreads();
-        if (wk > 0) continue;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
+            for (int v = 0; v < 4; ++v)
+                mine[col * (D / 4) + ((8 * d + 2 * v + half) ^ (col & 15))] =
+                    (f32x4_t){o[d][4 * v] * f, o[d][4 * v + 1] * f, o[d][4 * v + 2] * f, o[d][4 * v + 3] * f};
+        if (wk == 0 && half == 0) {
+            joint[2 * (wr * 32 + col)] = mg;
+            joint[2 * (wr * 32 + col) + 1] = lg;
+        }
+        __syncthreads();
+        const int live = min(BM, M - r0);
+#pragma unroll 1
+        for (int x = threadIdx.x; x < live * (D / 4); x += Shape::kThreads) {
+            const int row = x / (D / 4), c = x % (D / 4), wrow = row / 32, wcol = row % 32;
+            f32x4_t y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[d][4 * v + e] *= f;
-#pragma unroll
-                for (int x = 1; x < WK; ++x) {
-                    const f32x4_t y = reinterpret_cast<const f32x4_t*>(lds + (x * WR + wr) * 32 * D * 4)
-                        [col * (D / 4) + ((8 * d + 2 * v + half) ^ (col & 15))];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[d][4 * v + e] += y[e];
+            for (int k = 0; k < WK; ++k)
+                y += reinterpret_cast<const f32x4_t*>(lds + (k * WR + wrow) * 32 * D * 4)[wcol * (D / 4) + (c ^ (wcol & 15))];
+            const float lr = joint[2 * row + 1];
+            if (whole) {
+                const float inv = lr > 0.f ? 1.f / lr : (lr == 0.f ? 0.f : lr);
+                const int rr = r0 + row, tt = div_g(a, rr);
+                const float out[4] = {y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv};
+                store4<BF16>(a.out, (int64_t)(s0 + tt) * a.out_stride + (int64_t)(head_kv * a.G + rr - tt * a.G) * D + 4 * c, out);
+            } else {
+                const int64_t prow = (int64_t)part0 * BM + row;
+                const float out[4] = {y[0], y[1], y[2], y[3]};
+                store4<false>(a.part, prow * D + 4 * c, out);
+                if (c == 0) {
+                    a.stat[2 * prow] = joint[2 * row];
+                    a.stat[2 * prow + 1] = lr;
                 }
             }
-        m = mg;
-        l = lg;
-    }
+        }
+    } else {
     if (r >= M) continue;
     if (whole) {
         // a row that sees nothing gives zeros
@@ -805,7 +822,7 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
                 store4<BF16>(a.out, to + 32 * d + 8 * v + 4 * half, y);
             }
     } else {
-        const int64_t prow = (int64_t)(2 * wg + (tile0 == 0 ? 1 : 0)) * BM + wr * 32 + col;
+        const int64_t prow = (int64_t)part0 * BM + wr * 32 + col;
         if (half == 0) {
             a.stat[2 * prow] = m;
             a.stat[2 * prow + 1] = l;
@@ -817,6 +834,7 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
                 const float y[4] = {o[d][4 * v], o[d][4 * v + 1], o[d][4 * v + 2], o[d][4 * v + 3]};
                 store4<false>(a.part, prow * D + 32 * d + 8 * v + 4 * half, y);
             }
+    }
     }
     }
 }

@@ -262,8 +262,6 @@ df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_
     a.causal = causal ? 1 : 0;
     a.window = window;
     a.bm = pl.bm;
-    a.kt = pl.kt;
-    a.gk = pl.gk;
     a.wgs = pl.wgs;
     a.whole = pl.whole;
     a.inv_g = 1.0 / a.G;
