@@ -343,14 +343,15 @@ namespace {
 
 struct VerifyPlan {
     int nseg = 1, nseg_log = 0, per = 1;
-    int nseg2 = 1, per2 = 1, len2 = 1;
-    size_t off_seg = 0, off_cnt = 0, bytes = 0;
+    int nseg2 = 1, per2 = 1, chunks2 = 1, rounds2 = 1;
+    size_t off_seg = 0, off_chunk = 0, off_cnt = 0, bytes = 0;
 };
 
 // Segments of a row in launch 1: about eight workgroups a compute unit over all
 // rows, none under 4 KB, a power of two (launch 2 takes several rows a wave).
 // Segments of the one row that a sequence's draw reads: 4096 elements, 16 for
-// each lane, or more where that would be more workgroups than run at once.
+// each lane, or more where that would be more workgroups than run at once; up to
+// 64 chunks for each of a segment's four waves.
 VerifyPlan plan_verify(const df2_verify_dims* d) {
     VerifyPlan pl;
     const int64_t rows = (int64_t)d->B * (d->P + 1), cus = compute_units();
@@ -364,9 +365,12 @@ VerifyPlan plan_verify(const df2_verify_dims* d) {
     const int vectors = d->V / (d->dtype == DF2_BF16 ? 8 : 4);      // one less in some rows that start unaligned
     pl.per = std::max(1, (vectors + pl.nseg - 1) / pl.nseg);
     pl.per2 = std::max(1, (vectors + pl.nseg2 - 1) / pl.nseg2);
-    pl.len2 = (pl.per2 + kWG - 1) / kWG;
+    const int rounds = (pl.per2 + kWG - 1) / kWG;
+    pl.rounds2 = (rounds + 63) / 64;
+    pl.chunks2 = (rounds + pl.rounds2 - 1) / pl.rounds2;
     pl.off_seg = (size_t)rows * pl.nseg * 8;
-    pl.off_cnt = pl.off_seg + (size_t)d->B * pl.nseg2 * 8;
+    pl.off_chunk = pl.off_seg + (size_t)d->B * pl.nseg2 * 8;
+    pl.off_cnt = pl.off_chunk + (size_t)d->B * pl.nseg2 * kWaves * pl.chunks2 * 8;
     pl.bytes = (pl.off_cnt + (size_t)d->B * 4 + 15) / 16 * 16;
     return pl;
 }
@@ -420,8 +424,8 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
     clear_error();
     df2_status st = check_verify(dims);
     if (st != DF2_OK) return st;
-    if (!(temperature >= 0.f) || !std::isfinite(temperature))
-        return fail_with(DF2_EINVAL, "temperature must be >= 0 and finite");
+    if (!(temperature >= 0.f) || temperature > 1e30f)
+        return fail_with(DF2_EINVAL, "temperature must be in [0, 1e30]");
     const bool best = temperature == 0.f;
     const double c64 = best ? 0.0 : 1.4426950408889634 / (double)temperature;
     if (c64 > 3.0e38) return fail_with(DF2_EINVAL, "temperature too small (1 / temperature overflows fp32)");
@@ -452,6 +456,7 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
     a.out_prob = out_prob;
     a.part = reinterpret_cast<uint64_t*>(ws);
     a.seg = reinterpret_cast<double*>(ws + pl.off_seg);
+    a.chunk = reinterpret_cast<double*>(ws + pl.off_chunk);
     a.cnt = reinterpret_cast<uint32_t*>(ws + pl.off_cnt);
     a.B = dims->B;
     a.P = dims->P;
@@ -461,10 +466,12 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
     a.per = pl.per;
     a.nseg2 = pl.nseg2;
     a.per2 = pl.per2;
-    a.len2 = pl.len2;
+    a.chunks2 = pl.chunks2;
+    a.rounds2 = pl.rounds2;
     a.k_inv = (1u << 20) / (uint32_t)dims->K + 1;
     a.c = (float)c64;
     a.c_low = (float)(c64 - (double)a.c);
+    a.d_min = best ? 0.f : (float)(-1000.0 / c64);
     a.c64 = c64;
     return dims->dtype == DF2_BF16 ? launch_verify<true>(dims, best, pl, a, stream)
                                    : launch_verify<false>(dims, best, pl, a, stream);

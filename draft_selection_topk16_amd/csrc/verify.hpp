@@ -17,8 +17,8 @@
 // that the draw needs, whose place the partial sums decide: its weights in
 // fp64, because the drawn index must not depend on how sums were rounded (151
 // thousand boundaries stand an fp32 rounding apart from a uniform now and
-// then); each workgroup sums a segment, and the last to finish picks the
-// segment, then a lane's run of it, then the token.
+// then); each workgroup sums the chunks of a segment, and the last to finish picks
+// the segment, then the chunk, and goes through that one's few hundred elements.
 #pragma once
 
 #include "common.hpp"
@@ -44,13 +44,16 @@ struct VerifyArgs {
     float* out_prob;            // [B, P + 1]
     uint64_t* part;             // [B * (P + 1), nseg] (max, sum) or best word of a segment
     double* seg;                // [B, nseg2] fp64 sums of the drawn row's segments
+    double* chunk;              // [B, nseg2, 4 * chunks2] and of their chunks
     uint32_t* cnt;              // [B] arrivals, zeroed by launch 1
     uint32_t* err;
     int B, P, V, K;
     int nseg_log, per;          // launch 1: segments of a row (2^nseg_log), vectors of each
-    int nseg2, per2, len2;      // launch 2: the same, and vectors of a lane's run
+    int nseg2, per2;            // launch 2: the same
+    int chunks2, rounds2;       // chunks of a wave, rounds of 64 vectors in a chunk
     uint32_t k_inv;             // 2^20 / K + 1: x / K for x < 4096
     float c, c_low;             // log2(e) / temperature, and what fp32 leaves of it (Factor)
+    float d_min;                // -1000 / c: logits this far under the maximum weigh nothing
     double c64;
 };
 
@@ -188,12 +191,23 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
                 acc.s = acc.m == -INFINITY ? 0.f : acc.s * factor.exp2_of(acc.m - m);
                 acc.m = m;
             }
-            // the difference first: the product's rounding is relative to it
+            // The difference first: the product's rounding is relative to it.  It stops
+            // at d_min: -inf times the factor's two parts would be NaN.
             const float mm = acc.m == -INFINITY ? 0.f : acc.m;
-            for (int i = 0; i < n; ++i) {
-                const float d = x[i] - mm;
-                acc.s += __builtin_amdgcn_exp2f(__builtin_fmaf(d, a.c, d * a.c_low));
+            float y[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                y[i] = 0.f;
+                if (i >= n) continue;
+                const float d = fmaxf(x[i] - mm, a.d_min);
+                y[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(d, a.c, d * a.c_low));
             }
+            // pairs first: an eighth of the roundings at the size of the sum
+#pragma unroll
+            for (int i = E / 2; i > 0; i /= 2)
+#pragma unroll
+                for (int k = 0; k < i; ++k) y[k] += y[k + i];
+            acc.s += y[0];
         }
     };
     for (int v = v0 + tid; v < v1; v += kWG * U) {
@@ -294,53 +308,65 @@ __device__ __forceinline__ int find_prefix(const double* sum, int n, double& tar
     return at >= 0 ? at : last;
 }
 
-// First element of run `i` of a segment: its lanes take `len` vectors each, in
-// order, the row's ends go to the first and last run.
+// First element of chunk i of a segment; the row's ends go to its first and last.
 template <bool BF16>
-__device__ __forceinline__ int run_first(const RowCut<BF16>& cut, int seg, int len, int i) {
+__device__ __forceinline__ int chunk_first(const RowCut<BF16>& cut, int seg, int vectors, int chunks, int i) {
     if (i == 0) return cut.first(seg);
-    if (i == kWG) return cut.first(seg + 1);
-    return cut.head + min(cut.first_vec(seg) + i * len, cut.first_vec(seg + 1)) * RowCut<BF16>::kE;
+    if (i == chunks) return cut.first(seg + 1);
+    return cut.head + min(cut.first_vec(seg) + i * vectors, cut.first_vec(seg + 1)) * RowCut<BF16>::kE;
 }
 
-// The sum of a thread's share of a segment's weights in fp64: len vectors from
-// `first` on, `step` apart (1: a run of its own, kWG: the workgroup side by side),
-// four at a time with the next four on their way; the row's ends to the first and
-// last thread, as runs have them.
+// A wave's chunks of a segment, `chunks` of them, each `rounds` times 64 vectors side
+// by side: their weights summed in fp64, left in out, the whole returned (the same
+// in every lane).  Four loads at a time, the next four on their way.
 template <bool BF16, int KIND>
-__device__ __forceinline__ double share_sum(const char* rp, const RowCut<BF16>& cut, int seg, int len, int first,
-                                            int step, const Weights<KIND>& weight) {
+__device__ __forceinline__ double chunk_sums(const char* rp, const RowCut<BF16>& cut, int seg, int chunks, int rounds,
+                                             const Weights<KIND>& weight, double* out) {
     constexpr int E = RowCut<BF16>::kE, SZ = RowCut<BF16>::kSz, U = 4;
-    const int tid = threadIdx.x;
+    const int lane = lane_id(), w = wave_id();
     const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(rp + (size_t)cut.head * SZ);
-    const int v1 = cut.first_vec(seg + 1), v0 = cut.first_vec(seg) + first;
-    double s = 0.0;
-    if (v0 < v1) {
-        u32x4_t next[U];
+    const int v1 = cut.first_vec(seg + 1), v0 = cut.first_vec(seg) + w * chunks * rounds * 64 + lane;
+    const int all = chunks * rounds;
+    double s = 0.0, whole = 0.0;
+    int in_chunk = 0;
+    if (w == 0 && seg == 0 && lane < cut.head) s = weight(row_value<BF16>(rp, lane));
+    const bool vectors = cut.first_vec(seg) < v1;
+    u32x4_t next[U];
+    if (vectors) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) next[u] = vp[min(v0 + u * step, v1 - 1)];
-        for (int i = 0; i < len; i += U) {
-            u32x4_t now[U];
+        for (int u = 0; u < U; ++u) next[u] = vp[min(v0 + u * 64, v1 - 1)];
+    }
+    for (int i = 0; i < all; i += U) {
+        u32x4_t now[U];
+        if (vectors) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 now[u] = next[u];
-                next[u] = vp[min(v0 + (i + U + u) * step, v1 - 1)];
+                next[u] = vp[min(v0 + (i + U + u) * 64, v1 - 1)];
             }
+        }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i + u >= len || v0 + (i + u) * step >= v1) break;
+        for (int u = 0; u < U; ++u) {
+            if (i + u >= all) break;
+            if (v0 + (i + u) * 64 < v1) {
                 float x[E];
                 unpack16<BF16>(now[u], x);
 #pragma unroll
                 for (int e = 0; e < E; ++e) s += weight(x[e]);
             }
+            if (++in_chunk < rounds) continue;
+            // the chunk is complete
+            const int tail = cut.head + cut.nv * E + lane;
+            if (i + u == all - 1 && w == kWaves - 1 && seg == cut.nseg - 1 && tail < cut.V)
+                s += weight(row_value<BF16>(rp, tail));
+            s = lanes_sum(s);
+            if (lane == 0) xstore(out + w * chunks + (i + u) / rounds, s);
+            whole += s;
+            s = 0.0;
+            in_chunk = 0;
         }
     }
-    if (tid == 0 && seg == 0)
-        for (int e = 0; e < cut.head; ++e) s += weight(row_value<BF16>(rp, e));
-    if (tid == kWG - 1 && seg == cut.nseg - 1)
-        for (int e = cut.head + cut.nv * E; e < cut.V; ++e) s += weight(row_value<BF16>(rp, e));
-    return s;
+    return whole;
 }
 
 // Launch 2 (sampling): nseg2 workgroups a sequence.
@@ -453,7 +479,9 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
     }
 
     // 3. This segment of row t.
-    const double s = lanes_sum(share_sum<BF16, KIND>(rp, cut, seg, a.len2, tid, kWG, weight));
+    const int nch = kWaves * a.chunks2;
+    double* chunk = a.chunk + ((int64_t)b * a.nseg2 + seg) * nch;
+    const double s = chunk_sums<BF16, KIND>(rp, cut, seg, a.chunks2, a.rounds2, weight, chunk);
     if (lane == 0) sm.sums[w] = s;
     __syncthreads();
     if (tid == 0) xstore(a.seg + (int64_t)b * a.nseg2 + seg, sm.sums[0] + sm.sums[1] + sm.sums[2] + sm.sums[3]);
@@ -502,34 +530,77 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         }
     }
     __syncthreads();
-    const int g = sm.seg, len = a.len2;
-    {
-        double x = share_sum<BF16, KIND>(rp, cut, g, len, tid * len, 1, weight);
-        x -= loss_in(run_first(cut, g, len, tid), run_first(cut, g, len, tid + 1));
+    const int g = sm.seg, vectors = a.rounds2 * 64;
+    if (tid < nch) {
+        const double x = xload(a.chunk + ((int64_t)b * a.nseg2 + g) * nch + tid) -
+                         loss_in(chunk_first(cut, g, vectors, nch, tid), chunk_first(cut, g, vectors, nch, tid + 1));
         sm.sums[tid] = x > 0.0 ? x : 0.0;
     }
     __syncthreads();
     if (w == 0) {
+        constexpr int E = RowCut<BF16>::kE;
         double target = sm.target;
-        const int at = find_prefix(sm.sums, kWG, target);
-        const int i0 = run_first(cut, g, len, at), i1 = run_first(cut, g, len, at + 1);
-        double run = 0.0;
+        const int at = find_prefix(sm.sums, nch, target);
+        const int e0 = chunk_first(cut, g, vectors, nch, at), e1 = chunk_first(cut, g, vectors, nch, at + 1);
+        const int mine_id = lane < K ? sm.cid[lane] : -1;
+        const uint64_t inside = __ballot(mine_id >= e0 && mine_id < e1);
+        double run = 0.0, odds = 0.0, last_odds = 0.0;
         int pick = -1, last = -1;
-        for (int c0 = i0; c0 < i1 && pick < 0; c0 += 64) {
-            const int i = c0 + lane;
-            double x = 0.0;
-            if (i < i1) {
-                x = weight(row_value<BF16>(rp, i)) - loss_in(i, i + 1);
-                x = x > 0.0 ? x : 0.0;
+        // `own` elements of a lane from `first` on, the lanes in order
+        auto go_through = [&](const float (&x)[E], int first, int own) {
+            double full[E], rest[E], sum = 0.0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) rest[e] = full[e] = e < own ? weight(x[e]) : 0.0;
+            for (uint64_t c = inside; c; c &= c - 1) {
+                const int k = __builtin_ctzll(c), d = sm.cid[k] - first;
+                const double loss = sm.cut[k];
+#pragma unroll
+                for (int e = 0; e < E; ++e) rest[e] = d == e ? fmax(rest[e] - loss, 0.0) : rest[e];
             }
-            const double incl = lanes_scan(x);
-            const uint64_t some = __ballot(x > 0.0);
-            const uint64_t hit = __ballot(x > 0.0 && target < run + incl);
-            if (hit) pick = c0 + __builtin_ctzll(hit);
-            if (some) last = c0 + 63 - __builtin_clzll(some);
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum += rest[e];
+            const double incl = lanes_scan(sum);
+            const uint64_t some = __ballot(sum > 0.0), hit = __ballot(sum > 0.0 && target < run + incl);
+            if (some) {
+                // the lane's element where its running sum passes the target, or its last
+                double acc = run + (incl - sum), p = 0.0;
+                int found = -1, end = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    acc += rest[e];
+                    if (found < 0 && rest[e] > 0.0) {
+                        end = e;
+                        p = full[e];
+                        if (target < acc) found = e;
+                    }
+                }
+                const int f = hit ? __builtin_ctzll(hit) : 63 - __builtin_clzll(some);
+                last = __builtin_amdgcn_readlane(first + end, f);
+                last_odds = lane_value(p, f);
+                if (hit) pick = last;
+            }
             run += lane_value(incl, 63);
+        };
+        auto one = [&](int i, int n) {      // elements i .. i + n - 1, one a lane
+            float x[E] = {};
+            if (lane < n) x[0] = row_value<BF16>(rp, i + lane);
+            go_through(x, i + lane, lane < n ? 1 : 0);
+        };
+        int i = e0;
+        if (i < cut.head) {
+            one(i, min(cut.head, e1) - i);
+            i = cut.head;
         }
-        if (pick < 0) pick = last;
+        const int vec_end = min(e1, cut.head + cut.nv * E);
+        for (; pick < 0 && i < vec_end; i += 64 * E) {
+            const int first = i + lane * E;
+            float x[E] = {};
+            if (first < vec_end) unpack16<BF16>(*reinterpret_cast<const u32x4_t*>(rp + (size_t)first * SZ), x);
+            go_through(x, first, first < vec_end ? E : 0);
+        }
+        if (pick < 0 && vec_end < e1) one(max(vec_end, e0), e1 - max(vec_end, e0));
+        pick = pick < 0 ? last : pick;
+        odds = last_odds;
         const bool ok = mass && pick >= 0 && pick < a.V;
         if (!ok) {
             pick = 0;
@@ -537,7 +608,7 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         }
         if (lane == 0) {
             sm.pick = pick;
-            sm.odds[t] = ok ? (float)(weight(row_value<BF16>(rp, pick)) / sm.z) : 0.f;
+            sm.odds[t] = ok ? (float)(odds / sm.z) : 0.f;
             a.out_len[b] = t + 1;
         }
     }

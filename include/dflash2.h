@@ -528,7 +528,7 @@ typedef struct df2_verify_dims {
  *             without sampling K = 1, the path itself with probability 1
  *   n_draft   [B] int32  drafts in use of each sequence (clamped to [0, P]),
  *             or NULL: P
- *   temperature  >= 0, finite; 0: a draft is accepted while it is the largest
+ *   temperature  >= 0, at most 1e30, 1 / temperature finite in fp32; 0: a draft is accepted while it is the largest
  *             of its row (ties: lower id), and the next token is the largest;
  *             then cand_idx, cand_prob and u may be NULL.  With
  *             DF2_TARGET_PROBS only its being 0 matters.

@@ -398,6 +398,40 @@ def test_verify_masked_vocabulary_and_rows_without_mass():
     check_verify(even, tuple(x[2:3] for x in got))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tau", [0.3, 0.45, 0.7, 0.9, 1.0, 1.1, 1.7, 1e-6, 1e30])
+def test_verify_masked_vocabulary_at_temperatures(dtype, tau):
+    """Rows with -inf logits, whatever the sign of what fp32 leaves of log2(e) over
+    the temperature."""
+    say("verify masked", dtype, tau)
+    c = verify_case(17, F32, 3, 3, 5000, 7)
+    dead = torch.rand(5000, generator=torch.Generator().manual_seed(18)) < 0.5
+    dead[c["cand"].cpu().long().flatten()] = False
+    c["target"][:, :, dead.cuda()] = -float("inf")
+    c["target"] = c["target"].to(dtype)
+    got = df2.verify(c["target"], c["path"], c["cand"], c["prob"], c["u"], temperature=tau)
+    assert df2.device_error() == 0
+    assert bool((got[2] >= 0).all()) and not bool(dead[got[0].cpu().long().clamp(min=0)][got[0].cpu() >= 0].any())
+    if tau >= 0.3:
+        check_verify(c, got, tau)
+
+
+@pytest.mark.parametrize("dtype,V", [(BF, 9000001), (F32, 4194311), (BF, 4095), (F32, 4097), (BF, 262151)])
+def test_verify_draws_at_every_place_of_a_row(dtype, V):
+    """Uniforms spread over the row, its ends among them; rows of odd lengths start at
+    every alignment."""
+    say("verify places", dtype, V)
+    B = 2 if V > 1000000 else 9
+    c = verify_case(V, dtype, B, 2, V, 4)
+    c["u"][:, :2] = 0.0                                  # accepted while p > 0: the draw is from the last row
+    c["u"][:, 2] = torch.linspace(0, 1 - 2.0 ** -24, B)
+    check_verify(c, df2.verify(c["target"], c["path"], c["cand"], c["prob"], c["u"]))
+    c["u"][:, 0] = 1.0                                   # refused mostly: candidates lose weight
+    c["prob"].fill_(0.25)
+    check_verify(c, df2.verify(c["target"], c["path"], c["cand"], c["prob"], c["u"]))
+    assert df2.device_error() == 0
+
+
 def test_verify_ids_outside_the_vocabulary():
     say("verify bad ids")
     c = verify_case(8, BF, 3, 4, 1000, 4)

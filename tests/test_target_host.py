@@ -118,7 +118,7 @@ def test_verify_refusals(lib):
         assert call(VerifyDims(*dims)) == status, dims
         assert msg in lib.dflash2_last_error().decode()
         assert lib.dflash2_verify_workspace(ctypes.byref(VerifyDims(*dims))) == 0
-    for tau in (-1.0, float("nan"), float("inf"), 1e-39):
+    for tau in (-1.0, float("nan"), float("inf"), 1e-39, 2e30):
         assert call(good, tau=tau) == EINVAL
         assert b"temperature" in lib.dflash2_last_error()
     for kw in (dict(t=None), dict(path=None), dict(cand=None), dict(prob=None), dict(u=None), dict(o=(None, FAKE, FAKE)),
