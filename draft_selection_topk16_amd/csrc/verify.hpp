@@ -95,10 +95,10 @@ __device__ __forceinline__ void unpack16(u32x4_t w, float (&x)[BF16 ? 8 : 4]) {
 }
 
 // Weights of a row in fp64.  Logits: 2^y, y = (x - m) log2(e) / temperature, as
-// 2^e * 2^(j / 32) * 2^(f / 32), |f| <= 1/2: the whole part through the exponent
-// field, the 32nds from a table in LDS, the rest by the series of 2^(f / 32), whose
-// first term left out is below 1.3 10^-12.  That is half the fp64 instructions of
-// a series over a whole octave; the pass over a row is bound by them.
+// 2^e * 2^(j / 32) * 2^(f / 32), |f| <= 1/2: the 32nds from a table in LDS, the rest
+// by the series of 2^(f / 32), whose first term left out is below 1.3 10^-12.  That
+// is half the fp64 instructions of a series over a whole octave; the pass over a
+// row is bound by them.
 constexpr int kExpTable = 32;
 template <int KIND>
 struct Weights {
@@ -106,20 +106,43 @@ struct Weights {
     double m, c32;              // the row's maximum, 32 log2(e) / temperature
     __device__ __forceinline__ Weights(const double* t, float m_, double c64) : table(t), m(m_), c32(32.0 * c64) {}
     __device__ __forceinline__ double operator()(float x) const {
-        if constexpr (KIND == kVerifyProbs) return fmax((double)x, 0.0);
-        const double y = ((double)x - m) * c32;         // the difference first: it is exact next to m
-        const double shifted = y + 0x1.8p52;            // its low word is y to the nearest whole
-        const int n = (int)(uint32_t)(uint64_t)__double_as_longlong(shifted);
-        const double f = y - (shifted - 0x1.8p52);
+        const float one[1] = {x};
+        double w[1];
+        of(one, w);
+        return w[0];
+    }
+    // N of them side by side: one alone waits for each of its steps.
+    template <int N>
+    __device__ __forceinline__ void of(const float (&x)[N], double (&w)[N]) const {
+        if constexpr (KIND == kVerifyProbs) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = fmax((double)x[i], 0.0);
+            return;
+        }
+        double f[N], root[N];
+        int n[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // the difference first: it is exact next to m; stopped where 2^y is 0
+            const double y = fmax(((double)x[i] - m) * c32, -2048.0 * kExpTable);
+            const double shifted = y + 0x1.8p52;        // its low word is y to the nearest whole
+            n[i] = (int)(uint32_t)(uint64_t)__double_as_longlong(shifted);
+            f[i] = y - (shifted - 0x1.8p52);
+            root[i] = table[n[i] & (kExpTable - 1)];
+        }
+        __builtin_amdgcn_sched_barrier(0);
         constexpr double k = 0.69314718055994531 / kExpTable;
-        double s = k * k * k * k / 24.0;
-        s = fma(s, f, k * k * k / 6.0);
-        s = fma(s, f, k * k / 2.0);
-        s = fma(s, f, k);
-        s = fma(s, f, 1.0);
-        s *= table[n & (kExpTable - 1)];
-        const uint64_t w = (uint64_t)__double_as_longlong(s) + ((uint64_t)(uint32_t)((n >> 5) << 20) << 32);
-        return y > -1000.0 * kExpTable ? __longlong_as_double((long long)w) : 0.0;     // 2^-1000 and less: 0
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = fma(k * k * k * k / 24.0, f[i], k * k * k / 6.0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = fma(w[i], f[i], k * k / 2.0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = fma(w[i], f[i], k);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = fma(w[i], f[i], 1.0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = ldexp(w[i] * root[i], n[i] >> 5);
     }
 };
 __device__ __forceinline__ void fill_exp_table(double* table) {
@@ -351,8 +374,13 @@ __device__ __forceinline__ double chunk_sums(const char* rp, const RowCut<BF16>&
             if (v0 + (i + u) * 64 < v1) {
                 float x[E];
                 unpack16<BF16>(now[u], x);
+                double y[E];
+                weight.of(x, y);
 #pragma unroll
-                for (int e = 0; e < E; ++e) s += weight(x[e]);
+                for (int d = E / 2; d > 0; d /= 2)
+#pragma unroll
+                    for (int e = 0; e < d; ++e) y[e] += y[e + d];
+                s += y[0];
             }
             if (++in_chunk < rounds) continue;
             // the chunk is complete
@@ -549,8 +577,9 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         // `own` elements of a lane from `first` on, the lanes in order
         auto go_through = [&](const float (&x)[E], int first, int own) {
             double full[E], rest[E], sum = 0.0;
+            weight.of(x, full);
 #pragma unroll
-            for (int e = 0; e < E; ++e) rest[e] = full[e] = e < own ? weight(x[e]) : 0.0;
+            for (int e = 0; e < E; ++e) rest[e] = full[e] = e < own ? full[e] : 0.0;
             for (uint64_t c = inside; c; c &= c - 1) {
                 const int k = __builtin_ctzll(c), d = sm.cid[k] - first;
                 const double loss = sm.cut[k];

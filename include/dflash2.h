@@ -528,10 +528,10 @@ typedef struct df2_verify_dims {
  *             without sampling K = 1, the path itself with probability 1
  *   n_draft   [B] int32  drafts in use of each sequence (clamped to [0, P]),
  *             or NULL: P
- *   temperature  >= 0, at most 1e30, 1 / temperature finite in fp32; 0: a draft is accepted while it is the largest
- *             of its row (ties: lower id), and the next token is the largest;
- *             then cand_idx, cand_prob and u may be NULL.  With
- *             DF2_TARGET_PROBS only its being 0 matters.
+ *   temperature  >= 0, at most 1e30, 1 / temperature finite in fp32; 0: a draft
+ *             is accepted while it is the largest of its row (ties: lower id),
+ *             and the next token is the largest; then cand_idx, cand_prob and u
+ *             may be NULL.  With DF2_TARGET_PROBS only its being 0 matters.
  *   u         [B, P + 1] float, clamped into [0, 1)
  *   out_tok   [B, P + 1] int32  accepted drafts, the next token, then -1
  *   out_len   [B] int32         tokens that count: accepted drafts + 1
