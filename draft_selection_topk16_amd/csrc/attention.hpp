@@ -29,6 +29,19 @@
 // A key past the end of the stretch is replaced by its last key and masked:
 // a tile holds nothing but keys that some row of the block may see, so that
 // what else stands in the pages (NaN included) never meets the product.
+//
+// Measured (kernel, then join; head size 128, bf16 unless said):
+//   4 contexts of 65 to 131 thousand tokens, 8 new each, 32 / 8 heads: 249 + 7 us
+//     for 1.61 GB, 6.5 TB/s: a copy of the loads alone takes as long;
+//   32 contexts of 301 to 12007 tokens, 8 new each, 64 / 8 heads: 152 + 10 us for
+//     816 MB, 5.4 TB/s: some 20 us are the start, the parts (33 MB) and the end;
+//   1 new token after 1003, 32 / 8 heads: 7.6 + 3.4 us, latency: 1.9 us to the
+//     cut, 1.5 to the place, 0.8 for page ids, 0.9 for the first tile;
+//   3 drafted blocks in fp32 of head size 64, up to 2049 keys: 9.9 + 4.1 us;
+//   prompt chunks (739 GFLOP): 700 us, 1060 TFLOP/s, where a large library product
+//     reaches 1364.  Nothing alone bounds it: with its products only, it takes 565
+//     us (the clock falls to 2.05 GHz under them), LDS loads add 40, operand reads
+//     60, exponentials 90.
 #pragma once
 
 #include "common.hpp"
@@ -370,7 +383,9 @@ struct AttnTile {
 };
 
 // WR waves of 32 rows, WK groups of them on different keys, KS times 32 keys
-// a wave in each tile, NS stages of tiles in LDS.
+// a wave in each tile, NS stages of tiles in LDS.  More than two stages, with as
+// many bytes in flight, were slower wherever they were tried (one row block on
+// 131 thousand keys: 262 us with three, 349 with five).
 template <bool BF16, int D, int WR, int WK, int KS, int NS>
 __global__ void k_attend(AttnArgs a);
 
@@ -455,7 +470,11 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
         at.k = block_keys<Shape>(a, at.ctx, at.n, at.j);
     } else {
         h = (int)((unsigned)g / (unsigned)cut.head_tiles);
-        if (!find_place<Shape>(a, seqs, g - h * cut.head_tiles, at)) return;
+        if (!find_place<Shape>(a, seqs, g - h * cut.head_tiles, at)) {
+            // only where sequences overlap, by more tokens than there are
+            if (g == start && threadIdx.x == 0) split[0] = -1;
+            return;
+        }
     }
     // the same in every lane; said so, they live in scalar registers
     const auto uni = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
@@ -853,7 +872,8 @@ __global__ __launch_bounds__(256) void k_attend_join(AttnArgs a) {
     __shared__ float lds_m[NG], lds_l[NG];
     const int slice = blockIdx.x % kJoinWgs, boundary = 1 + blockIdx.x / kJoinWgs;
     const int32_t* split = a.split + 8 * boundary;
-    const int w0 = boundary - 1, w1 = split[0], h = split[1], s0 = split[2], r0 = split[3], M = split[4];
+    const int w0 = boundary - 1, w1 = min(split[0], (int)(gridDim.x / kJoinWgs));
+    const int h = split[1], s0 = split[2], r0 = split[3], M = split[4];
     if (w1 < 0) return;
     const int group = threadIdx.x / L, d = (threadIdx.x % L) * 4;
     const int rows = a.bm / kJoinWgs;                   // of this workgroup: 2 to 16

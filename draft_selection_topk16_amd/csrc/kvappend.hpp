@@ -20,6 +20,11 @@
 // D * size / 16 lanes hold a head, 16 bytes each; a rotation's partner comes from
 // the lane that has it.  A workgroup takes one token, or four neighbouring ones
 // where there are enough; with few tokens, several workgroups share one.
+//
+// Measured: 15 thousand tokens of 32 + 2 * 8 heads of 128 in bf16 87 us for 378 MB,
+// 4.3 TB/s, where a large copy reaches 5.1 (eight tokens a workgroup 120 us, one
+// 97); a block of 8 tokens 4.4 us, latency of the loads that follow one another:
+// sequence, page id, row.
 #pragma once
 
 #include "attention.hpp"

@@ -19,6 +19,12 @@
 // thousand boundaries stand an fp32 rounding apart from a uniform now and
 // then); each workgroup sums the chunks of a segment, and the last to finish picks
 // the segment, then the chunk, and goes through that one's few hundred elements.
+//
+// Measured (launch 1 + launch 2, bf16): 64 sequences of 16 rows of 262144 91 + 32 us,
+// launch 1 at 5.9 TB/s; 32 of 8 rows of 151936 17 + 17 us for 78 MB; one of 8 rows
+// 3.6 + 10.8 us.  Launch 2 is a chain of short steps (2.3 us to the decision, 1.7 for
+// the segment, 1.1 to the last arrival, 1.6, 0.8 and 1.9 for segment, chunk and
+// token of one sequence) and, with many sequences, the fp64 weights.
 #pragma once
 
 #include "common.hpp"

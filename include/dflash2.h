@@ -481,14 +481,17 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
  *           counts); a token whose position is negative sees none and gets 0
  *   scale   positive and finite
  *   max_len an upper estimate of ctx_len + n over the batch for the launch
- *           plan, 0: table_width * page_size; results do not depend on its truth
+ *           plan, 0: table_width * page_size.  Only the order in which partial
+ *           sums are added depends on it, so it need not be true.
  *   q, out  token rows of Hq heads (dtype); out must not overlap q
  *   workspace  dflash2_paged_attention_workspace(kv, max_len) bytes (0: may be
  *           NULL), 16-byte aligned
  * Scores, softmax statistics and sums are fp32; bf16 probabilities are
  * rounded to bf16 for the second product.  Keys and values that a token of
  * the batch sees must be finite; whatever else stands in the pages is not
- * used.
+ * used.  The work is counted in tiles of 32 to 128 keys: (N * Hq / Hkv / 32 + B)
+ * * Hkv times the tiles of a whole page table must stay below 2^31
+ * (DF2_EUNSUPPORTED).
  */
 size_t dflash2_paged_attention_workspace(const df2_paged_kv* kv, int32_t max_len);
 df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_t q_stride,

@@ -68,6 +68,9 @@ ATTENTION = [
     ("empty_and_late", BF, 128, 4, 1, 16, [0, 4, 0, 1], [10, 0, 0, 65], True, 0),
     ("before_the_start", BF, 128, 4, 1, 16, [6, 2], [-3, -7], True, 0),
     ("big_page", BF, 128, 4, 2, 1024, [9], [1500], True, 0),
+    ("pages_of_one_token", BF, 128, 8, 2, 1, [3, 1], [5003, 2050], True, 0),
+    ("pages_of_one_token_f32_window", F32, 64, 4, 4, 1, [2, 1], [3500, 1], True, 2500),
+    ("chunk_small_pages", BF, 128, 32, 8, 2, [4100], [300], True, 0),
 ]
 
 
@@ -199,6 +202,8 @@ APPEND = [
     ("no_rotation", BF, 256, 2, 1, 64, [70], [60], 0, False, True),
     ("copy", BF, 64, 2, 1, 16, [3], [14], 0, False, False),
     ("before_the_start", BF, 128, 2, 1, 16, [5], [-2], 128, False, True),
+    ("many", BF, 64, 3, 1, 16, [(37 * i) % 113 for i in range(80)], [(91 * i) % 300 for i in range(80)], 64, False, True),
+    ("many_f32", F32, 128, 2, 2, 8, [2049, 0, 2048, 7], [5, 0, 100000, 70000], 128, True, True),
 ]
 
 
@@ -257,6 +262,17 @@ def test_append_against_fp64(case):
     keep = ~seen[:, None, :, None].expand(k0.shape)
     assert torch.equal(c["k_cache"].cpu()[keep], want_k[keep])
     assert bool((out[sum(new):] == -7.0).all())         # rows that no sequence owns
+
+
+def test_nothing_is_done_for_rows_that_no_sequence_owns():
+    say("no owned rows")
+    c = append_case(5, BF, 128, 4, 2, 16, [0, 0, 0], [10, 0, 31], 128, True, pad=6)
+    k0, v0 = c["k_cache"].clone(), c["v_cache"].clone()
+    out = torch.full_like(c["q"].contiguous(), -7.0)
+    append(c, False, out_q=out)
+    assert torch.equal(c["k_cache"], k0) and torch.equal(c["v_cache"], v0) and bool((out == -7.0).all())
+    df2.paged_attention(c["q"], c["k_cache"], c["v_cache"], c["table"], c["ctx"], c["start"], out=out)
+    assert bool((out == -7.0).all()) and df2.device_error() == 0
 
 
 def test_append_in_place_and_keys_only():
