@@ -107,7 +107,7 @@ def load() -> ctypes.CDLL:
         "dflash2_kv_append": [kvp, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, vp, i32, i32, vp, i64, vp],
         "dflash2_paged_attention": [kvp, vp, i64, ctypes.c_float, i32, i32, i32, vp, i64, vp, ctypes.c_size_t,
                                     vp],
-        "dflash2_verify": [vdp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+        "dflash2_verify": [vdp, vp, vp, vp, vp, vp, ctypes.c_double, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
         "dflash2_plan_override": [ctypes.c_int, i32],
         "dflash2_release": [],
     }

@@ -349,36 +349,57 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
 namespace {
 
 struct VerifyPlan {
+    bool sums = false;          // launch 1 makes every row's chunk sums
     int nseg = 1, nseg_log = 0, per = 1;
     int nseg2 = 1, per2 = 1, chunks2 = 1, rounds2 = 1;
-    size_t off_seg = 0, off_chunk = 0, off_cnt = 0, bytes = 0;
+    size_t off_seg = 0, off_chunk = 0, off_top = 0, off_cnt = 0, bytes = 0;
 };
 
-// Segments of a row in launch 1: about eight workgroups a compute unit over all
-// rows, none under 4 KB, a power of two (launch 2 takes several rows a wave).
-// Segments of the one row that a sequence's draw reads: 4096 elements, 16 for
-// each lane, or more where that would be more workgroups than run at once; up to
-// 64 chunks for each of a segment's four waves.
-VerifyPlan plan_verify(const df2_verify_dims* d) {
+// Few elements: launch 1 makes the fp64 sums of all rows, so that launch 2 is one
+// short step.  Against the other way, both launches, rows of 151936 in bf16, 8 a
+// sequence: 11.7 us and 13.7 at one sequence, 17.7 and 19.6 at 8, 24.5 and 26.5 at
+// 16, 38.9 and 33.4 at 32; of 32000, 64 sequences, 22.2 and 21.7.  Segments of 2048
+// elements, or longer ones where that would be more workgroups than run at once, as
+// far as a workgroup holds them.
+// Else launch 1 takes fp32 sums, about eight workgroups a compute unit over all
+// rows, none under 4 KB, a power of two of them a row (launch 2 takes several rows
+// a wave), and launch 2 goes through the one row that a sequence's draw reads: in
+// segments of 4096 elements, 16 for each lane, or more where that would be more
+// workgroups than run at once; up to 64 chunks for each of a segment's four waves.
+constexpr int64_t kFewElements = 1 << 24;
+VerifyPlan plan_verify(const df2_verify_dims* d, bool best) {
     VerifyPlan pl;
     const int64_t rows = (int64_t)d->B * (d->P + 1), cus = compute_units();
-    const int64_t row_bytes = (int64_t)d->V * (d->dtype == DF2_BF16 ? 2 : 4);
-    while (pl.nseg < kVerifySegs && 2 * pl.nseg * rows <= 8 * cus && 2 * pl.nseg * 4096 <= row_bytes) {
-        pl.nseg *= 2;
-        ++pl.nseg_log;
+    const int per16 = d->dtype == DF2_BF16 ? 8 : 4, vectors = d->V / per16;     // one less in some rows that start unaligned
+    if (!best && rows * d->V <= kFewElements) {
+        const int64_t most = (int64_t)kHold * kWG * per16;
+        int64_t each = 2048;
+        while (each < most && ((d->V + each - 1) / each > kVerifySegs || rows * ((d->V + each - 1) / each) > 8 * cus))
+            each *= 2;
+        pl.nseg2 = (int)((d->V + each - 1) / each);
+        pl.per2 = std::max(1, (vectors + pl.nseg2 - 1) / pl.nseg2);
+        pl.chunks2 = (pl.per2 + kWG - 1) / kWG;
+        pl.sums = pl.nseg2 <= kVerifySegs && pl.chunks2 <= kHold;
     }
-    pl.nseg2 = (int)std::max<int64_t>(1, std::min<int64_t>(
-        {kVerifySegs, (d->V + 4095) / 4096, 2 * cus / d->B}));
-    const int vectors = d->V / (d->dtype == DF2_BF16 ? 8 : 4);      // one less in some rows that start unaligned
-    pl.per = std::max(1, (vectors + pl.nseg - 1) / pl.nseg);
-    pl.per2 = std::max(1, (vectors + pl.nseg2 - 1) / pl.nseg2);
-    const int rounds = (pl.per2 + kWG - 1) / kWG;
-    pl.rounds2 = (rounds + 63) / 64;
-    pl.chunks2 = (rounds + pl.rounds2 - 1) / pl.rounds2;
-    pl.off_seg = (size_t)rows * pl.nseg * 8;
-    pl.off_chunk = pl.off_seg + (size_t)d->B * pl.nseg2 * 8;
-    pl.off_cnt = pl.off_chunk + (size_t)d->B * pl.nseg2 * kWaves * pl.chunks2 * 8;
-    pl.bytes = (pl.off_cnt + (size_t)d->B * 4 + 15) / 16 * 16;
+    if (!pl.sums) {
+        const int64_t row_bytes = (int64_t)d->V * (16 / per16);
+        while (pl.nseg < kVerifySegs && 2 * pl.nseg * rows <= 8 * cus && 2 * pl.nseg * 4096 <= row_bytes) {
+            pl.nseg *= 2;
+            ++pl.nseg_log;
+        }
+        pl.per = std::max(1, (vectors + pl.nseg - 1) / pl.nseg);
+        pl.nseg2 = (int)std::max<int64_t>(1, std::min<int64_t>({kVerifySegs, (d->V + 4095) / 4096, 2 * cus / d->B}));
+        pl.per2 = std::max(1, (vectors + pl.nseg2 - 1) / pl.nseg2);
+        const int rounds = (pl.per2 + kWG - 1) / kWG;
+        pl.rounds2 = (rounds + 63) / 64;
+        pl.chunks2 = (rounds + pl.rounds2 - 1) / pl.rounds2;
+    }
+    const size_t segs = (size_t)(pl.sums ? rows : d->B) * pl.nseg2;
+    pl.off_seg = pl.sums ? 0 : (size_t)rows * pl.nseg * 8;
+    pl.off_chunk = pl.off_seg + segs * 8;
+    pl.off_top = pl.off_chunk + segs * kWaves * pl.chunks2 * 8;
+    pl.off_cnt = pl.off_top + (pl.sums ? segs * 4 : 0);
+    pl.bytes = (pl.off_cnt + (pl.sums ? 0 : (size_t)d->B * 4) + 15) / 16 * 16;
     return pl;
 }
 
@@ -404,14 +425,22 @@ df2_status launch_verify(const df2_verify_dims* d, bool best, const VerifyPlan& 
     if (best) {
         hipLaunchKernelGGL((k_verify_rows<BF16, kVerifyArgmax>), rows, wg, 0, stream, a);
         hipLaunchKernelGGL((k_verify_best<BF16>), dim3((unsigned)d->B), wg, 0, stream, a);
-    } else if (d->kind == DF2_TARGET_PROBS) {
-        hipLaunchKernelGGL((k_verify_rows<BF16, kVerifyProbs>), rows, wg, 0, stream, a);
-        hipLaunchKernelGGL((k_verify_draw<BF16, kVerifyProbs>), draw, wg, 0, stream, a);
-    } else {
-        hipLaunchKernelGGL((k_verify_rows<BF16, kVerifyLogits>), rows, wg, 0, stream, a);
-        hipLaunchKernelGGL((k_verify_draw<BF16, kVerifyLogits>), draw, wg, 0, stream, a);
+        return launched("dflash2_verify launch");
     }
-    return launched("dflash2_verify launch");
+    const auto go = [&](auto kind) {
+        constexpr int KIND = decltype(kind)::value;
+        if (pl.sums) {
+            const dim3 all((unsigned)((int64_t)d->B * (d->P + 1) * pl.nseg2));
+            hipLaunchKernelGGL((k_verify_sums<BF16, KIND>), all, wg, 0, stream, a);
+            hipLaunchKernelGGL((k_verify_pick<BF16, KIND>), dim3((unsigned)d->B), wg, 0, stream, a);
+        } else {
+            hipLaunchKernelGGL((k_verify_rows<BF16, KIND>), rows, wg, 0, stream, a);
+            hipLaunchKernelGGL((k_verify_draw<BF16, KIND>), draw, wg, 0, stream, a);
+        }
+        return launched("dflash2_verify launch");
+    };
+    if (d->kind == DF2_TARGET_PROBS) return go(std::integral_constant<int, kVerifyProbs>());
+    return go(std::integral_constant<int, kVerifyLogits>());
 }
 
 }  // namespace
@@ -421,20 +450,20 @@ extern "C" {
 size_t dflash2_verify_workspace(const df2_verify_dims* dims) {
     clear_error();
     if (check_verify(dims) != DF2_OK || dims->B == 0) return 0;
-    return plan_verify(dims).bytes;
+    return std::max(plan_verify(dims, false).bytes, plan_verify(dims, true).bytes);
 }
 
 df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const int32_t* path,
                           const int32_t* cand_idx, const float* cand_prob, const int32_t* n_draft,
-                          float temperature, const float* u, int32_t* out_tok, int32_t* out_len,
+                          double temperature, const float* u, int32_t* out_tok, int32_t* out_len,
                           float* out_prob, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     clear_error();
     df2_status st = check_verify(dims);
     if (st != DF2_OK) return st;
-    if (!(temperature >= 0.f) || temperature > 1e30f)
+    if (!(temperature >= 0.0) || temperature > 1e30)
         return fail_with(DF2_EINVAL, "temperature must be in [0, 1e30]");
-    const bool best = temperature == 0.f;
-    const double c64 = best ? 0.0 : 1.4426950408889634 / (double)temperature;
+    const bool best = temperature == 0.0;
+    const double c64 = best ? 0.0 : 1.4426950408889634 / temperature;
     if (c64 > 3.0e38) return fail_with(DF2_EINVAL, "temperature too small (1 / temperature overflows fp32)");
     if (dims->B == 0) return DF2_OK;
     if (!target || !path || !out_tok || !out_len || !out_prob) return fail_with(DF2_EINVAL, "NULL pointer argument");
@@ -443,7 +472,7 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
     if (!aligned(path, 4) || !aligned(cand_idx, 4) || !aligned(cand_prob, 4) || !aligned(n_draft, 4) ||
         !aligned(u, 4) || !aligned(out_tok, 4) || !aligned(out_len, 4) || !aligned(out_prob, 4))
         return fail_with(DF2_EINVAL, "arguments must be 4-byte aligned");
-    const VerifyPlan pl = plan_verify(dims);
+    const VerifyPlan pl = plan_verify(dims, best);
     if (!workspace || workspace_bytes < pl.bytes)
         return fail_with(DF2_EINVAL, "workspace of " + std::to_string(workspace ? workspace_bytes : 0) +
                                          " bytes; the call needs " + std::to_string(pl.bytes));
@@ -464,6 +493,7 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
     a.part = reinterpret_cast<uint64_t*>(ws);
     a.seg = reinterpret_cast<double*>(ws + pl.off_seg);
     a.chunk = reinterpret_cast<double*>(ws + pl.off_chunk);
+    a.top = reinterpret_cast<float*>(ws + pl.off_top);
     a.cnt = reinterpret_cast<uint32_t*>(ws + pl.off_cnt);
     a.B = dims->B;
     a.P = dims->P;

@@ -12,19 +12,23 @@
 //   * with every draft accepted, from p_a, a = the number of drafts:
 //     the first v whose running sum exceeds u_P times the whole sum.
 //
-// Launch 1 reads every row once: (max, sum) of each segment in fp32, a maximum
-// per lane with rescaling, so one pass does.  Launch 2 works on the one row a
-// that the draw needs, whose place the partial sums decide: its weights in
-// fp64, because the drawn index must not depend on how sums were rounded (151
-// thousand boundaries stand an fp32 rounding apart from a uniform now and
-// then); each workgroup sums the chunks of a segment, and the last to finish picks
-// the segment, then the chunk, and goes through that one's few hundred elements.
+// A token is drawn from weights in fp64, because the drawn index must not depend on
+// how sums were rounded (151 thousand boundaries stand an fp32 rounding apart from
+// a uniform now and then), by chunks of a few hundred elements: the segment of the
+// row first, then the chunk, then the element.
+//
+// Many rows: launch 1 reads every row once, (max, sum) of each segment in fp32, a
+// maximum per lane with rescaling, so one pass does.  Launch 2 works on the one row
+// that the draw needs, whose place the partial sums decide: each workgroup sums the
+// chunks of a segment, the last to finish draws.  Few rows: launch 1 makes every
+// row's chunk sums in fp64 at once, launch 2 only decides and draws.
 //
 // Measured (launch 1 + launch 2, bf16): 64 sequences of 16 rows of 262144 91 + 32 us,
-// launch 1 at 5.9 TB/s; 32 of 8 rows of 151936 17 + 17 us for 78 MB; one of 8 rows
-// 3.6 + 10.8 us.  Launch 2 is a chain of short steps (2.3 us to the decision, 1.7 for
-// the segment, 1.1 to the last arrival, 1.6, 0.8 and 1.9 for segment, chunk and
-// token of one sequence) and, with many sequences, the fp64 weights.
+// launch 1 at 5.9 TB/s; 32 of 8 rows of 151936 17 + 17 us for 78 MB; one of 8 rows,
+// the second form, 4.8 + 7.3 us (3.6 + 10.8 in the first).  Launch 2 of the first is
+// a chain of short steps (2.3 us to the decision, 1.7 for the segment, 1.1 to the last
+// arrival, 1.6, 0.8 and 1.9 for segment, chunk and token of one sequence) and, with
+// many sequences, the fp64 weights.
 #pragma once
 
 #include "common.hpp"
@@ -51,6 +55,8 @@ struct VerifyArgs {
     uint64_t* part;             // [B * (P + 1), nseg] (max, sum) or best word of a segment
     double* seg;                // [B, nseg2] fp64 sums of the drawn row's segments
     double* chunk;              // [B, nseg2, 4 * chunks2] and of their chunks
+    float* top;                 // few rows: [B * (P + 1), nseg2] maxima of segments, to which
+                                // seg and chunk, then of all rows, are relative
     uint32_t* cnt;              // [B] arrivals, zeroed by launch 1
     uint32_t* err;
     int B, P, V, K;
@@ -290,7 +296,8 @@ __global__ __launch_bounds__(kWG) void k_verify_rows(VerifyArgs a) {
 }
 
 struct VerifyLds {
-    float m[72], s[72];         // maximum and sum of each row (P + 1 <= 65)
+    float m[72];                // maximum and sum of each row (P + 1 <= 65)
+    double s[72];
     uint32_t q[72];             // bits of the draft's probability of each drafted token
     float odds[72];             // p of each drafted token
     int cid[64];                // candidates of the drawn row, and what they lose
@@ -403,86 +410,66 @@ __device__ __forceinline__ double chunk_sums(const char* rp, const RowCut<BF16>&
     return whole;
 }
 
-// Launch 2 (sampling): nseg2 workgroups a sequence.
-template <bool BF16, int KIND>
-__global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
-    constexpr int SZ = RowCut<BF16>::kSz;
-    __shared__ VerifyLds sm;
-    const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
-    const int b = (int)(blockIdx.x / a.nseg2), seg = (int)(blockIdx.x % a.nseg2);
-    const int P = a.P, R = P + 1, K = a.K;
-    const int64_t row0 = (int64_t)b * R;
-    const char* rows = reinterpret_cast<const char*>(a.target) + (size_t)row0 * a.V * SZ;
-
-    // 1. Every row's maximum and sum from its segments (a power of two of them: the
-    // lanes of a wave take several rows at once), and the draft's probability of
-    // each drafted token.  All loads go out before any is used.
-    constexpr int kFirst = 2;               // candidates a thread looks at in the first go
+// What the decision about the drafts needs beside the rows' sums: loaded before
+// those are there.
+constexpr int kFirst = 2;               // candidates a thread looks at in the first go
+struct Drafts {
     int32_t cid[kFirst], cdraft[kFirst];
     float cq[kFirst];
+    int32_t draft;                      // wave 0, lane t: draft t
+    float at_draft, u_draft;
+};
+template <bool BF16>
+__device__ __forceinline__ Drafts load_drafts(const VerifyArgs& a, VerifyLds& sm, int b, const char* rows) {
+    constexpr int SZ = RowCut<BF16>::kSz;
+    const int tid = threadIdx.x, lane = lane_id(), w = wave_id(), P = a.P, K = a.K;
+    Drafts d;
 #pragma unroll
     for (int i = 0; i < kFirst; ++i) {
         const int x = min(tid + i * kWG, P * K - 1);
-        cid[i] = a.cand[(int64_t)b * P * K + x];
-        cq[i] = a.prob[(int64_t)b * P * K + x];
-        cdraft[i] = a.path[(int64_t)b * P + (int)((uint32_t)x * a.k_inv >> 20)];
+        d.cid[i] = a.cand[(int64_t)b * P * K + x];
+        d.cq[i] = a.prob[(int64_t)b * P * K + x];
+        d.cdraft[i] = a.path[(int64_t)b * P + (int)((uint32_t)x * a.k_inv >> 20)];
     }
-    int32_t draft = -1;
-    float at_draft = 0.f, u_draft = 0.f;
+    d.draft = -1;
+    d.at_draft = d.u_draft = 0.f;
     if (w == 0 && lane < P) {
-        draft = a.path[(int64_t)b * P + lane];
-        u_draft = a.u[row0 + lane];
-        if ((unsigned)draft < (unsigned)a.V) at_draft = row_value<BF16>(rows + (size_t)lane * a.V * SZ, draft);
+        d.draft = a.path[(int64_t)b * P + lane];
+        d.u_draft = a.u[(int64_t)b * (P + 1) + lane];
+        if ((unsigned)d.draft < (unsigned)a.V) d.at_draft = row_value<BF16>(rows + (size_t)lane * a.V * SZ, d.draft);
     }
     if (tid < 72) sm.q[tid] = 0;
     fill_exp_table(sm.table);
-    const int parts = R << a.nseg_log;
-    const Factor factor = {a.c, a.c_low};
-    for (int x0 = w * 64; x0 < parts; x0 += kWG) {
-        const int x = x0 + lane;
-        Lse acc = {KIND == kVerifyProbs ? 0.f : -INFINITY, 0.f};
-        if (x < parts) {
-            const uint64_t y = a.part[(row0 << a.nseg_log) + x];
-            acc = {__uint_as_float((uint32_t)(y >> 32)), __uint_as_float((uint32_t)y)};
-        }
-        switch (a.nseg_log) {
-            case 0: break;
-            case 1: acc = lse_lanes<KIND, 2>(acc, factor); break;
-            case 2: acc = lse_lanes<KIND, 4>(acc, factor); break;
-            case 3: acc = lse_lanes<KIND, 8>(acc, factor); break;
-            case 4: acc = lse_lanes<KIND, 16>(acc, factor); break;
-            case 5: acc = lse_lanes<KIND, 32>(acc, factor); break;
-            default: acc = lse_lanes<KIND, 64>(acc, factor); break;
-        }
-        if (x < parts && (x & ((1 << a.nseg_log) - 1)) == 0) {
-            sm.m[x >> a.nseg_log] = acc.m;
-            sm.s[x >> a.nseg_log] = acc.s;
-        }
-    }
-    __syncthreads();
+    return d;
+}
+
+// Which drafts are accepted, from the rows' maxima and sums in LDS: sm.taken of
+// sm.nd, and p of each.  Every thread calls, after a barrier; ends with one.
+template <bool BF16, int KIND>
+__device__ __forceinline__ void decide(const VerifyArgs& a, VerifyLds& sm, int b, const Drafts& d) {
+    const int tid = threadIdx.x, lane = lane_id(), w = wave_id(), P = a.P, K = a.K;
     // candidates of a row are distinct: one hit at most (the largest otherwise)
     for (int x = tid, i = 0; x < P * K; x += kWG, ++i) {
         const int64_t at = (int64_t)b * P * K + x;
-        const int32_t id = i == 0 ? cid[0] : i == 1 ? cid[1] : a.cand[at];
-        const float q = i == 0 ? cq[0] : i == 1 ? cq[1] : a.prob[at];
+        const int32_t id = i == 0 ? d.cid[0] : i == 1 ? d.cid[1] : a.cand[at];
+        const float q = i == 0 ? d.cq[0] : i == 1 ? d.cq[1] : a.prob[at];
         const int t = (int)((uint32_t)x * a.k_inv >> 20);      // x / K
-        const int32_t d = i == 0 ? cdraft[0] : i == 1 ? cdraft[1] : a.path[(int64_t)b * P + t];
-        if (id == d) atomicMax(&sm.q[t], __float_as_uint(fmaxf(q, 0.f)));
+        const int32_t draft = i == 0 ? d.cdraft[0] : i == 1 ? d.cdraft[1] : a.path[(int64_t)b * P + t];
+        if (id == draft) atomicMax(&sm.q[t], __float_as_uint(fmaxf(q, 0.f)));
     }
     __syncthreads();
-
-    // 2. Which drafts are accepted: lane t of wave 0 takes draft t.
+    // lane t of wave 0 takes draft t
     if (w == 0) {
         const int nd = a.n_draft ? min(max(a.n_draft[b], 0), P) : P;
         bool yes = false;
         if (lane < P) {
             double p = 0.0;
-            if ((unsigned)draft < (unsigned)a.V) {
-                if (sm.s[lane] > 0.f) p = Weights<KIND>(sm.table, sm.m[lane], a.c64)(at_draft) / (double)sm.s[lane];
+            if ((unsigned)d.draft < (unsigned)a.V) {
+                if (sm.s[lane] > 0.0) p = Weights<KIND>(sm.table, sm.m[lane], a.c64)(d.at_draft) / sm.s[lane];
             } else if (lane < nd) {
                 atomicOr(a.err, kFlagDraft);
             }
-            const float u = (u_draft >= 0.f) ? fminf(u_draft, 0x1.fffffep-1f) : 0.f;
+            const float u = (d.u_draft >= 0.f) ? fminf(d.u_draft, 0x1.fffffep-1f) : 0.f;
             yes = lane < nd && (double)u * (double)__uint_as_float(sm.q[lane]) < p;
             sm.odds[lane] = (float)p;
         }
@@ -494,39 +481,44 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         }
     }
     __syncthreads();
-    const int t = sm.taken;
-    const bool refused = t < sm.nd;
-    const Weights<KIND> weight(sm.table, sm.m[t], a.c64);
-    const bool mass = sm.s[t] > 0.f;
-    const char* rp = rows + (size_t)t * a.V * SZ;
-    const RowCut<BF16> cut(rp, a.V, a.per2, a.nseg2);
-    // The row's candidates, for the workgroup that will draw: on their way while
-    // the segment is summed.
-    int id = -1;
-    float at_cand = 0.f, q_cand = 0.f;
-    if (w == 1 && lane < K && refused) {
-        const int64_t at = ((int64_t)b * P + t) * K + lane;
-        id = a.cand[at];
-        q_cand = fmaxf(a.prob[at], 0.f);
-        if ((unsigned)id < (unsigned)a.V) at_cand = row_value<BF16>(rp, id);
-        else atomicOr(a.err, 2u), id = -1;
+}
+
+// A refused row's candidates, one a lane of wave 1: id (-1: none), value, and the
+// draft's probability.
+struct Cand {
+    int id;
+    float value, q;
+};
+template <bool BF16>
+__device__ __forceinline__ Cand load_cand(const VerifyArgs& a, const VerifyLds& sm, int b, const char* rp) {
+    const int lane = lane_id(), t = sm.taken;
+    Cand c = {-1, 0.f, 0.f};
+    if (wave_id() == 1 && lane < a.K && t < sm.nd) {
+        const int64_t at = ((int64_t)b * a.P + t) * a.K + lane;
+        c.id = a.cand[at];
+        c.q = fmaxf(a.prob[at], 0.f);
+        if ((unsigned)c.id < (unsigned)a.V) c.value = row_value<BF16>(rp, c.id);
+        else atomicOr(a.err, 2u), c.id = -1;
     }
+    return c;
+}
 
-    // 3. This segment of row t.
-    const int nch = kWaves * a.chunks2;
-    double* chunk = a.chunk + ((int64_t)b * a.nseg2 + seg) * nch;
-    const double s = chunk_sums<BF16, KIND>(rp, cut, seg, a.chunks2, a.rounds2, weight, chunk);
-    if (lane == 0) sm.sums[w] = s;
-    __syncthreads();
-    if (tid == 0) xstore(a.seg + (int64_t)b * a.nseg2 + seg, sm.sums[0] + sm.sums[1] + sm.sums[2] + sm.sums[3]);
-    if (!block_arrive_last(&a.cnt[b], (uint32_t)a.nseg2, &sm.flag)) return;
-
-    // 4. The last workgroup draws.  What each candidate loses is min(w, q Z).
-    const double mine = w <= 1 && lane < a.nseg2 ? xload(a.seg + (int64_t)b * a.nseg2 + lane) : 0.0;
+// One workgroup draws the sequence's next token and writes its outputs.  mine: the
+// sum of segment `lane` of row t (waves 0 and 1); chunk_of(g, i): that of chunk i
+// of segment g.  What each candidate loses is min(w, q Z).
+template <bool BF16, int KIND, typename ChunkOf>
+__device__ __forceinline__ void draw_token(const VerifyArgs& a, VerifyLds& sm, int b, const char* rp,
+                                           const RowCut<BF16>& cut, const Weights<KIND>& weight, const Cand& cand,
+                                           double mine, ChunkOf chunk_of) {
+    constexpr int SZ = RowCut<BF16>::kSz, E = RowCut<BF16>::kE;
+    const int tid = threadIdx.x, lane = lane_id(), w = wave_id(), P = a.P, R = P + 1, K = a.K, t = sm.taken;
+    const int nch = kWaves * a.chunks2, vectors = a.rounds2 * 64;
+    const int64_t row0 = (int64_t)b * R;
+    const bool mass = sm.s[t] > 0.0;
     const double z = lanes_sum(mine);       // in waves 0 and 1
     if (w == 1) {
-        sm.cid[lane] = id;
-        sm.cut[lane] = id >= 0 ? fmin(weight(at_cand), (double)q_cand * z) : 0.0;
+        sm.cid[lane] = cand.id;
+        sm.cut[lane] = cand.id >= 0 ? fmin(weight(cand.value), (double)cand.q * z) : 0.0;
     }
     __syncthreads();
     // what the candidates among elements e0 .. e1 - 1 lose (places past K are empty)
@@ -564,15 +556,14 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         }
     }
     __syncthreads();
-    const int g = sm.seg, vectors = a.rounds2 * 64;
+    const int g = sm.seg;
     if (tid < nch) {
-        const double x = xload(a.chunk + ((int64_t)b * a.nseg2 + g) * nch + tid) -
+        const double x = chunk_of(g, tid) -
                          loss_in(chunk_first(cut, g, vectors, nch, tid), chunk_first(cut, g, vectors, nch, tid + 1));
         sm.sums[tid] = x > 0.0 ? x : 0.0;
     }
     __syncthreads();
     if (w == 0) {
-        constexpr int E = RowCut<BF16>::kE;
         double target = sm.target;
         const int at = find_prefix(sm.sums, nch, target);
         const int e0 = chunk_first(cut, g, vectors, nch, at), e1 = chunk_first(cut, g, vectors, nch, at + 1);
@@ -652,6 +643,194 @@ __global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
         a.out_tok[row0 + tid] = tid < t ? a.path[(int64_t)b * P + tid] : (tid == t ? sm.pick : -1);
         a.out_prob[row0 + tid] = tid <= t ? sm.odds[tid] : 0.f;
     }
+}
+
+// Launch 2 (sampling, many rows): nseg2 workgroups a sequence sum the row that its
+// draw needs; the last one draws.
+template <bool BF16, int KIND>
+__global__ __launch_bounds__(kWG) void k_verify_draw(VerifyArgs a) {
+    constexpr int SZ = RowCut<BF16>::kSz;
+    __shared__ VerifyLds sm;
+    const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
+    const int b = (int)(blockIdx.x / a.nseg2), seg = (int)(blockIdx.x % a.nseg2);
+    const int R = a.P + 1;
+    const int64_t row0 = (int64_t)b * R;
+    const char* rows = reinterpret_cast<const char*>(a.target) + (size_t)row0 * a.V * SZ;
+
+    // Every row's maximum and sum from its segments (a power of two of them: the
+    // lanes of a wave take several rows at once).  All loads go out before any is
+    // used.
+    const Drafts drafts = load_drafts<BF16>(a, sm, b, rows);
+    const int parts = R << a.nseg_log;
+    const Factor factor = {a.c, a.c_low};
+    for (int x0 = w * 64; x0 < parts; x0 += kWG) {
+        const int x = x0 + lane;
+        Lse acc = {KIND == kVerifyProbs ? 0.f : -INFINITY, 0.f};
+        if (x < parts) {
+            const uint64_t y = a.part[(row0 << a.nseg_log) + x];
+            acc = {__uint_as_float((uint32_t)(y >> 32)), __uint_as_float((uint32_t)y)};
+        }
+        switch (a.nseg_log) {
+            case 0: break;
+            case 1: acc = lse_lanes<KIND, 2>(acc, factor); break;
+            case 2: acc = lse_lanes<KIND, 4>(acc, factor); break;
+            case 3: acc = lse_lanes<KIND, 8>(acc, factor); break;
+            case 4: acc = lse_lanes<KIND, 16>(acc, factor); break;
+            case 5: acc = lse_lanes<KIND, 32>(acc, factor); break;
+            default: acc = lse_lanes<KIND, 64>(acc, factor); break;
+        }
+        if (x < parts && (x & ((1 << a.nseg_log) - 1)) == 0) {
+            sm.m[x >> a.nseg_log] = acc.m;
+            sm.s[x >> a.nseg_log] = acc.s;
+        }
+    }
+    __syncthreads();
+    decide<BF16, KIND>(a, sm, b, drafts);
+
+    // This segment of row t.  The candidates, for the workgroup that will draw, are
+    // on their way meanwhile.
+    const int t = sm.taken;
+    const Weights<KIND> weight(sm.table, sm.m[t], a.c64);
+    const char* rp = rows + (size_t)t * a.V * SZ;
+    const RowCut<BF16> cut(rp, a.V, a.per2, a.nseg2);
+    const Cand cand = load_cand<BF16>(a, sm, b, rp);
+    const int nch = kWaves * a.chunks2;
+    double* chunks = a.chunk + (int64_t)b * a.nseg2 * nch;
+    const double s = chunk_sums<BF16, KIND>(rp, cut, seg, a.chunks2, a.rounds2, weight, chunks + (int64_t)seg * nch);
+    if (lane == 0) sm.sums[w] = s;
+    __syncthreads();
+    if (tid == 0) xstore(a.seg + (int64_t)b * a.nseg2 + seg, sm.sums[0] + sm.sums[1] + sm.sums[2] + sm.sums[3]);
+    if (!block_arrive_last(&a.cnt[b], (uint32_t)a.nseg2, &sm.flag)) return;
+
+    const double mine = w <= 1 && lane < a.nseg2 ? xload(a.seg + (int64_t)b * a.nseg2 + lane) : 0.0;
+    draw_token<BF16, KIND>(a, sm, b, rp, cut, weight, cand, mine,
+                           [&](int g, int i) { return xload(chunks + (int64_t)g * nch + i); });
+}
+
+// Few rows: launch 1 makes the chunk sums of every row in fp64, a segment's
+// relative to its own maximum, which the workgroup finds first, the segment in
+// registers (at most kHold vectors a lane).
+constexpr int kHold = 4;
+template <bool BF16, int KIND>
+__global__ __launch_bounds__(kWG) void k_verify_sums(VerifyArgs a) {
+    constexpr int E = RowCut<BF16>::kE, SZ = RowCut<BF16>::kSz;
+    __shared__ double table[kExpTable], sums[kWaves];
+    __shared__ float most[kWaves];
+    const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
+    const int64_t row = blockIdx.x / a.nseg2;
+    const int seg = (int)(blockIdx.x % a.nseg2);
+    const char* rp = reinterpret_cast<const char*>(a.target) + (size_t)row * a.V * SZ;
+    const RowCut<BF16> cut(rp, a.V, a.per2, a.nseg2);
+    const u32x4_t* vp = reinterpret_cast<const u32x4_t*>(rp + (size_t)cut.head * SZ);
+    const int v1 = cut.first_vec(seg + 1), v0 = cut.first_vec(seg) + w * a.chunks2 * 64 + lane;
+
+    float x[kHold][E], head = -INFINITY, tail = -INFINITY;
+    u32x4_t ld[kHold];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+        if (i < a.chunks2 && v0 + i * 64 < v1) ld[i] = __builtin_nontemporal_load(vp + v0 + i * 64);
+    if (w == 0 && seg == 0 && lane < cut.head) head = row_value<BF16>(rp, lane);
+    const int last = cut.head + cut.nv * E + lane;
+    if (w == kWaves - 1 && seg == cut.nseg - 1 && last < a.V) tail = row_value<BF16>(rp, last);
+    fill_exp_table(table);
+    float m = fmaxf(head, tail);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        if (i < a.chunks2 && v0 + i * 64 < v1) {
+            unpack16<BF16>(ld[i], x[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[i][e] = -INFINITY;        // weighs nothing, of either kind
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) m = fmaxf(m, x[i][e]);
+    }
+    m = lanes_max(m);
+    if (lane == 0) most[w] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    const Weights<KIND> weight(table, m, a.c64);
+    const int64_t at = row * a.nseg2 + seg;
+    double whole = 0.0;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+        if (i >= a.chunks2) break;
+        double y[E];
+        weight.of(x[i], y);
+#pragma unroll
+        for (int d = E / 2; d > 0; d /= 2)
+#pragma unroll
+            for (int e = 0; e < d; ++e) y[e] += y[e + d];
+        double s = y[0];
+        if (i == 0 && w == 0 && seg == 0) s += weight(head);
+        if (i == a.chunks2 - 1 && w == kWaves - 1 && seg == cut.nseg - 1) s += weight(tail);
+        s = lanes_sum(s);
+        if (lane == 0) a.chunk[(at * kWaves + w) * a.chunks2 + i] = s;
+        whole += s;
+    }
+    if (lane == 0) sums[w] = whole;
+    __syncthreads();
+    if (tid == 0) {
+        a.top[at] = m;
+        a.seg[at] = sums[0] + sums[1] + sums[2] + sums[3];
+    }
+}
+
+// Launch 2 of few rows: one workgroup a sequence.
+template <bool BF16, int KIND>
+__global__ __launch_bounds__(kWG) void k_verify_pick(VerifyArgs a) {
+    constexpr int SZ = RowCut<BF16>::kSz;
+    __shared__ VerifyLds sm;
+    __shared__ double scaled[65 * kVerifySegs];     // sums of the rows' segments, relative to the row's maximum
+    const int lane = lane_id(), w = wave_id(), b = (int)blockIdx.x, R = a.P + 1;
+    const int64_t row0 = (int64_t)b * R;
+    const char* rows = reinterpret_cast<const char*>(a.target) + (size_t)row0 * a.V * SZ;
+    const Drafts drafts = load_drafts<BF16>(a, sm, b, rows);
+    __syncthreads();
+    constexpr int U = 4;                            // rows of a wave on their way at once
+    for (int r0 = w; r0 < R; r0 += kWaves * U) {
+        float m[U];
+        double s[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int r = r0 + i * kWaves;
+            const bool live = r < R && lane < a.nseg2;
+            const int64_t at = (row0 + (live ? r : 0)) * a.nseg2 + (live ? lane : 0);
+            m[i] = a.top[at];
+            s[i] = a.seg[at];
+            if (!live) {
+                m[i] = -INFINITY;
+                s[i] = 0.0;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int r = r0 + i * kWaves;
+            if (r >= R) break;
+            const float most = lanes_max(m[i]);
+            double y = s[i];
+            if constexpr (KIND != kVerifyProbs) y *= Weights<KIND>(sm.table, most, a.c64)(m[i]);
+            scaled[r * kVerifySegs + lane] = y;
+            const double z = lanes_sum(y);
+            if (lane == 0) {
+                sm.m[r] = most;
+                sm.s[r] = z;
+            }
+        }
+    }
+    __syncthreads();
+    decide<BF16, KIND>(a, sm, b, drafts);
+    const int t = sm.taken;
+    const Weights<KIND> weight(sm.table, sm.m[t], a.c64);
+    const char* rp = rows + (size_t)t * a.V * SZ;
+    const RowCut<BF16> cut(rp, a.V, a.per2, a.nseg2);
+    const Cand cand = load_cand<BF16>(a, sm, b, rp);
+    const int64_t at = (row0 + t) * a.nseg2;
+    draw_token<BF16, KIND>(a, sm, b, rp, cut, weight, cand, w <= 1 ? scaled[t * kVerifySegs + lane] : 0.0,
+                           [&](int g, int i) {
+                               const double x = a.chunk[(at + g) * kWaves * a.chunks2 + i];
+                               return KIND == kVerifyProbs ? x : x * weight(a.top[at + g]);
+                           });
 }
 
 // Launch 2 at temperature 0: a draft is accepted while it is its row's best

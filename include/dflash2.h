@@ -540,8 +540,10 @@ typedef struct df2_verify_dims {
  *   out_len   [B] int32         tokens that count: accepted drafts + 1
  *   out_prob  [B, P + 1] float  p of each such token (1 at temperature 0), then 0
  *   workspace dflash2_verify_workspace(dims) bytes, 16-byte aligned
- * Row sums are fp32 of fp32 weights; the row that a token is drawn from is
- * summed in fp64, so that the token does not depend on how sums are rounded.
+ * Row sums are fp32 of fp32 weights (with up to 2^24 elements in all rows, fp64);
+ * the row that a token is drawn from is summed in fp64, so that the token does
+ * not depend on how sums are rounded, and the temperature is a double for the
+ * same reason.
  * -inf logits have weight 0; other non-finite values are outside the
  * contract.  Where no token is left to draw (a row without weight, or
  * candidates' probabilities that add to more than 1), flag bit 6 is raised and
@@ -550,7 +552,7 @@ typedef struct df2_verify_dims {
 size_t dflash2_verify_workspace(const df2_verify_dims* dims);
 df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const int32_t* path,
                           const int32_t* cand_idx, const float* cand_prob,
-                          const int32_t* n_draft, float temperature, const float* u,
+                          const int32_t* n_draft, double temperature, const float* u,
                           int32_t* out_tok, int32_t* out_len, float* out_prob,
                           void* workspace, size_t workspace_bytes, hipStream_t stream);
 

@@ -448,6 +448,41 @@ def test_verify_draws_at_every_place_of_a_row(dtype, V):
     assert df2.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype,B,P,V,K,tau", [
+    (BF, 32, 7, 70001, 16, 0.8), (F32, 4300, 3, 1003, 5, 1.2), (BF, 300, 64, 1001, 64, 1.0), (F32, 70, 15, 16384, 3, 1.0),
+    (BF, 130, 2, 50000, 8, 2.0), (BF, 8, 7, 262143, 16, 1.0), (BF, 8, 7, 262145, 16, 1.0),
+])
+def test_verify_many_elements_against_fp64(dtype, B, P, V, K, tau):
+    """Sizes on both sides of what takes fp64 sums of every row."""
+    say("verify many", dtype, B, P, V, K, tau)
+    c = verify_case(B + V, dtype, B, P, V, K)
+    nd = torch.randint(0, P + 1, (B,), generator=torch.Generator().manual_seed(B), dtype=torch.int32).cuda()
+    got = df2.verify(c["target"], c["path"], c["cand"], c["prob"], c["u"], temperature=tau, n_draft=nd)
+    assert df2.device_error() == 0
+    check_verify(c, got, tau, nd)
+
+
+@pytest.mark.parametrize("B", [3, 1200])
+@pytest.mark.parametrize("kind,tau", [("logits", 0.45), ("logits", 0.7), ("logits", 1.3), ("probs", 1.0)])
+def test_verify_masked_rows_few_and_many(B, kind, tau):
+    """Half of the vocabulary without weight, some rows without any."""
+    say("verify masked", B, kind, tau)
+    V = 5000
+    c = verify_case(B, F32, B, 3, V, 7)
+    dead = torch.rand((B, 1, V), generator=torch.Generator().manual_seed(B)) < 0.5
+    dead.scatter_(2, c["cand"].cpu().long().flatten(1)[:, None], False)
+    c["target"] = c["target"].masked_fill(dead.cuda(), -float("inf"))
+    if kind == "probs":
+        c["target"] = torch.softmax(c["target"], -1)
+    args = (c["path"], c["cand"], c["prob"], c["u"])
+    check_verify(c, df2.verify(c["target"], *args, temperature=tau, kind=kind), tau, None, kind)
+    assert df2.device_error() == 0
+    c["target"][1] = 0.0 if kind == "probs" else -float("inf")
+    tok, cnt, p = df2.verify(c["target"], *args, temperature=tau, kind=kind)
+    assert df2.device_error() == 64
+    assert tok[1].tolist() == [0, -1, -1, -1] and int(cnt[1]) == 1 and float(p[1].abs().max()) == 0.0
+
+
 def test_verify_ids_outside_the_vocabulary():
     say("verify bad ids")
     c = verify_case(8, BF, 3, 4, 1000, 4)
