@@ -52,7 +52,6 @@ namespace df2 {
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
@@ -86,6 +85,7 @@ struct AttnArgs {
     int G, causal, window;
     int bm;                 // rows of a block
     int wgs, whole;         // workgroups of the launch; 1: each takes a whole block
+    int cus;                // compute units
     double inv_g;           // 1 / G
     float c;                // scale * log2(e)
 };
@@ -201,6 +201,12 @@ __device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
     }
     const int all = c.head_tiles * a.kv.Hkv;
     c.wgs = min(a.wgs, all);
+    // More than one workgroup a compute unit only with eight tiles for each: shorter
+    // stretches leave more parts than they save (event times with 512 workgroups and
+    // the join, then with 256: 4 contexts of 25 thousand tokens, 8 new, 16 / 2 heads, 6
+    // tiles each, 34 + 14.5 and 34 + 9.8 us; 2 of 4000, 32 new, 32 / 8 heads, 2 tiles,
+    // 29 + 16.6 and 25 + 12.8; but 16 such, 16 tiles, 68 + 12.1 and 76 + 12.0).
+    if (!a.whole && c.wgs > a.cus && all < 8 * c.wgs) c.wgs = a.cus;
     c.each = c.wgs > 0 ? (int)((unsigned)all / (unsigned)c.wgs) : 0;
     c.more = all - c.each * c.wgs;
     return c;
@@ -399,7 +405,6 @@ struct AttnShape {
     static constexpr int KT = 32 * WK * KS;
     static constexpr int kTileBytes = KT * Tile::kRow;       // of K, and of V
     static constexpr int kStage = 2 * kTileBytes;
-    static constexpr int kStages = NS;
     static constexpr int kLoads = kTileBytes / (1024 * kWaves);     // of a wave for K, and for V
     static constexpr int kRows = KT / kWaves;                       // keys that they bring
     static constexpr int kGroup = kLoads % 4 == 0 && Tile::kRow >= 256 ? 4 : kLoads % 2 == 0 ? 2 : 1;
@@ -448,7 +453,7 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
     LaneSeq seqs;
     const Cut cut = cut_work<Shape>(a, seqs);
     int wg = blockIdx.x;
-    if (!a.whole && cut.wgs % 8 == 0 && cut.wgs == (int)gridDim.x)
+    if (!a.whole && cut.wgs % 8 == 0 && wg < cut.wgs)
         wg = (int)(blockIdx.x % 8) * (cut.wgs / 8) + (int)(blockIdx.x / 8);
     int32_t* split = a.split + 8 * wg;
     if (wg >= cut.wgs) {

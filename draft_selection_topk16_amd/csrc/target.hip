@@ -271,6 +271,7 @@ df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_
     a.bm = pl.bm;
     a.wgs = pl.wgs;
     a.whole = pl.whole;
+    a.cus = compute_units();
     a.inv_g = 1.0 / a.G;
     a.c = (float)((double)scale * 1.4426950408889634);
     return with_type(kv, [&](auto bf16, auto d) {
