@@ -107,9 +107,12 @@ struct AttnPlan {
 // The kernels there are: rows (WR waves of 32), key groups, 32-key steps.  A block
 // of few rows gets its waves from groups of keys (one row after 1003 tokens, event
 // times: 9.7 us and 6.0 for the join with four groups, 8.8 and 7.4 with one, which
-// leaves four times the parts); with many rows each wave reads all keys, and longer
-// tiles meet less often (prompt chunks: 128 keys a tile 700 us, 96 712, blocks of 128
-// rows, two a compute unit, 730).
+// leaves four times the parts); with 64 rows of head size 128 in bf16 two workgroups
+// of two waves a compute unit do as well without groups to meet (128 contexts of a
+// thousand tokens 119 + 16 us, two groups 124 + 18, four groups, one workgroup a
+// unit, 136 + 11); with many rows each wave reads all keys, and longer tiles meet
+// less often (prompt chunks: 128 keys a tile 700 us, 96 712, blocks of 128 rows, two
+// a compute unit, 730).
 template <bool BF16, int D, typename F>
 auto with_shape(int wr, F&& f) {
     constexpr int RB = AttnTile<BF16, D>::kRow;
@@ -120,7 +123,7 @@ auto with_shape(int wr, F&& f) {
         return f(AttnShape<BF16, D, 8, 1, 2, 2>());
     } else if constexpr (RB == 256 && BF16) {
         if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 1, 2, 2>());
         if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2>());
         return f(AttnShape<BF16, D, 8, 1, 4, 2>());
     } else if constexpr (RB == 256) {
