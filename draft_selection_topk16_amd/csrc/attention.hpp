@@ -33,11 +33,12 @@
 // Measured (kernel, then join; head size 128, bf16 unless said):
 //   4 contexts of 65 to 131 thousand tokens, 8 new each, 32 / 8 heads: 249 + 7 us
 //     for 1.61 GB, 6.5 TB/s: a copy of the loads alone takes as long;
-//   32 contexts of 301 to 12007 tokens, 8 new each, 64 / 8 heads: 152 + 10 us for
-//     816 MB, 5.4 TB/s: some 20 us are the start, the parts (33 MB) and the end;
-//   1 new token after 1003, 32 / 8 heads: 7.6 + 3.4 us, latency: 1.9 us to the
+//   32 contexts of 301 to 12007 tokens, 8 new each, 64 / 8 heads: 155 + 11 us (156
+//     back to back) for 816 MB, 5.3 TB/s: some 20 us are the start, the parts (25 MB)
+//     and the end;
+//   1 new token after 1003, 32 / 8 heads: 7.5 + 3.5 us, latency: 1.9 us to the
 //     cut, 1.5 to the place, 0.8 for page ids, 0.9 for the first tile;
-//   3 drafted blocks in fp32 of head size 64, up to 2049 keys: 9.9 + 4.1 us;
+//   3 drafted blocks in fp32 of head size 64, up to 2049 keys: 9.8 + 4.2 us;
 //   prompt chunks (739 GFLOP): 700 us, 1060 TFLOP/s, where a large library product
 //     reaches 1364.  Nothing alone bounds it: with its products only, it takes 565
 //     us (the clock falls to 2.05 GHz under them), LDS loads add 40, operand reads
