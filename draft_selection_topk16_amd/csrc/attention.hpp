@@ -333,24 +333,26 @@ __device__ __forceinline__ void run_products(Read read, Mul mul) {
         "s_mov_b32 m0, %0\n\t"                              \
         "s_nop 0\n\t"                                       \
         "global_load_lds_dwordx4 %1, %3" NT "\n\t"          \
-        "global_load_lds_dwordx4 %2, %3 offset:1024" NT     \
+        "global_load_lds_dwordx4 %2, %3 offset:%4" NT       \
         :                                                   \
-        : "s"(lds_base), "v"(off[0]), "v"(off[1]), "s"(base) \
+        : "s"(lds_base), "v"(off[0]), "v"(off[1]), "s"(base), "n"(kLoad) \
         : "memory")
 #define DF2_TO_LDS_4(NT)                                    \
     asm volatile(                                           \
         "s_mov_b32 m0, %0\n\t"                              \
         "s_nop 0\n\t"                                       \
         "global_load_lds_dwordx4 %1, %5" NT "\n\t"          \
-        "global_load_lds_dwordx4 %2, %5 offset:1024" NT "\n\t" \
-        "global_load_lds_dwordx4 %3, %5 offset:2048" NT "\n\t" \
-        "global_load_lds_dwordx4 %4, %5 offset:3072" NT     \
+        "global_load_lds_dwordx4 %2, %5 offset:%6" NT "\n\t" \
+        "global_load_lds_dwordx4 %3, %5 offset:%7" NT "\n\t" \
+        "global_load_lds_dwordx4 %4, %5 offset:%8" NT       \
         :                                                   \
-        : "s"(lds_base), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base) \
+        : "s"(lds_base), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base), "n"(kLoad), \
+          "n"(2 * kLoad), "n"(3 * kLoad)                    \
         : "memory")
 template <int G, bool ONCE>
 __device__ __forceinline__ void load_to_lds(const void* base, const uint32_t* off, uint32_t lds_base) {
     static_assert(G == 1 || G == 2 || G == 4, "loads in a group");
+    constexpr int kLoad = 1024;         // bytes of a wave's load
     // the same in the wave, also where the compiler cannot see it
     const uint64_t addr = (uint64_t)base;
     base = reinterpret_cast<const void*>(

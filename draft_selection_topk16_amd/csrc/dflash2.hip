@@ -1271,7 +1271,7 @@ df2_status dflash2_select_sample_rows(const df2_dims* dims, const void* logits, 
                                       const int32_t* prev_tok, int32_t K, float temperature,
                                       const float* u, int32_t* out_path, float* out_q,
                                       float* out_score, int32_t* out_cand, float* out_rows,
-                                           hipStream_t stream) {
+                                      hipStream_t stream) {
     g_last_error.clear();
     float inv_tau = 0.f;
     df2_status st = sample_inv_tau(temperature, &inv_tau);

@@ -172,6 +172,20 @@ def test_attention_far_pages():
     assert torch.equal(kc[num - small:], c["k_cache"]) and torch.equal(vc[num - small:], c["v_cache"])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_shared_pages(dtype):
+    """Sequences with a common beginning name the same pages; one is listed twice."""
+    say("attention shared pages", dtype)
+    c = paged_case(60, dtype, 64, 8, 2, 16, [3, 3, 8], [800, 800, 793])
+    c["table"][1, :49] = c["table"][0, :49]
+    c["table"][2, :30] = c["table"][0, :30]
+    check_attention(c, attend(c))
+    twice = dict(c, table=c["table"][[0, 0, 2]].contiguous(), ctx=c["ctx"][[0, 0, 2]].contiguous())
+    twice["q"][3:6] = twice["q"][:3]
+    out = attend(twice)
+    check_attention(twice, out)
+
+
 def test_attention_many_sequences():
     """More sequences than a wave scans at once, empty ones among them."""
     say("attention many sequences")
