@@ -868,15 +868,15 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
 
 // Joins the parts of the blocks that lie across workgroups:
 //     sum_s 2^(m_s - m) (o_s, l_s)
-// over the parts s of a row.  Sixteen workgroups for each boundary of stretches, of
-// which the first inside a block does the block.  D / 4 lanes take a row, or
-// several such groups the row's parts in turn (few rows, perhaps many parts),
-// which then meet in LDS.
-constexpr int kJoinWgs = 16;
+// over the parts s of a row.  kJoinWgs workgroups for each boundary of stretches, of
+// which the first inside a block does the block.  D / 4 lanes take a row, four parts
+// at a time; with more parts several such groups share the row and meet in LDS, so
+// that a hundred parts of a few rows are a few loads one after another.
+constexpr int kJoinWgs = 16, kJoinThreads = 256;
 template <bool BF16, int D>
-__global__ __launch_bounds__(256) void k_attend_join(AttnArgs a) {
-    constexpr int L = D / 4, NG = 256 / L;
-    __shared__ f32x4_t lds_y[256];
+__global__ __launch_bounds__(kJoinThreads) void k_attend_join(AttnArgs a) {
+    constexpr int L = D / 4, NG = kJoinThreads / L;
+    __shared__ f32x4_t lds_y[kJoinThreads];
     __shared__ float lds_m[NG], lds_l[NG];
     const int slice = blockIdx.x % kJoinWgs, boundary = 1 + blockIdx.x / kJoinWgs;
     const int32_t* split = a.split + 8 * boundary;
@@ -884,15 +884,15 @@ __global__ __launch_bounds__(256) void k_attend_join(AttnArgs a) {
     const int h = split[1], s0 = split[2], r0 = split[3], M = split[4];
     if (w1 < 0) return;
     const int group = threadIdx.x / L, d = (threadIdx.x % L) * 4;
-    const int rows = a.bm / kJoinWgs;                   // of this workgroup: 2 to 16
-    const int share = max(NG / rows, 1);                // groups of a row
+    const int live = min(a.bm, M - r0);
+    int share = 1;                                      // groups of a row, as long as one go takes all rows
+    while (4 * share < w1 - w0 + 1 && share < NG && live * share * 2 <= NG * kJoinWgs) share *= 2;
     const int at_once = NG / share;
-    for (int i0 = slice * rows; i0 < (slice + 1) * rows && r0 + i0 < M; i0 += at_once) {
+    for (int i0 = slice * at_once; i0 < live; i0 += kJoinWgs * at_once) {
         const int i = i0 + group / share, r = r0 + i;
-        const bool live = r < M;
         float m = -INFINITY, l = 0.f;
         f32x4_t y = {0.f, 0.f, 0.f, 0.f};
-        if (live) {
+        if (i < live) {
             for (int w = w0 + group % share; w <= w1; w += 4 * share) {
                 float pm[4], pl[4];
                 f32x4_t py[4];
@@ -929,18 +929,19 @@ __global__ __launch_bounds__(256) void k_attend_join(AttnArgs a) {
                 lds_l[group] = l;
             }
             __syncthreads();
-            if (group % share != 0) continue;
-            for (int x = 1; x < share; ++x) {
-                const float mx = lds_m[group + x];
-                if (mx == -INFINITY) continue;
-                const float mn = fmaxf(m, mx);
-                const float f = __builtin_amdgcn_exp2f(m - mn), e = __builtin_amdgcn_exp2f(mx - mn);
-                m = mn;
-                l = f * l + e * lds_l[group + x];
-                y = f * y + e * lds_y[(group + x) * L + threadIdx.x % L];
+            if (group % share == 0) {
+                for (int x = 1; x < share; ++x) {
+                    const float mx = lds_m[group + x];
+                    if (mx == -INFINITY) continue;
+                    const float mn = fmaxf(m, mx);
+                    const float f = __builtin_amdgcn_exp2f(m - mn), e = __builtin_amdgcn_exp2f(mx - mn);
+                    m = mn;
+                    l = f * l + e * lds_l[group + x];
+                    y = f * y + e * lds_y[(group + x) * L + threadIdx.x % L];
+                }
             }
         }
-        if (!live) continue;
+        if (i >= live || group % share != 0) continue;
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         const int t = div_g(a, r), head = h * a.G + r - t * a.G;
         const float out[4] = {y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv};

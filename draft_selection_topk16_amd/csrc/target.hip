@@ -152,30 +152,37 @@ auto with_type(const df2_paged_kv* kv, F&& f) {
     return f(integral_constant<bool, false>(), integral_constant<int, 256>());
 }
 
-// Blocks of as many rows as a sequence has on average, and as many workgroups as
-// are resident at once (fewer where max_len says that there are fewer tiles).  Whole
-// blocks from two for each resident workgroup on: there is then no part to leave and
-// join, and the end is short against the rest.
+// Blocks of as many rows as a sequence has on average, but smaller ones where a
+// compute unit then gets less than three tiles: parts of large blocks cost more than
+// reading the keys again (event times with the join, blocks of 256, 128, 64 and 32
+// rows: one chunk of 1432 tokens after 700, 4 / 2 heads, 48, 36, 35 and 40 us; 2 of 59
+// after 1849, 16 / 4 heads, 35, 32, 27 and 28; 4 of 64 after 4000, 32 / 8 heads, 4
+// tiles, 49 and 51).  As many workgroups as are resident at once (fewer where max_len
+// says that there are fewer tiles).  Whole blocks from two for each resident
+// workgroup on: there is then no part to leave and join, and the end is short
+// against the rest.
 AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
     AttnPlan pl;
     const int64_t rows = (int64_t)kv->N * (kv->Hq / kv->Hkv);
     const int64_t seqs = std::min(kv->B, kv->N);
     const int64_t each = (rows + seqs - 1) / seqs;
-    pl.wr = each <= 32 ? 1 : each <= 64 ? 2 : each <= 128 ? 4 : 8;
     int per_cu = 1;
-    with_type(kv, [&](auto bf16, auto d) {
-        return with_shape<decltype(bf16)::value, decltype(d)::value>(pl.wr, [&](auto shape) {
-            using S = decltype(shape);
-            pl.bm = S::BM;
-            pl.kt = S::KT;
-            pl.gk = S::kGroupKeys;
-            per_cu = std::max(1, std::min(160 * 1024 / S::kAllLds, 8 / S::kWaves));
-            return 0;
+    const auto tiles = [&](int64_t len) { return (len + pl.gk + pl.kt - 1) / pl.kt; };
+    for (pl.wr = each <= 32 ? 1 : each <= 64 ? 2 : each <= 128 ? 4 : 8;; pl.wr /= 2) {
+        with_type(kv, [&](auto bf16, auto d) {
+            return with_shape<decltype(bf16)::value, decltype(d)::value>(pl.wr, [&](auto shape) {
+                using S = decltype(shape);
+                pl.bm = S::BM;
+                pl.kt = S::KT;
+                pl.gk = S::kGroupKeys;
+                per_cu = std::max(1, std::min(160 * 1024 / S::kAllLds, 8 / S::kWaves));
+                return 0;
+            });
         });
-    });
+        if (pl.wr == 1 || seqs * ((each + pl.bm - 1) / pl.bm) * kv->Hkv * tiles(max_len) >= 3 * compute_units()) break;
+    }
     const int64_t blocks = rows / pl.bm + seqs;     // one more in each sequence that has tokens
     const int64_t resident = (int64_t)compute_units() * per_cu;
-    const auto tiles = [&](int64_t len) { return (len + pl.gk + pl.kt - 1) / pl.kt; };
     pl.fits = blocks * kv->Hkv * tiles((int64_t)kv->table_width * kv->page_size) < (1LL << 31);
     pl.whole = pl.wr == 8 && rows / pl.bm * kv->Hkv >= 2 * resident;
     if (pl.whole) {
@@ -217,7 +224,8 @@ df2_status launch_attend(const AttnPlan& pl, const AttnArgs& a, hipStream_t stre
         return launched("dflash2_paged_attention launch");
     });
     if (st != DF2_OK || pl.wgs == 1 || pl.whole) return st;
-    hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)(kJoinWgs * (pl.wgs - 1))), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)(kJoinWgs * (pl.wgs - 1))),
+                       dim3(kJoinThreads), 0, stream, a);
     return launched("dflash2_paged_attention join launch");
 }
 

@@ -71,6 +71,18 @@ ATTENTION = [
     ("pages_of_one_token", BF, 128, 8, 2, 1, [3, 1], [5003, 2050], True, 0),
     ("pages_of_one_token_f32_window", F32, 64, 4, 4, 1, [2, 1], [3500, 1], True, 2500),
     ("chunk_small_pages", BF, 128, 32, 8, 2, [4100], [300], True, 0),
+    # enough tiles for blocks of 256, 128 and 64 rows, not for whole ones
+    ("blocks_of_256", BF, 128, 32, 8, 16, [200, 130], [3000, 2500], True, 0),
+    ("blocks_of_256_64", BF, 64, 32, 8, 32, [200, 130], [1500, 1900], True, 0),
+    ("blocks_of_256_whole_block", BF, 128, 16, 4, 16, [300, 257], [3000, 3050], False, 0),
+    ("blocks_of_128", BF, 128, 32, 8, 16, [31, 1, 32], [3300, 2, 3100], True, 0),
+    ("blocks_of_128_window", BF, 64, 32, 8, 16, [31, 20, 32], [3300, 40, 3100], True, 900),
+    ("blocks_of_128_f32", F32, 128, 16, 8, 16, [64, 40], [1650, 1700], True, 0),
+    ("blocks_of_128_f32_64", F32, 64, 16, 8, 16, [64, 40], [1650, 1700], False, 0),
+    ("blocks_of_128_256", BF, 256, 16, 8, 16, [64, 40], [1650, 1700], True, 0),
+    ("blocks_of_64", BF, 128, 32, 8, 16, [16, 9, 16], [2300, 4, 2200], True, 0),
+    ("blocks_of_64_64", BF, 64, 32, 8, 16, [16, 9, 16], [4700, 4, 4500], True, 0),
+    ("blocks_of_64_f32", F32, 64, 32, 8, 16, [16, 9, 16], [2300, 4, 2200], True, 700),
 ]
 
 
