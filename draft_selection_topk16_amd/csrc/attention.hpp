@@ -85,8 +85,10 @@ struct AttnArgs {
     int64_t q_stride, out_stride;
     int G, causal, window;
     int bm;                 // rows of a block
-    int wgs, whole;         // workgroups of the launch; 1: each takes a whole block
+    int wgs, whole;         // workgroups that take stretches; 1: each takes a whole block
     int cus;                // compute units
+    int join;               // there may be parts, and a workspace for them
+    int choose;             // blocks enough for the kernel to choose whole ones
     double inv_g;           // 1 / G
     float c;                // scale * log2(e)
 };
@@ -118,9 +120,11 @@ __device__ __forceinline__ int inside_table(const PagedKv& kv, int ctx, int n) {
 // workgroup is written at once; of one that lies across a boundary, each
 // workgroup leaves its part, and k_attend_join adds them up.  A workgroup has at
 // most two such parts: where its stretch begins and where it ends.
-// With many more blocks than workgroups (long chunks) each workgroup takes one
-// whole block instead (`whole`: a block counts as one tile of the line): blocks
-// of a head then run side by side and share its keys in the L2.
+// Or each workgroup takes one whole block (`whole`: a block counts as one tile of
+// the line): there are no parts to leave and join, and blocks of a head run side by
+// side and share its keys in the L2.  So it is with many more blocks than
+// workgroups (long chunks: the launch has no join then), and where the lengths make
+// it the shorter way (Cut).
 // Lengths are in device memory, so each wave finds its place itself, a lane to
 // a sequence.
 // ----------------------------------------------------------------------------
@@ -150,33 +154,46 @@ __device__ __forceinline__ BlockKeys block_keys(const AttnArgs& a, int ctx, int 
 // a block; others by their lane.
 constexpr int kLaneBlocks = 4;
 
-// A lane's sequence: its tokens, blocks and length on the line.
+// A lane's sequence: its tokens, blocks and length on the line, and the tiles of its
+// longest block.
 struct LaneSeq {
-    int s0, n, ctx, blocks, tiles;
+    int s0, n, ctx, blocks, tiles, most;
 };
 template <typename Shape>
-__device__ __forceinline__ LaneSeq lane_seq(const AttnArgs& a, int c0) {
-    LaneSeq q = {0, 0, 0, 0, 0};
+__device__ __forceinline__ LaneSeq lane_seq(const AttnArgs& a, int c0, bool whole) {
+    LaneSeq q = {0, 0, 0, 0, 0, 0};
     const int lane = lane_id(), i = c0 + lane;
     if (i < a.kv.B) {
         seq_tokens(a.kv, i, q.s0, q.n);
         q.ctx = inside_table(a.kv, a.kv.ctx[i], q.n);
         q.blocks = (int)((unsigned)(q.n * a.G + Shape::BM - 1) / (unsigned)Shape::BM);
     }
-    if (a.whole) {
+    if (whole) {
         q.tiles = q.blocks;
         return q;
     }
     if (q.blocks <= kLaneBlocks)
-        for (int j = 0; j < q.blocks; ++j) q.tiles += block_keys<Shape>(a, q.ctx, q.n, j).tiles;
+        for (int j = 0; j < q.blocks; ++j) {
+            const int tiles = block_keys<Shape>(a, q.ctx, q.n, j).tiles;
+            q.tiles += tiles;
+            q.most = max(q.most, tiles);
+        }
     for (uint64_t big = __ballot(q.blocks > kLaneBlocks); big; big &= big - 1) {
         const int f = __builtin_ctzll(big);
         const int ctx = __builtin_amdgcn_readlane(q.ctx, f), n = __builtin_amdgcn_readlane(q.n, f);
         const int blocks = __builtin_amdgcn_readlane(q.blocks, f);
-        int sum = 0;
-        for (int j = lane; j < blocks; j += 64) sum += block_keys<Shape>(a, ctx, n, j).tiles;
+        int sum = 0, most = 0;
+        for (int j = lane; j < blocks; j += 64) {
+            const int tiles = block_keys<Shape>(a, ctx, n, j).tiles;
+            sum += tiles;
+            most = max(most, tiles);
+        }
         sum = __builtin_amdgcn_readlane(lanes_scan(sum), 63);
-        if (lane == f) q.tiles = sum;
+        most = (int)lanes_max((float)most);         // below 2^24, or near enough
+        if (lane == f) {
+            q.tiles = sum;
+            q.most = most;
+        }
     }
     return q;
 }
@@ -184,6 +201,7 @@ __device__ __forceinline__ LaneSeq lane_seq(const AttnArgs& a, int c0) {
 // The stretches: `each` tiles and one more in the first `more` of them.
 struct Cut {
     int head_tiles, wgs, each, more;
+    bool whole;
     __device__ __forceinline__ int first(int i) const { return i * each + min(i, more); }
     // the workgroup that has tile g
     __device__ __forceinline__ int owner(int g) const {
@@ -195,19 +213,42 @@ struct Cut {
 template <typename Shape>
 __device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
     Cut c;
+    c.whole = a.whole;
     c.head_tiles = 0;
+    int blocks = 0, most = 0;
     for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
-        q = lane_seq<Shape>(a, c0);
+        q = lane_seq<Shape>(a, c0, c.whole);
         c.head_tiles += __builtin_amdgcn_readlane(lanes_scan(q.tiles), 63);
+        if (a.choose) {
+            blocks += __builtin_amdgcn_readlane(lanes_scan(q.blocks), 63);
+            most = max(most, __builtin_amdgcn_readfirstlane((int)lanes_max((float)q.most)));
+        }
     }
-    const int all = c.head_tiles * a.kv.Hkv;
-    c.wgs = min(a.wgs, all);
+    int all = c.head_tiles * a.kv.Hkv;
+    c.wgs = min(a.whole ? (int)gridDim.x : a.wgs, all);
+    if (a.choose) {
+        // Whole blocks where the longest and half of it on top of the average stay
+        // within the average and what parts and their join cost, in tiles: 5 for
+        // blocks of 32 rows, 16 for larger ones.  (Times with the join, stretches then
+        // whole blocks, head size 128: 16 contexts of a thousand tokens and one row
+        // 26 us and 26, 8 of them 21 and 23; 32 of 500, 8 new, 64 / 8 heads, 38 and 27;
+        // 32 of a thousand 46 and 44; 128 of them 131 and 117; 64 of 500, 32 new, 66 and
+        // 42; one chunk of 2048 tokens without context 95 and 58.)
+        const int average = (int)((unsigned)all / (unsigned)max(a.wgs, 1));
+        if (blocks * a.kv.Hkv <= (int)gridDim.x && max(most, average + most / 2) <= average + (Shape::BM == 32 ? 5 : 16)) {
+            c.whole = true;
+            q.tiles = q.blocks;
+            c.head_tiles = blocks;
+            all = blocks * a.kv.Hkv;
+            c.wgs = all;
+        }
+    }
     // More than one workgroup a compute unit only with eight tiles for each: shorter
     // stretches leave more parts than they save (event times with 512 workgroups and
     // the join, then with 256: 4 contexts of 25 thousand tokens, 8 new, 16 / 2 heads, 6
     // tiles each, 34 + 14.5 and 34 + 9.8 us; 2 of 4000, 32 new, 32 / 8 heads, 2 tiles,
     // 29 + 16.6 and 25 + 12.8; but 16 such, 16 tiles, 68 + 12.1 and 76 + 12.0).
-    if (!a.whole && c.wgs > a.cus && all < 8 * c.wgs) c.wgs = a.cus;
+    if (!c.whole && c.wgs > a.cus && all < 8 * c.wgs) c.wgs = a.cus;
     c.each = c.wgs > 0 ? (int)((unsigned)all / (unsigned)c.wgs) : 0;
     c.more = all - c.each * c.wgs;
     return c;
@@ -221,10 +262,10 @@ struct Place {
 // The block that has tile g of a head.  q: the lanes' sequences if there are no
 // more than 64.
 template <typename Shape>
-__device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, int g, Place& p) {
+__device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, bool whole, int g, Place& p) {
     int before = 0;
     for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
-        if (a.kv.B > 64) q = lane_seq<Shape>(a, c0);
+        if (a.kv.B > 64) q = lane_seq<Shape>(a, c0, whole);
         const int incl = lanes_scan(q.tiles);
         const uint64_t hit = __ballot(before + incl > g);
         if (hit) {
@@ -236,7 +277,7 @@ __device__ __forceinline__ bool find_place(const AttnArgs& a, LaneSeq q, int g, 
             p.blocks = __builtin_amdgcn_readlane(q.blocks, f);
             p.first = before + __builtin_amdgcn_readlane(incl - q.tiles, f);
             p.j = 0;
-            if (a.whole) {
+            if (whole) {
                 // a later block sees more keys: it goes first
                 p.j = p.blocks - 1 - (g - p.first);
                 p.first = g;
@@ -455,22 +496,21 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
     // different heads, so that with eight of them an XCD keeps one head's keys.
     LaneSeq seqs;
     const Cut cut = cut_work<Shape>(a, seqs);
+    const bool blocks_whole = cut.whole;
     int wg = blockIdx.x;
-    if (!a.whole && cut.wgs % 8 == 0 && wg < cut.wgs)
+    if (!blocks_whole && cut.wgs % 8 == 0 && wg < cut.wgs)
         wg = (int)(blockIdx.x % 8) * (cut.wgs / 8) + (int)(blockIdx.x / 8);
     int32_t* split = a.split + 8 * wg;
-    if (wg >= cut.wgs) {
-        if (!a.whole && threadIdx.x == 0) split[0] = -1;
-        return;
-    }
+    if (a.join && wg < a.wgs && (blocks_whole || wg >= cut.wgs) && threadIdx.x == 0) split[0] = -1;
+    if (wg >= cut.wgs) return;
     int g = cut.first(wg), h = 0;
     const int start = g, stop = cut.first(wg + 1);
     Place at;
     at.j = at.blocks = 0;
     while (g < stop) {
-    if (a.whole) {
+    if (blocks_whole) {
         h = g % kv.Hkv;
-        if (!find_place<Shape>(a, seqs, g / kv.Hkv, at)) return;
+        if (!find_place<Shape>(a, seqs, blocks_whole, g / kv.Hkv, at)) return;
         at.first = g - h * cut.head_tiles;      // the block is the whole stretch
     } else if (at.j + 1 < at.blocks) {
         at.first += at.k.tiles;         // the next block of the sequence
@@ -478,9 +518,9 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
         at.k = block_keys<Shape>(a, at.ctx, at.n, at.j);
     } else {
         h = (int)((unsigned)g / (unsigned)cut.head_tiles);
-        if (!find_place<Shape>(a, seqs, g - h * cut.head_tiles, at)) {
+        if (!find_place<Shape>(a, seqs, blocks_whole, g - h * cut.head_tiles, at)) {
             // only where sequences overlap, by more tokens than there are
-            if (g == start && threadIdx.x == 0) split[0] = -1;
+            if (a.join && g == start && threadIdx.x == 0) split[0] = -1;
             return;
         }
     }
@@ -489,10 +529,10 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
     const int b = uni(at.b), s0 = uni(at.s0), n = uni(at.n), ctx = uni(at.ctx), r0 = uni(at.j) * BM;
     const int M = n * a.G, head_kv = uni(h), tiles = uni(at.k.tiles);
     const int first = uni(h * cut.head_tiles + at.first);
-    const int tile0 = a.whole ? 0 : uni(g) - first;
-    const int tile1 = a.whole ? tiles : min(tiles, stop - first);
+    const int tile0 = blocks_whole ? 0 : uni(g) - first;
+    const int tile1 = blocks_whole ? tiles : min(tiles, stop - first);
     const bool whole = tile0 == 0 && tile1 == tiles;
-    if (!a.whole && g == start && threadIdx.x == 0) {
+    if (a.join && !blocks_whole && g == start && threadIdx.x == 0) {
         // the first boundary inside a block tells the join about the block
         const bool cuts = tile0 > 0 && cut.first(wg - 1) <= first;
         split[0] = cuts ? cut.owner(first + tiles - 1) : -1;
@@ -501,7 +541,7 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
         split[3] = r0;
         split[4] = M;
     }
-    g += a.whole ? 1 : tile1 - tile0;
+    g += blocks_whole ? 1 : tile1 - tile0;
     const int t_lo = uni(at.k.t_lo), t_hi = uni(at.k.t_hi);
     const int origin = uni(at.k.origin);
     const int klo = max(uni(at.k.begin), origin + tile0 * KT);

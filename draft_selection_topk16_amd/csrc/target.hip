@@ -99,7 +99,8 @@ df2_status check_rows(const df2_paged_kv* kv, const void* p, int64_t stride, int
 struct AttnPlan {
     int wr = 1;                 // waves of 32 rows in a block
     int bm = 32, kt = 32, gk = 16;
-    int wgs = 1, whole = 0;
+    int wgs = 1, whole = 0;     // workgroups for stretches, or for whole blocks
+    int choose = 0, grid = 1;   // the kernel may take whole blocks by itself; workgroups for either
     bool fits = true;           // 32-bit tile numbers
     size_t part = 0, bytes = 0; // workspace: the parts' outputs, all of it
 };
@@ -186,10 +187,13 @@ AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
     pl.fits = blocks * kv->Hkv * tiles((int64_t)kv->table_width * kv->page_size) < (1LL << 31);
     pl.whole = pl.wr == 8 && rows / pl.bm * kv->Hkv >= 2 * resident;
     if (pl.whole) {
-        pl.wgs = (int)std::min<int64_t>(blocks * kv->Hkv, 0x7FFFFFFF);
+        pl.grid = pl.wgs = (int)std::min<int64_t>(blocks * kv->Hkv, 0x7FFFFFFF);
         return pl;
     }
     pl.wgs = (int)std::min(resident, blocks * kv->Hkv * tiles(max_len));
+    // with fewer blocks a stretch is shorter than any of them
+    pl.choose = blocks * kv->Hkv * 4 >= pl.wgs && blocks * kv->Hkv <= (1 << 30);
+    pl.grid = pl.choose ? std::max(pl.wgs, (int)(blocks * kv->Hkv)) : pl.wgs;
     pl.part = (size_t)2 * pl.wgs * pl.bm * kv->D;
     pl.bytes = pl.wgs > 1 ? (pl.part + (size_t)(4 * pl.bm + 8) * pl.wgs) * sizeof(float) : 0;
     return pl;
@@ -220,10 +224,10 @@ df2_status launch_attend(const AttnPlan& pl, const AttnArgs& a, hipStream_t stre
                                                            hipFuncAttributeMaxDynamicSharedMemorySize, S::kAllLds)).first;
             if (it->second != hipSuccess) return hip_failed(it->second, "hipFuncSetAttribute (attention)");
         }
-        hipLaunchKernelGGL(fn, dim3((unsigned)pl.wgs), dim3(S::kThreads), S::kAllLds, stream, a);
+        hipLaunchKernelGGL(fn, dim3((unsigned)pl.grid), dim3(S::kThreads), S::kAllLds, stream, a);
         return launched("dflash2_paged_attention launch");
     });
-    if (st != DF2_OK || pl.wgs == 1 || pl.whole) return st;
+    if (st != DF2_OK || !a.join) return st;
     hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)(kJoinWgs * (pl.wgs - 1))),
                        dim3(kJoinThreads), 0, stream, a);
     return launched("dflash2_paged_attention join launch");
@@ -283,6 +287,8 @@ df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_
     a.wgs = pl.wgs;
     a.whole = pl.whole;
     a.cus = compute_units();
+    a.join = pl.bytes > 0;
+    a.choose = pl.choose;
     a.inv_g = 1.0 / a.G;
     a.c = (float)((double)scale * 1.4426950408889634);
     return with_type(kv, [&](auto bf16, auto d) {

@@ -68,6 +68,17 @@ ATTENTION = [
     ("empty_and_late", BF, 128, 4, 1, 16, [0, 4, 0, 1], [10, 0, 0, 65], True, 0),
     ("before_the_start", BF, 128, 4, 1, 16, [6, 2], [-3, -7], True, 0),
     ("big_page", BF, 128, 4, 2, 1024, [9], [1500], True, 0),
+    # one tile in all: no workspace
+    ("one_tile", BF, 128, 4, 1, 16, [1], [20], True, 0),
+    ("one_tile_64", BF, 64, 1, 1, 16, [1], [0], True, 0),
+    ("one_tile_f32", F32, 128, 2, 1, 16, [3], [5], False, 0),
+    ("one_tile_256", BF, 256, 8, 1, 16, [2], [3], True, 0),
+    # short blocks, taken whole
+    ("many_short", BF, 128, 32, 8, 16, [1 + i % 3 for i in range(70)], [(37 * i) % 211 for i in range(70)], True, 0),
+    ("many_short_64_f32", F32, 64, 16, 8, 16, [4 + i % 5 for i in range(66)], [(37 * i) % 311 for i in range(66)], False, 0),
+    ("many_short_256", BF, 256, 16, 4, 16, [i % 4 for i in range(40)], [(91 * i) % 300 for i in range(40)], True, 60),
+    ("chunk_from_nothing", BF, 128, 32, 8, 16, [1024], [0], True, 0),
+    ("mixed_lengths", BF, 128, 16, 4, 16, [8, 1, 300, 8, 2], [9000, 3, 0, 40, 700], True, 0),
     ("pages_of_one_token", BF, 128, 8, 2, 1, [3, 1], [5003, 2050], True, 0),
     ("pages_of_one_token_f32_window", F32, 64, 4, 4, 1, [2, 1], [3500, 1], True, 2500),
     ("chunk_small_pages", BF, 128, 32, 8, 2, [4100], [300], True, 0),
