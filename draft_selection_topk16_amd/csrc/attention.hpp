@@ -643,11 +643,11 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
 #pragma unroll
             for (int v = 0; v < 16; ++v) y[v] = 0.f;
         };
+        // sums start where their first product stands, which then takes a constant
         if constexpr (BF16) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) zero(x[ks]);
             run_products<NQ>([&](int u) { return key_operand(slot, u); },
                              [&](int u, u32x4_t kf) {
+                                 if (u < KS) zero(x[u]);
                                  x[u % KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                                      as_bf16x8(kf), as_bf16x8(qf[u / KS]), x[u % KS], 0, 0, 0);
                              });
@@ -659,10 +659,9 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
             static_assert(KS == 1, "one sub-tile");
             constexpr int NA = D <= 128 ? 4 : 2;
             f32x16_t part[NA];
-#pragma unroll
-            for (int i = 0; i < NA; ++i) zero(part[i]);
             run_products<NQ>([&](int u) { return key_operand(slot, u); },
                              [&](int u, u32x4_t kf) {
+                                 if (u < NA) zero(part[u]);
 #pragma unroll
                                  for (int e = 0; e < 4; ++e)
                                      part[u % NA] = __builtin_amdgcn_mfma_f32_32x32x2f32(
