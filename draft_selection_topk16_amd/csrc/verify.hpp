@@ -565,12 +565,11 @@ __device__ __forceinline__ void draw_token(const VerifyArgs& a, VerifyLds& sm, i
     __syncthreads();
     if (w == 0) {
         double target = sm.target;
-        const int at = find_prefix(sm.sums, nch, target);
-        const int e0 = chunk_first(cut, g, vectors, nch, at), e1 = chunk_first(cut, g, vectors, nch, at + 1);
+        const int chosen = g * nch + find_prefix(sm.sums, nch, target), chunks = a.nseg2 * nch;
         const int mine_id = lane < K ? sm.cid[lane] : -1;
-        const uint64_t inside = __ballot(mine_id >= e0 && mine_id < e1);
-        double run = 0.0, odds = 0.0, last_odds = 0.0;
         int pick = -1, last = -1;
+        double run = 0.0, last_odds = 0.0;
+        uint64_t inside = 0;
         // `own` elements of a lane from `first` on, the lanes in order
         auto go_through = [&](const float (&x)[E], int first, int own) {
             double full[E], rest[E], sum = 0.0;
@@ -612,21 +611,44 @@ __device__ __forceinline__ void draw_token(const VerifyArgs& a, VerifyLds& sm, i
             if (lane < n) x[0] = row_value<BF16>(rp, i + lane);
             go_through(x, i + lane, lane < n ? 1 : 0);
         };
-        int i = e0;
-        if (i < cut.head) {
-            one(i, min(cut.head, e1) - i);
-            i = cut.head;
+        // What is left of a range is a difference of two sums: where the candidates in it
+        // hold all of its weight and lose all of it, rounding may leave something, and
+        // where they hold nearly all, nothing.  What is left of an element is exact.  So
+        // where the chosen chunk has no element to draw, the target stands at its border:
+        // the first element of the next chunk that has one is drawn, or, with none behind
+        // it, the last one before it.  visit(j) is the j-th chunk on that way.
+        const auto visit = [&](int j) { return chosen + j < chunks ? chosen + j : chunks - 1 - j; };
+        for (int j = 0; mass && pick < 0 && j < chunks;) {
+            const int at = visit(j), cg = (int)((unsigned)at / (unsigned)nch), ci = at - cg * nch;
+            const int e0 = chunk_first(cut, cg, vectors, nch, ci), e1 = chunk_first(cut, cg, vectors, nch, ci + 1);
+            inside = __ballot(mine_id >= e0 && mine_id < e1);
+            run = 0.0;
+            int i = e0;
+            if (i < cut.head) {
+                one(i, min(cut.head, e1) - i);
+                i = cut.head;
+            }
+            const int vec_end = min(e1, cut.head + cut.nv * E);
+            for (; pick < 0 && i < vec_end; i += 64 * E) {
+                const int first = i + lane * E;
+                float x[E] = {};
+                if (first < vec_end) unpack16<BF16>(*reinterpret_cast<const u32x4_t*>(rp + (size_t)first * SZ), x);
+                go_through(x, first, first < vec_end ? E : 0);
+            }
+            if (pick < 0 && vec_end < e1) one(max(vec_end, e0), e1 - max(vec_end, e0));
+            pick = pick < 0 ? last : pick;
+            if (pick >= 0) break;
+            // on to the next chunk with any weight, 64 looked at at once
+            uint64_t some = 0;
+            for (++j; j < chunks; j += 64) {
+                const int c = visit(min(j + lane, chunks - 1)), of = (int)((unsigned)c / (unsigned)nch);
+                some = __ballot(j + lane < chunks && chunk_of(of, c - of * nch) > 0.0);
+                if (some) break;
+            }
+            if (some) j += __builtin_ctzll(some);
+            target = chosen + j < chunks ? -1.0 : HUGE_VAL;
         }
-        const int vec_end = min(e1, cut.head + cut.nv * E);
-        for (; pick < 0 && i < vec_end; i += 64 * E) {
-            const int first = i + lane * E;
-            float x[E] = {};
-            if (first < vec_end) unpack16<BF16>(*reinterpret_cast<const u32x4_t*>(rp + (size_t)first * SZ), x);
-            go_through(x, first, first < vec_end ? E : 0);
-        }
-        if (pick < 0 && vec_end < e1) one(max(vec_end, e0), e1 - max(vec_end, e0));
-        pick = pick < 0 ? last : pick;
-        odds = last_odds;
+        const double odds = last_odds;
         const bool ok = mass && pick >= 0 && pick < a.V;
         if (!ok) {
             pick = 0;
