@@ -550,7 +550,8 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
     // This lane's row: row col of the wave's 32 (the last row again past the end).
     const int r = r0 + wr * 32 + col;
     const int rc = min(r, M - 1), t = div_g(a, rc), head = head_kv * a.G + rc - t * a.G;
-    const int lim = a.causal ? ctx + t + 1 : khi;                 // first key it does not see
+    // first key it does not see; a token before position 0 sees none
+    const int lim = a.causal || ctx + t < 0 ? ctx + t + 1 : khi;
     const int low = a.window ? ctx + t + 1 - a.window : 0;        // first key it sees
 
     // The query rows, as the products want them: half the columns in each lane.
@@ -676,7 +677,7 @@ __global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) vo
     };
     // Masks the keys that a row does not see (tiles that every row sees whole need
     // none) and returns the row's maximum in units of log2.
-    const int first_lim = min(a.causal ? ctx + t_lo + 1 : khi, khi);
+    const int first_lim = a.causal || ctx + t_lo < 0 ? min(ctx + t_lo + 1, khi) : khi;
     const int last_low = max(a.window ? ctx + t_hi + 1 - a.window : 0, klo);
     const int top = min(lim, khi), bottom = max(low, klo);
     auto mask_and_max = [&](int k0, f32x16_t (&x)[KS]) {

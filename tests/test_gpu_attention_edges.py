@@ -1,0 +1,63 @@
+"""GPU tests of paged attention at the ends of its ranges: positions before the
+first, whole blocks of every head size."""
+import pytest
+import torch
+
+import draft_selection_topk16_amd as df2
+from gpu_util import say
+from target_ref import paged_case
+from test_gpu_target import attend, check_attention
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, NAN = torch.bfloat16, torch.float32, float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    df2.load()
+    df2.device_error()
+    yield
+    torch.cuda.synchronize()
+
+
+BEFORE = [
+    # name, dtype, D, Hq, Hkv, page, new, ctx, window
+    ("few_rows", BF, 128, 4, 1, 16, [6, 2, 8], [-3, -7, -1], 0),
+    ("few_rows_64", BF, 64, 3, 3, 1, [6, 5], [-3, 20], 0),
+    ("few_rows_256", BF, 256, 4, 2, 16, [6, 8], [-3, 40], 0),
+    ("few_rows_f32", F32, 128, 8, 2, 16, [6, 2], [-3, 9], 0),
+    ("window", BF, 128, 8, 2, 16, [9, 8], [-4, -2], 2),
+    ("blocks_of_64", BF, 128, 32, 8, 16, [16, 9], [-5, 2300], 0),
+    ("blocks_of_128_f32", F32, 64, 16, 8, 16, [64, 40], [-9, -30], 0),
+    ("blocks_of_256", BF, 128, 32, 8, 16, [200, 130], [-77, 2500], 0),
+    ("blocks_of_256_window", BF, 64, 32, 8, 16, [300, 130], [-77, -129], 20),
+    ("many_blocks", BF, 64, 32, 8, 16, [4100, 300], [-100, -299], 0),
+    ("split", BF, 128, 8, 2, 16, [5, 3, 4], [-2, 2900, -3], 0),
+]
+
+
+@pytest.mark.parametrize("case", BEFORE, ids=[c[0] for c in BEFORE])
+def test_whole_blocks_before_the_first_position(case):
+    """A token whose position is negative sees nothing and gets 0, in a whole block too."""
+    name, dtype, D, Hq, Hkv, page, new, ctx, window = case
+    say("attention whole block before the start", name)
+    c = paged_case(len(name) * 7 + D, dtype, D, Hq, Hkv, page, new, ctx, garbage=NAN)
+    out = attend(c, causal=False, window=window)
+    check_attention(c, out, False, window)
+    start = c["start"].tolist()
+    for b, at in enumerate(ctx):
+        if at < 0:
+            assert bool((out[start[b]:start[b] + min(-at, new[b])] == 0).all())
+    assert df2.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,new,ctx,window", [(BF, [8, 5], [50, 0], 0), (BF, [70, 3], [45, 31], 0), (BF, [9, 8], [400, 7], 33),
+                                                  (F32, [8, 40], [99, 3], 0)])
+def test_whole_blocks_of_head_size_256(dtype, new, ctx, window):
+    say("attention whole block 256", dtype, new)
+    c = paged_case(new[0] + ctx[0], dtype, 256, 8, 2, 16, new, ctx, garbage=NAN)
+    check_attention(c, attend(c, causal=False, window=window), False, window)
+    assert df2.device_error() == 0
