@@ -47,11 +47,11 @@ struct AppendArgs {
     float eps;
 };
 
-// A new token's sequence (the first whose end lies behind it), its first token,
-// count and context; false if the token belongs to none.  The same in the whole
+// A new token's sequence (the first whose end lies behind it), its first token
+// and context; false if the token belongs to none.  The same in the whole
 // wave; everything about 64 sequences is loaded at once.
 struct TokenSeq {
-    int b, s0, n, ctx;
+    int b, s0, ctx;
 };
 __device__ __forceinline__ bool find_sequence(const PagedKv& kv, int tok, TokenSeq& q) {
     const int lane = lane_id();
@@ -65,8 +65,7 @@ __device__ __forceinline__ bool find_sequence(const PagedKv& kv, int tok, TokenS
             const int f = __builtin_ctzll(hit);
             q.b = c0 + f;
             q.s0 = __builtin_amdgcn_readlane(s0, f);
-            q.n = __builtin_amdgcn_readlane(n, f);
-            q.ctx = inside_table(kv, __builtin_amdgcn_readlane(ctx, f), q.n);
+            q.ctx = __builtin_amdgcn_readlane(ctx, f);
             return q.s0 <= tok;
         }
     }
@@ -111,7 +110,7 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
     // A and B of the query heads, then of the key heads
     __shared__ __attribute__((aligned(16))) float form[T][2][2][D];
     __shared__ float turn[T][D];            // cosines, then sines, of the rot / 2 pairs
-    __shared__ int where[T][3];             // position (of a token that has one), page, sequence or -1
+    __shared__ int where[T][3];             // slot of its page, page or -1, sequence or -1
     const PagedKv& kv = a.kv;
     const int tid = threadIdx.x, lane = lane_id(), w = wave_id();
     const int tok0 = blockIdx.x * T;
@@ -173,11 +172,15 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
     // a wave a token: its place, and its turns
     for (int j = w; j < T; j += kWaves) {
         TokenSeq q;
-        int pos = 0, page = -1, seq = -1;
+        int page = -1, seq = -1;
+        int64_t pos = 0;
+        bool placed = false, behind = false;
         if (tok0 + j < kv.N && find_sequence(kv, tok0 + j, q)) {
             seq = q.b;
-            pos = q.ctx + tok0 + j - q.s0;
-            if (pos >= 0) page = kv.table[(int64_t)q.b * kv.table_stride + (pos >> kv.page_shift)];
+            pos = (int64_t)q.ctx + tok0 + j - q.s0;
+            behind = pos >= (int64_t)kv.table_width << kv.page_shift;
+            placed = pos >= 0 && !behind;
+            if (placed) page = kv.table[(int64_t)q.b * kv.table_stride + (pos >> kv.page_shift)];
         }
         for (int i = lane; i < half; i += 64) {
             const double rev = (double)pos * a.freq[i] * 0.15915494309189535;   // 1 / (2 pi): whole turns drop out
@@ -187,12 +190,11 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
             turn[j][half + i] = s;
         }
         // a token without a place in the cache is not written there
-        if (seq >= 0 && pos >= 0 && (unsigned)page >= (unsigned)kv.num_pages) {
-            if (lane == 0) atomicOr(kv.err, kFlagPage);
-            page = -1;
-        }
+        const bool lost = placed && (unsigned)page >= (unsigned)kv.num_pages;
+        if (lost) page = -1;
         if (lane == 0) {
-            where[j][0] = pos;
+            if (lost || behind) atomicOr(kv.err, lost ? kFlagPage : kFlagLength);
+            where[j][0] = (int)(pos & ((1 << kv.page_shift) - 1));
             where[j][1] = page;
             where[j][2] = seq;
         }
@@ -217,7 +219,7 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs a) {
     for (int j = 0; j < T; ++j) {
         const int tok = tok0 + j;
         if (tok >= kv.N) return;
-        const int page = where[j][1], seq = where[j][2], slot = where[j][0] & ((1 << kv.page_shift) - 1);
+        const int page = where[j][1], seq = where[j][2], slot = where[j][0];
         const int64_t place = (int64_t)page * kv.page_stride + (int64_t)slot * D;
 #pragma unroll 1
         for (int u = u_first; u < units; u += u_step) {

@@ -430,8 +430,9 @@ df2_status dflash2_conv2(const void* x, const void* x_prev, const void* base,
  *                device flag bit 3: nothing is written there, and reads take
  *                page 0 instead
  *   table_width  pages a sequence may have (table_width * page_size <= 2^30);
- *                with ctx_len + new tokens beyond them, flag bit 4 is raised
- *                and ctx_len taken as if the last new token had the last place
+ *                with ctx_len + new tokens beyond them, flag bit 4 is raised: the
+ *                append writes no token whose place they do not have, attention
+ *                takes ctx_len as if the last new token had the last place
  * Token rows of queries, keys, values and outputs hold their heads one after
  * the other ([heads, D]); their stride from token to token is given in
  * elements, a multiple of 16 bytes, so that they may be parts of one row.
@@ -463,7 +464,8 @@ typedef struct df2_paged_kv {
  *   interleaved  pair i is elements (i, i + rot / 2) if 0, else (2i, 2i + 1)
  *   out_q   token rows of Hq heads; may be q itself with q's stride
  * fp32 arithmetic (angles reduced in fp64), one rounding at the store.  A
- * token with a negative position is not written to the cache.
+ * token with a negative position, or one behind the page table, is not written to
+ * the cache; its query is turned by that position all the same.
  */
 df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_stride,
                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,
