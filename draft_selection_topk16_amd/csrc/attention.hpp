@@ -165,7 +165,8 @@ __device__ __forceinline__ LaneSeq lane_seq(const AttnArgs& a, int c0, bool whol
     const int lane = lane_id(), i = c0 + lane;
     if (i < a.kv.B) {
         seq_tokens(a.kv, i, q.s0, q.n);
-        q.ctx = inside_table(a.kv, a.kv.ctx[i], q.n);
+        const int ctx = a.kv.ctx[i];
+        if (q.n > 0) q.ctx = inside_table(a.kv, ctx, q.n);     // without new tokens, any length is right
         q.blocks = (int)((unsigned)(q.n * a.G + Shape::BM - 1) / (unsigned)Shape::BM);
     }
     if (whole) {

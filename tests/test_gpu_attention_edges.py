@@ -61,3 +61,29 @@ def test_whole_blocks_of_head_size_256(dtype, new, ctx, window):
     c = paged_case(new[0] + ctx[0], dtype, 256, 8, 2, 16, new, ctx, garbage=NAN)
     check_attention(c, attend(c, causal=False, window=window), False, window)
     assert df2.device_error() == 0
+
+
+def test_slots_without_new_tokens_may_hold_any_length():
+    """A captured batch has empty slots whose lengths are stale: nothing is read for
+    them and no flag is raised, in the append as in the attention."""
+    say("attention empty slots")
+    c = paged_case(70, BF, 128, 8, 2, 16, [0, 3, 0, 2, 0], [0, 40, 0, 7, 0], garbage=NAN)
+    want = attend(c)
+    stale = dict(c, ctx=torch.tensor([1 << 30, 40, -(1 << 31), 7, (1 << 31) - 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(attend(stale), want)
+    assert df2.device_error() == 0
+    k = torch.randn((5, 2, 128), device="cuda").to(BF)
+    df2.kv_append(k, k, c["k_cache"], c["v_cache"], c["table"], stale["ctx"], c["start"])
+    assert df2.device_error() == 0
+
+
+@pytest.mark.parametrize("ctx", [(1 << 31) - 1, 48, -(1 << 31)])
+def test_lengths_at_the_ends_of_their_type(ctx):
+    """Beyond the page table: as if the last new token had the last place; far below
+    0: zeros."""
+    say("attention lengths", ctx)
+    c = paged_case(71, BF, 64, 4, 2, 16, [3, 2], [45, 20])
+    far = dict(c, ctx=torch.tensor([ctx, 20], dtype=torch.int32, device="cuda"))
+    out, want = attend(far), attend(c)
+    assert df2.device_error() == (16 if ctx > 0 else 0)
+    assert torch.equal(out, want if ctx > 0 else torch.cat((torch.zeros_like(want[:3]), want[3:])))
