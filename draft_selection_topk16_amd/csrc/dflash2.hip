@@ -668,6 +668,9 @@ __global__ __launch_bounds__(kWG) void k_fill_zero(uint32_t* __restrict__ p, int
     if (i < n) p[i] = 0u;
 }
 
+// Clears bits of a flag word that kernels of other streams may be raising flags in.
+__global__ void k_clear_bits(uint32_t* word, uint32_t bits) { atomicAnd(word, ~bits); }
+
 // Scratch of dflash2_select_noalloc: one copy per device, zero when the
 // module loads, kept until the process ends.  Host code uses only the
 // address hipGetSymbolAddress returns for the current device, never the
@@ -1640,13 +1643,15 @@ df2_status dflash2_device_error(hipStream_t stream, uint32_t* flags) {
     }
     uint32_t sv = 0;
     if (sptr) {
-        // flags of no-allocation calls on this device
+        // Flags of no-allocation calls and of the target's side on this device, by any
+        // stream: only the bits that were read are cleared, so that one raised
+        // meanwhile stays for a later call.
         if ((e = hipMemcpy(&sv, sptr, 4, hipMemcpyDeviceToHost)) != hipSuccess)
             return hip_fail(e, "hipMemcpy flags");
         if (sv) {
-            const uint32_t zero = 0;
-            if ((e = hipMemcpy(sptr, &zero, 4, hipMemcpyHostToDevice)) != hipSuccess)
-                return hip_fail(e, "hipMemcpy flags");
+            hipLaunchKernelGGL(k_clear_bits, dim3(1), dim3(1), 0, stream, reinterpret_cast<uint32_t*>(sptr), sv);
+            if ((e = hipGetLastError()) != hipSuccess || (e = hipStreamSynchronize(stream)) != hipSuccess)
+                return hip_fail(e, "clearing the flags");
         }
     }
     if (!ptr) {

@@ -566,11 +566,12 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
  * replaced by 0; bit 2: a row merge of dflash2_select gave up waiting for
  * its gate rows (launches 1 or 2 only), which only a fault elsewhere can
  * cause, and its scores are then unreliable; bits 3 to 6: the paged operators
- * and dflash2_verify, see there; theirs are kept once a device and reported
- * on any of its streams).  A raised flag can leave a late gate arrival
- * counted in the stream's scratch, so after reporting one the next call on
- * that stream clears all its arrival counters before it launches.  Returns
- * DF2_OK, or DF2_EHIP.
+ * and dflash2_verify, see there; theirs, and those of dflash2_select_noalloc,
+ * are kept once a device and reported on any of its streams: work that still
+ * runs on another stream may raise some that a later call reports).  A raised
+ * flag can leave a late gate arrival counted in the stream's scratch, so after
+ * reporting one the next call on that stream clears all its arrival counters
+ * before it launches.  Returns DF2_OK, or DF2_EHIP.
  */
 df2_status dflash2_device_error(hipStream_t stream, uint32_t* flags);
 
