@@ -6,7 +6,9 @@ then enqueues with little host work on the stream that is current when it is
 called, and a function that prepares and calls.  Refill the tensors of a
 prepared call in place between calls; calls of one prepared call (and replays
 of graphs that captured it) share its outputs and workspace and must be
-ordered.  The arithmetic is in the HIP kernels (include/dflash2.h).
+ordered.  It may be dropped while it still runs on any stream that it was called
+on, but must be kept as long as a graph that captured it is replayed.  The
+arithmetic is in the HIP kernels (include/dflash2.h).
 """
 from __future__ import annotations
 
@@ -39,14 +41,27 @@ class _Prepared:
                            for a, kind in zip(args, fn.argtypes))
         self._fn, self._keep, self._out = fn, keep, out
         self._index = device.index if device.index is not None else torch.cuda.current_device()
+        self._streams = {_raw_stream(self._index)}      # that the allocator knows to use the tensors
+
+    def _use_on(self, index: int, stream: int) -> None:
+        """Tells the allocator of another stream than the one that the tensors were made
+        on: their memory is not given away while a call runs there."""
+        current = torch.cuda.current_stream(index)
+        for t in self._keep:
+            if t is not None:
+                t.record_stream(current)
+        self._streams.add(stream)
 
     def __call__(self):
         index = self._index
+        stream = _raw_stream(index)
+        if stream not in self._streams:
+            self._use_on(index, stream)
         if _current_device() == index:
-            status = self._fn(*self._args, _raw_stream(index))
+            status = self._fn(*self._args, stream)
         else:
             with torch.cuda.device(index):
-                status = self._fn(*self._args, _raw_stream(index))
+                status = self._fn(*self._args, stream)
         if status:
             _check(status)
         return self._out
