@@ -459,6 +459,14 @@ struct AttnShape {
     static constexpr int kMergeBytes = WK > 1 ? kWaves * (32 * D * 4 + 256) + BM * 8 : 0;
     static constexpr int kLds = NS * kStage > kMergeBytes ? NS * kStage : kMergeBytes;   // tiles, or the merge
     static constexpr int kAllLds = kLds + 4 * kPageIds;
+    // Waves of a SIMD: two where the registers of a row of D values leave room for them.
+    // (With two counted everywhere, twice the stretches were cut: blocks of 128 rows,
+    // 8 sequences after 6000 tokens, bf16 256 138 us and 116, fp32 128 251 and 239.)
+    static constexpr int kSimdWaves = Tile::kRow <= 256 ? 2 : 1;
+    // workgroups resident on a compute unit, by LDS and by registers
+    static constexpr int kResident = 160 * 1024 / kAllLds < 4 * kSimdWaves / kWaves ? 160 * 1024 / kAllLds
+                                                                                    : 4 * kSimdWaves / kWaves;
+    static_assert(kResident >= 1, "a workgroup fits a compute unit");
     static_assert(kTileBytes % (1024 * kWaves) == 0, "every wave brings whole loads");
     static_assert(kAhead < 64, "the counter of loads in flight");
     static_assert(kAllLds <= 160 * 1024, "LDS of a compute unit");
@@ -480,7 +488,7 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float (&x)[4
 }
 
 template <bool BF16, int D, int WR, int WK, int KS, int NS>
-__global__ __launch_bounds__(64 * WR * WK, D * (BF16 ? 2 : 4) <= 256 ? 2 : 1) void k_attend(AttnArgs a) {
+__global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::kSimdWaves)) void k_attend(AttnArgs a) {
     using Shape = AttnShape<BF16, D, WR, WK, KS, NS>;
     using Tile = AttnTile<BF16, D>;
     constexpr int RB = Tile::kRow, CH = Tile::kChunks, KT = Shape::KT, BM = Shape::BM;

@@ -176,7 +176,7 @@ AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
                 pl.bm = S::BM;
                 pl.kt = S::KT;
                 pl.gk = S::kGroupKeys;
-                per_cu = std::max(1, std::min(160 * 1024 / S::kAllLds, 8 / S::kWaves));
+                per_cu = S::kResident;
                 return 0;
             });
         });
