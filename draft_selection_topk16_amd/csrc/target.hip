@@ -161,7 +161,9 @@ auto with_type(const df2_paged_kv* kv, F&& f) {
 // tiles, 49 and 51).  As many workgroups as are resident at once (fewer where max_len
 // says that there are fewer tiles).  Whole blocks from two for each resident
 // workgroup on: there is then no part to leave and join, and the end is short
-// against the rest.
+// against the rest.  A window is not counted: planned with the tiles that it leaves, 32
+// new tokens after 100000 in a window of 1024, 32 / 8 heads, took 20.1 us (blocks of 32
+// rows) and not 18.6 (128); a chunk of 2048 in a window of 4096 143 us either way.
 AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
     AttnPlan pl;
     const int64_t rows = (int64_t)kv->N * (kv->Hq / kv->Hkv);

@@ -483,8 +483,9 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
  *           counts); a token whose position is negative sees none and gets 0
  *   scale   positive and finite
  *   max_len an upper estimate of ctx_len + n over the batch for the launch
- *           plan, 0: table_width * page_size.  Only the order in which partial
- *           sums are added depends on it, so it need not be true.
+ *           plan, 0: table_width * page_size.  Speed and the order in which
+ *           partial sums are added depend on it, nothing else, so it need not be
+ *           true; a near one is faster where there are few tokens.
  *   q, out  token rows of Hq heads (dtype); out must not overlap q
  *   workspace  dflash2_paged_attention_workspace(kv, max_len) bytes (0: may be
  *           NULL), 16-byte aligned
