@@ -93,6 +93,32 @@ df2_status check_rows(const df2_paged_kv* kv, const void* p, int64_t stride, int
     return DF2_OK;
 }
 
+// Token rows as the arguments give them: stride and heads * D in elements.
+struct TokenRows {
+    const void* p;
+    int64_t stride;
+    int heads;
+};
+// Whether some row of one shares memory with a row of the other.  (Rows of both may
+// be parts of the same wider rows.)
+bool rows_meet(const df2_paged_kv* kv, const TokenRows& a, const TokenRows& b) {
+    const int64_t size = kv->dtype == DF2_BF16 ? 2 : 4, last = kv->N - 1;
+    const int64_t sa = a.stride * size, wa = (int64_t)a.heads * kv->D * size;
+    const int64_t sb = b.stride * size, wb = (int64_t)b.heads * kv->D * size;
+    const int64_t d = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
+    if (d >= last * sa + wa || -d >= last * sb + wb) return false;
+    if (sa == sb) {
+        const int64_t m = ((d % sa) + sa) % sa;         // where b's rows begin within a's stride
+        return m < wa || sa - m < wb;
+    }
+    for (int64_t i = 0; i <= last; ++i) {
+        const int64_t x = i * sa - d;                   // a's row against b's first
+        const int64_t j = x < wb ? 0 : (x - wb) / sb + 1;       // b's first row that ends behind its beginning
+        if (j <= last && j * sb < x + wa) return true;
+    }
+    return false;
+}
+
 // ----------------------------------------------------------------------------
 // Attention.
 // ----------------------------------------------------------------------------
@@ -272,6 +298,8 @@ df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_
                                              " bytes; the call needs " + std::to_string(pl.bytes));
         if (!aligned(workspace, 16)) return fail_with(DF2_EINVAL, "workspace must be 16-byte aligned");
     }
+    if (rows_meet(kv, {q, q_stride, kv->Hq}, {out, out_stride, kv->Hq}))
+        return fail_with(DF2_EINVAL, "out must not overlap q");
     if ((st = device_flag_word(&a.kv.err)) != DF2_OK) return st;
     a.q = q;
     a.k = kv->k_cache;
@@ -328,6 +356,12 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
     if (!aligned(q_norm, 16) || !aligned(k_norm, 16))
         return fail_with(DF2_EINVAL, "q_norm and k_norm must be 16-byte aligned");
     if (!aligned(rope_freq, 8)) return fail_with(DF2_EINVAL, "rope_freq must be 8-byte aligned");
+    if (q) {
+        const TokenRows out = {out_q, out_q_stride, kv->Hq};
+        if ((q != out_q && rows_meet(kv, {q, q_stride, kv->Hq}, out)) || rows_meet(kv, {k, k_stride, kv->Hkv}, out) ||
+            rows_meet(kv, {v, v_stride, kv->Hkv}, out))
+            return fail_with(DF2_EINVAL, "out_q must not overlap q (unless it is q), k or v");
+    }
     if ((st = device_flag_word(&a.kv.err)) != DF2_OK) return st;
     a.q = q;
     a.k = k;

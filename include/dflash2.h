@@ -462,7 +462,8 @@ typedef struct df2_paged_kv {
  *   rope_freq [rot / 2] double  radians a position; rot: leading elements of a
  *           head that are rotated, a multiple of 16 (0: none, rope_freq unused)
  *   interleaved  pair i is elements (i, i + rot / 2) if 0, else (2i, 2i + 1)
- *   out_q   token rows of Hq heads; may be q itself with q's stride
+ *   out_q   token rows of Hq heads; may be q itself with q's stride, else it must
+ *           not overlap q, k or v (DF2_EINVAL)
  * fp32 arithmetic (angles reduced in fp64), one rounding at the store.  A
  * token with a negative position, or one behind the page table, is not written to
  * the cache; its query is turned by that position all the same.
@@ -486,7 +487,7 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
  *           plan, 0: table_width * page_size.  Speed and the order in which
  *           partial sums are added depend on it, nothing else, so it need not be
  *           true; a near one is faster where there are few tokens.
- *   q, out  token rows of Hq heads (dtype); out must not overlap q
+ *   q, out  token rows of Hq heads (dtype); out must not overlap q (DF2_EINVAL)
  *   workspace  dflash2_paged_attention_workspace(kv, max_len) bytes (0: may be
  *           NULL), 16-byte aligned
  * Scores, softmax statistics and sums are fp32; bf16 probabilities are
