@@ -1489,7 +1489,7 @@ df2_status dflash2_draft_rows(const float* S, const int32_t* cand_idx, const int
     if (P < 1 || P > kMaxP) return fail(DF2_EINVAL, "P must be in [1, 64]");
     if (K < 1 || K > kMaxK) return fail(DF2_EINVAL, "K must be in [1, 64]");
     if (B == 0) return DF2_OK;
-    if ((int64_t)B * P > 0x7FFFFFFF) return fail(DF2_EUNSUPPORTED, "too many rows");
+    if ((int64_t)B * P * 64 > 0xFFFFFFFF) return fail(DF2_EUNSUPPORTED, "too many rows");     // threads of a launch
     if (!S || !cand_idx || !path || !out_rows) return fail(DF2_EINVAL, "NULL pointer argument");
     if (((uintptr_t)S & 3u) || ((uintptr_t)cand_idx & 3u) || ((uintptr_t)path & 3u) || ((uintptr_t)out_rows & 3u))
         return fail(DF2_EINVAL, "arguments must be 4-byte aligned");

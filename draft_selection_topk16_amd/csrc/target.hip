@@ -28,6 +28,9 @@ using namespace df2::host;
 
 namespace {
 
+// Threads of a launch along one dimension.
+constexpr int64_t kMostThreads = 0xFFFFFFFF;
+
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 df2_status launched(const char* what) {
@@ -195,7 +198,7 @@ AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
     const int64_t rows = (int64_t)kv->N * (kv->Hq / kv->Hkv);
     const int64_t seqs = std::min(kv->B, kv->N);
     const int64_t each = (rows + seqs - 1) / seqs;
-    int per_cu = 1;
+    int per_cu = 1, threads = 64;
     const auto tiles = [&](int64_t len) { return (len + pl.gk + pl.kt - 1) / pl.kt; };
     for (pl.wr = each <= 32 ? 1 : each <= 64 ? 2 : each <= 128 ? 4 : 8;; pl.wr /= 2) {
         with_type(kv, [&](auto bf16, auto d) {
@@ -205,6 +208,7 @@ AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
                 pl.kt = S::KT;
                 pl.gk = S::kGroupKeys;
                 per_cu = S::kResident;
+                threads = S::kThreads;
                 return 0;
             });
         });
@@ -213,14 +217,15 @@ AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
     const int64_t blocks = rows / pl.bm + seqs;     // one more in each sequence that has tokens
     const int64_t resident = (int64_t)compute_units() * per_cu;
     pl.fits = blocks * kv->Hkv * tiles((int64_t)kv->table_width * kv->page_size) < (1LL << 31);
-    pl.whole = pl.wr == 8 && rows / pl.bm * kv->Hkv >= 2 * resident;
+    const bool launchable = blocks * kv->Hkv * threads <= kMostThreads;     // a workgroup a block
+    pl.whole = pl.wr == 8 && rows / pl.bm * kv->Hkv >= 2 * resident && launchable;
     if (pl.whole) {
-        pl.grid = pl.wgs = (int)std::min<int64_t>(blocks * kv->Hkv, 0x7FFFFFFF);
+        pl.grid = pl.wgs = (int)(blocks * kv->Hkv);
         return pl;
     }
     pl.wgs = (int)std::min(resident, blocks * kv->Hkv * tiles(max_len));
     // with fewer blocks a stretch is shorter than any of them
-    pl.choose = blocks * kv->Hkv * 4 >= pl.wgs && blocks * kv->Hkv <= (1 << 30);
+    pl.choose = blocks * kv->Hkv * 4 >= pl.wgs && launchable;
     pl.grid = pl.choose ? std::max(pl.wgs, (int)(blocks * kv->Hkv)) : pl.wgs;
     pl.part = (size_t)2 * pl.wgs * pl.bm * kv->D;
     pl.bytes = pl.wgs > 1 ? (pl.part + (size_t)(4 * pl.bm + 8) * pl.wgs) * sizeof(float) : 0;
@@ -342,6 +347,7 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
         return fail_with(DF2_EUNSUPPORTED, "rot must be a multiple of 16 in [0, D]");
     if (!(eps >= 0.f) || !std::isfinite(eps)) return fail_with(DF2_EINVAL, "eps must be finite and >= 0");
     if (kv->B == 0 || kv->N == 0) return DF2_OK;
+    if (((int64_t)kv->N + 3) / 4 * 256 > kMostThreads) return fail_with(DF2_EUNSUPPORTED, "N above 2^26 - 4");
     if (!k || !v || (rot > 0 && !rope_freq)) return fail_with(DF2_EINVAL, "NULL pointer argument");
     if (!q != !out_q) return fail_with(DF2_EINVAL, "q and out_q come together");
     if (!q && q_norm) return fail_with(DF2_EINVAL, "q_norm without q");
@@ -467,7 +473,7 @@ df2_status check_verify(const df2_verify_dims* d) {
     if (d->V < 1) return fail_with(DF2_EINVAL, "V < 1");
     if (d->V > (1 << 29)) return fail_with(DF2_EUNSUPPORTED, "V above 2^29");
     if (d->K < 1 || d->K > 64 || d->K > d->V) return fail_with(DF2_EINVAL, "K must be in [1, min(V, 64)]");
-    if ((int64_t)d->B * (d->P + 1) * kVerifySegs > 0x7FFFFFFF)
+    if ((int64_t)d->B * (d->P + 1) * kWG > kMostThreads)
         return fail_with(DF2_EUNSUPPORTED, "B * (P + 1) too large");
     return DF2_OK;
 }

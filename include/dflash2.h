@@ -339,7 +339,7 @@ df2_status dflash2_sample_walk(const float* S, const int32_t* cand_idx,
  * temperature of S[b][t][i], i the rank of path[b][t - 1] in cand_idx[b][t - 1]
  * (row 0 at t == 0, and for a token that is no candidate).
  *   S [B, P, K, K] float, cand_idx [B, P, K] int32, path [B, P] int32,
- *   out_rows [B, P, K] float
+ *   out_rows [B, P, K] float;  B P < 2^26
  */
 df2_status dflash2_draft_rows(const float* S, const int32_t* cand_idx, const int32_t* path,
                               int32_t B, int32_t P, int32_t K, float temperature,
@@ -466,7 +466,7 @@ typedef struct df2_paged_kv {
  *           not overlap q, k or v (DF2_EINVAL)
  * fp32 arithmetic (angles reduced in fp64), one rounding at the store.  A
  * token with a negative position, or one behind the page table, is not written to
- * the cache; its query is turned by that position all the same.
+ * the cache; its query is turned by that position all the same.  N <= 2^26 - 4.
  */
 df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_stride,
                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -509,7 +509,7 @@ typedef enum { DF2_TARGET_LOGITS = 0, DF2_TARGET_PROBS = 1 } df2_target_kind;
 /*
  * Sizes of a verification: B sequences (0 enqueues nothing), P drafted
  * positions (1 .. 64), vocabulary V (<= 2^29), K candidates a position
- * (1 .. min(V, 64)); dtype and kind of the target rows.
+ * (1 .. min(V, 64)); dtype and kind of the target rows.  B (P + 1) < 2^24.
  */
 typedef struct df2_verify_dims {
     int32_t B, P, V, K;

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import draft_selection_topk16_amd as df2
-from draft_selection_topk16_amd.binding import PagedKv
+from draft_selection_topk16_amd.binding import PagedKv, VerifyDims
 
 F32, BF16 = 0, 1
 
@@ -35,3 +35,20 @@ def test_no_more_stretches_than_workgroups_that_run_at_once(dtype, D, n, bm, per
     """By LDS: two stages of keys and values.  By registers: heads of 512 bytes and more
     leave one wave a SIMD, so one workgroup of four waves a compute unit."""
     assert workspace(kv(4, 4 * n, 32, 8, D, dtype)) == parts(256 * per_cu, bm, D)
+
+
+def test_sizes_beyond_a_launch_are_refused():
+    """A launch takes fewer than 2^32 threads: these sizes, small enough for memory,
+    would need more."""
+    lib, at = df2.load(), 0x100000
+    k = kv(1, (1 << 26) - 3, 1, 1, 64, BF16)
+    assert lib.dflash2_kv_append(ctypes.byref(k), None, 0, at, 64, at, 64, None, None, 1e-6, None, 0, 0, None, 0, None) == 2
+    assert b"2^26" in lib.dflash2_last_error()
+    for B, P in ((1 << 23, 1), (1 << 21, 7)):
+        d = VerifyDims(B, P, 8, 1, BF16, 0)
+        assert lib.dflash2_verify_workspace(ctypes.byref(d)) == 0
+        assert lib.dflash2_verify(ctypes.byref(d), at, at, at, at, None, 1.0, at, at, at, at, at, 1 << 40, None) == 2
+        assert b"too large" in lib.dflash2_last_error()
+        assert lib.dflash2_verify_workspace(ctypes.byref(VerifyDims(B - 1, P, 8, 1, BF16, 0))) > 0
+    assert lib.dflash2_draft_rows(at, at, at, 1 << 20, 64, 1, 1.0, at, None) == 2
+    assert b"too many" in lib.dflash2_last_error()
