@@ -67,6 +67,13 @@ class _Prepared:
         return self._out
 
 
+def _int32(**sizes: int) -> None:
+    """ctypes would cut a larger number down to 32 bits."""
+    for name, x in sizes.items():
+        if not -2**31 <= x < 2**31:
+            raise ValueError("%s = %d does not fit 32 bits" % (name, x))
+
+
 def _ints(t: torch.Tensor, name: str, shape) -> torch.Tensor:
     if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
         raise ValueError("%s must be int32 %s" % (name, list(shape)))
@@ -108,6 +115,7 @@ def _descriptor(k_cache, v_cache, block_table, ctx_len, tok_start, N: int, Hq: i
         raise ValueError("block_table must be a GPU tensor")
     if width > 1 and block_table.stride(1) != 1:
         raise ValueError("block_table: a sequence's row must be contiguous")
+    _int32(N=N, num_pages=pages, table_width=width)
     return PagedKv(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), _dev(ctx_len, "ctx_len"),
                    _dev(tok_start, "tok_start"), k_cache.stride(0) if pages > 1 else dense[0],
                    block_table.stride(0) if B > 1 else width, B, N, Hq, Hkv, D, page, pages, width,
@@ -172,6 +180,8 @@ class PreparedAttention(_Prepared):
                  causal: bool = True, window: int = 0, max_len: Optional[int] = None,
                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
         lib = load()
+        length = min(int(max_len), 2**31 - 1) if max_len is not None else 0
+        _int32(window=int(window), max_len=length)
         N, Hq, D = q.shape
         self.kv = kv = _descriptor(k_cache, v_cache, block_table, ctx_len, tok_start, N, Hq)
         dt = k_cache.dtype
@@ -181,7 +191,6 @@ class PreparedAttention(_Prepared):
         if out is None:
             out = torch.empty((N, Hq, D), dtype=dt, device=q.device)
         out_stride = _rows(out, "out", N, Hq, D, dt)
-        length = int(max_len) if max_len is not None else 0
         need = lib.dflash2_paged_attention_workspace(ctypes.byref(kv), length)
         if workspace is None:
             workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
@@ -210,6 +219,7 @@ class PreparedVerify(_Prepared):
         if target.dim() != 3 or target.shape[1] < 2:
             raise ValueError("target must be [B, P + 1, V]")
         B, P, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+        _int32(B=B, V=V)
         _ints(path, "path", (B, P))
         K = 1
         if cand is not None:
