@@ -710,9 +710,17 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::
     };
 
     // exp2 of the scores over the row's maximum, into the row's sum and packed for
-    // the second product: bf16 (one rounding, relative 2^-9 at most a value; the sum
-    // keeps the fp32 values), or as they are.
-    constexpr int PN = BF16 ? 8 : 16;
+    // the second product: as they are in fp32; in bf16 as a high part, their rounding
+    // (off by 2^-8 of a value at most), and in blocks of up to 64 rows a low part, what
+    // the rounding left, rounded likewise: 16 bits in all.  The sum keeps the fp32
+    // values.  The low part doubles the second product, which few rows have time for
+    // (without and with it: 1 row 10.8 and 10.9 us, 32 contexts of 64 rows 158 and 164,
+    // 16 after 1000 23.3 and 23.6, head size 256 61.5 and 64.2); blocks of 128 rows lose a
+    // tenth by it (79 and 87) and prompt chunks more (690 and 940), so there the weights
+    // are rounded.  Outputs against fp64, relative: 2.1e-3 without it, 1.7e-3, the
+    // rounding of the output alone, with it.
+    constexpr bool kLow = BF16 && WR <= 2;
+    constexpr int PN = BF16 ? (kLow ? 16 : 8) : 16;
     auto weights = [&](const f32x16_t (&x)[KS], uint32_t (&p)[KS][PN]) {
         const float ms = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -724,12 +732,17 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::
                 l += e[v];
             }
 #pragma unroll
-            for (int v = 0; v < PN; ++v) {
-                if constexpr (BF16)
-                    p[ks][v] = __builtin_bit_cast(uint32_t, __builtin_convertvector(
-                        (f32x2_t){e[2 * v], e[2 * v + 1]}, bf16x2_t));
-                else
+            for (int v = 0; v < (BF16 ? 8 : 16); ++v) {
+                if constexpr (BF16) {
+                    const auto pack = [](float x0, float x1) {
+                        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){x0, x1}, bf16x2_t));
+                    };
+                    const uint32_t high = pack(e[2 * v], e[2 * v + 1]);
+                    p[ks][v] = high;
+                    if constexpr (kLow) p[ks][8 + v] = pack(e[2 * v] - bf16_lo(high), e[2 * v + 1] - bf16_hi(high));
+                } else {
                     p[ks][v] = __float_as_uint(e[v]);
+                }
             }
         }
     };
@@ -763,9 +776,12 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::
     };
     auto value_product = [&](int u, u32x4_t vf, const uint32_t (&p)[KS][PN]) {
         const int d = u % DB, j = u / DB;
-        const uint32_t* w4 = &p[j / 2][(j & 1) * 4];
-        const u32x4_t pf = {w4[0], w4[1], w4[2], w4[3]};
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vf), as_bf16x8(pf), o[d], 0, 0, 0);
+#pragma unroll
+        for (int part = 0; part < (kLow ? 2 : 1); ++part) {
+            const uint32_t* w4 = &p[j / 2][8 * part + (j & 1) * 4];
+            const u32x4_t pf = {w4[0], w4[1], w4[2], w4[3]};
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vf), as_bf16x8(pf), o[d], 0, 0, 0);
+        }
     };
     auto add_values = [&](int slot, const uint32_t (&p)[KS][PN]) {
         if constexpr (BF16) {

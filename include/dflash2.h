@@ -484,14 +484,17 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
  *           counts); a token whose position is negative sees none and gets 0
  *   scale   positive and finite
  *   max_len an upper estimate of ctx_len + n over the batch for the launch
- *           plan, 0: table_width * page_size.  Speed and the order in which
- *           partial sums are added depend on it, nothing else, so it need not be
- *           true; a near one is faster where there are few tokens.
+ *           plan, 0: table_width * page_size.  Speed and roundings (the order in
+ *           which partial sums are added, the size of the blocks) depend on it,
+ *           nothing else, so it need not be true; a near one is faster where there
+ *           are few tokens.
  *   q, out  token rows of Hq heads (dtype); out must not overlap q (DF2_EINVAL)
  *   workspace  dflash2_paged_attention_workspace(kv, max_len) bytes (0: may be
  *           NULL), 16-byte aligned
- * Scores, softmax statistics and sums are fp32; bf16 probabilities are
- * rounded to bf16 for the second product.  Keys and values that a token of
+ * Scores, softmax statistics and sums are fp32.  The probabilities of bf16 calls
+ * enter the second product with 16 bits (a bf16 high part and a low one) in blocks
+ * of up to 64 rows (tokens of a sequence times Hq / Hkv, on average), and rounded
+ * to bf16 in larger ones, as of prompt chunks.  Keys and values that a token of
  * the batch sees must be finite; whatever else stands in the pages is not
  * used.  The work is counted in tiles of 32 to 128 keys: (N * Hq / Hkv / 32 + B)
  * * Hkv times the tiles of a whole page table must stay below 2^31
