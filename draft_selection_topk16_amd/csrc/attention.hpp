@@ -155,16 +155,18 @@ __device__ __forceinline__ BlockKeys block_keys(const AttnArgs& a, int ctx, int 
 constexpr int kLaneBlocks = 4;
 
 // A lane's sequence: its tokens, blocks and length on the line, and the tiles of its
-// longest block.
+// longest block.  falls: the next sequence's tokens do not begin behind it.
 struct LaneSeq {
     int s0, n, ctx, blocks, tiles, most;
+    bool falls;
 };
 template <typename Shape>
 __device__ __forceinline__ LaneSeq lane_seq(const AttnArgs& a, int c0, bool whole) {
-    LaneSeq q = {0, 0, 0, 0, 0, 0};
+    LaneSeq q = {0, 0, 0, 0, 0, 0, false};
     const int lane = lane_id(), i = c0 + lane;
     if (i < a.kv.B) {
         seq_tokens(a.kv, i, q.s0, q.n);
+        q.falls = a.kv.start[i + 1] < a.kv.start[i];
         const int ctx = a.kv.ctx[i];
         if (q.n > 0) q.ctx = inside_table(a.kv, ctx, q.n);     // without new tokens, any length is right
         q.blocks = (int)((unsigned)(q.n * a.G + Shape::BM - 1) / (unsigned)Shape::BM);
@@ -217,13 +219,21 @@ __device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
     c.whole = a.whole;
     c.head_tiles = 0;
     int blocks = 0, most = 0;
+    uint64_t falls = 0;
     for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
         q = lane_seq<Shape>(a, c0, c.whole);
+        falls |= __ballot(q.falls);
         c.head_tiles += __builtin_amdgcn_readlane(lanes_scan(q.tiles), 63);
         if (a.choose) {
             blocks += __builtin_amdgcn_readlane(lanes_scan(q.blocks), 63);
             most = max(most, __builtin_amdgcn_readfirstlane((int)lanes_max((float)q.most)));
         }
+    }
+    // Sequences that overlap could make a line of any length, beyond what a tile's
+    // number holds: no work then, and a flag.
+    if (falls) {
+        if (lane_id() == 0) atomicOr(a.kv.err, kFlagLength);
+        blocks = c.head_tiles = 0;
     }
     int all = c.head_tiles * a.kv.Hkv;
     c.wgs = min(a.whole ? (int)gridDim.x : a.wgs, all);
@@ -527,11 +537,7 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::
         at.k = block_keys<Shape>(a, at.ctx, at.n, at.j);
     } else {
         h = (int)((unsigned)g / (unsigned)cut.head_tiles);
-        if (!find_place<Shape>(a, seqs, blocks_whole, g - h * cut.head_tiles, at)) {
-            // only where sequences overlap, by more tokens than there are
-            if (a.join && g == start && threadIdx.x == 0) split[0] = -1;
-            return;
-        }
+        if (!find_place<Shape>(a, seqs, blocks_whole, g - h * cut.head_tiles, at)) return;
     }
     // the same in every lane; said so, they live in scalar registers
     const auto uni = [](int x) { return __builtin_amdgcn_readfirstlane(x); };

@@ -420,9 +420,10 @@ df2_status dflash2_conv2(const void* x, const void* x_prev, const void* base,
  *   ctx_len      [B] int32    tokens the cache holds before the new ones
  *   tok_start    [B + 1] int32, ascending: sequence b's new tokens are rows
  *                tok_start[b] .. tok_start[b + 1] - 1 of the N token rows (any
- *                count, zero too); new token j has position ctx_len[b] + j
+ *                count, zero too); new token j has position ctx_len[b] + j.
+ *                Attention does nothing and raises flag bit 4 if it descends
  *   B, N         sequences, token rows (0: nothing is enqueued).  Rows that no
- *                sequence owns are neither read nor written.
+ *                sequence owns have no effect; outputs leave theirs as they are
  *   Hq, Hkv, D   query heads, key/value heads (Hq a multiple of Hkv; query
  *                head i reads key/value head i / (Hq / Hkv)), head size 64, 128 or 256
  *   page_size    a power of two up to 65536

@@ -87,3 +87,20 @@ def test_lengths_at_the_ends_of_their_type(ctx):
     out, want = attend(far), attend(c)
     assert df2.device_error() == (16 if ctx > 0 else 0)
     assert torch.equal(out, want if ctx > 0 else torch.cat((torch.zeros_like(want[:3]), want[3:])))
+
+
+@pytest.mark.parametrize("start", [[0, 8, 0, 8, 0, 8, 13], [13, 0, 0, 0, 0, 0, 0], [0, 2, 4, 6, 8, 13, 12]])
+@pytest.mark.parametrize("B", [6, 150])
+def test_descending_token_starts_do_nothing(start, B):
+    """Overlapping sequences could ask for more work than there are tokens: outputs stay
+    and flag bit 4 is raised."""
+    say("attention descending starts", start, B)
+    c = paged_case(72, BF, 128, 8, 2, 16, [2, 2, 2, 2, 2, 3], [500, 3, 0, 70, 9, 40])
+    good = attend(c)
+    s = torch.tensor(start, dtype=torch.int32, device="cuda")
+    reps = -(-B // 6)
+    bad = dict(c, table=c["table"].repeat(reps, 1), ctx=c["ctx"].repeat(reps), start=torch.cat([s[:-1].repeat(reps), s[-1:]]))
+    out = torch.full_like(good, -7.0)
+    assert attend(bad, out=out) is out
+    assert bool((out == -7.0).all()) and df2.device_error() == 16
+    assert torch.equal(attend(c), good) and df2.device_error() == 0
