@@ -536,7 +536,8 @@ typedef struct df2_verify_dims {
  *                             and raises flag bit 5)
  *   cand_idx  [B, P, K] int32, distinct in a row, cand_prob [B, P, K] float:
  *             as dflash2_select_sample_rows returns them, or for a path chosen
- *             without sampling K = 1, the path itself with probability 1
+ *             without sampling K = 1, the path itself with probability 1.  Where
+ *             a draft is refused, an id outside [0, V) is left out and raises bit 1
  *   n_draft   [B] int32  drafts in use of each sequence (clamped to [0, P]),
  *             or NULL: P
  *   temperature  >= 0, at most 1e30, 1 / temperature finite in fp32; 0: a draft
@@ -555,7 +556,8 @@ typedef struct df2_verify_dims {
  * -inf logits have weight 0; other non-finite values are outside the
  * contract.  Where no token is left to draw (a row without weight, or
  * candidates' probabilities that add to more than 1), flag bit 6 is raised and
- * the token is 0 with probability 0.
+ * the token is 0 with probability 0.  At temperature 0 nothing is drawn: a row
+ * without weight has its lowest id as the largest.
  */
 size_t dflash2_verify_workspace(const df2_verify_dims* dims);
 df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const int32_t* path,

@@ -6,6 +6,8 @@ import torch
 
 import draft_selection_topk16_amd as df2
 from gpu_util import say
+from target_ref import verify_ref
+from test_gpu_target import verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +83,20 @@ def test_no_token_left_raises_the_flag(B):
     tok, cnt, p = df2.verify(c["target"], c["path"], c["cand"], c["prob"], c["u"])
     assert df2.device_error() == 64
     assert bool((tok[:, 0] == 0).all()) and bool((cnt == 1).all()) and float(p.abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("dtype,B,P,V,K,tau,kind", [(BF, 4, 7, 151936, 16, 1.0, "logits"), (F32, 9, 7, 32003, 5, 0.7, "logits"),
+                                                    (F32, 64, 15, 5000, 32, 1.3, "logits"), (BF, 20, 3, 9001, 8, 1.0, "probs")])
+def test_few_elements_are_summed_in_64_bits(dtype, B, P, V, K, tau, kind):
+    """Up to 2^24 elements p is rounded once, to fp32 (half a step 2^-24; the fp64 weights
+    and sums are good to 10^-11), and decisions further apart than that are fp64's."""
+    say("verify 64 bits", dtype, B, P, V, K, tau, kind)
+    c = verify_case(B + P + V, F32, B, P, V, K)
+    c["target"] = (torch.softmax(c["target"], -1) if kind == "probs" else c["target"]).to(dtype)
+    args = (c["target"], c["path"], c["cand"], c["prob"], c["u"])
+    got = [x.cpu().numpy() for x in df2.verify(*args, temperature=tau, kind=kind)]
+    tok, cnt, p, margin = verify_ref(*args, tau, None, kind)
+    clear = margin > 2.0 ** -24
+    assert clear.mean() > 0.9 and df2.device_error() == 0
+    assert np.array_equal(got[0][clear], tok[clear]) and np.array_equal(got[1][clear], cnt[clear])
+    assert np.all(np.abs(got[2] - p)[clear] <= 2.0 ** -24 * (1 + 2.0 ** -10) * p[clear])
