@@ -30,19 +30,18 @@
 // a tile holds nothing but keys that some row of the block may see, so that
 // what else stands in the pages (NaN included) never meets the product.
 //
-// Measured (kernel, then join; head size 128, bf16 unless said):
-//   4 contexts of 65 to 131 thousand tokens, 8 new each, 32 / 8 heads: 249 + 7 us
-//     for 1.61 GB, 6.5 TB/s: a copy of the loads alone takes as long;
-//   32 contexts of 301 to 12007 tokens, 8 new each, 64 / 8 heads: 155 + 11 us (156
-//     back to back) for 816 MB, 5.3 TB/s: some 20 us are the start, the parts (25 MB)
-//     and the end;
-//   1 new token after 1003, 32 / 8 heads: 7.5 + 3.5 us, latency: 1.9 us to the
+// Measured (head size 128, bf16 unless said; passes back to back):
+//   4 contexts of 65 to 131 thousand tokens, 8 new each, 32 / 8 heads: 244 us for 1.61
+//     GB, 6.6 TB/s, where a kernel that only reads reaches 7.1;
+//   32 contexts of 301 to 12007 tokens, 8 new each, 64 / 8 heads: 161 us for 816 MB
+//     (kernel 153, 5.3 TB/s; join 8): some 20 us are the start, the parts (25 MB) and the end;
+//   1 new token after 1003, 32 / 8 heads: 11.1 us (7.7 and 3.4), latency: 1.9 us to the
 //     cut, 1.5 to the place, 0.8 for page ids, 0.9 for the first tile;
-//   3 drafted blocks in fp32 of head size 64, up to 2049 keys: 9.8 + 4.2 us;
-//   prompt chunks (739 GFLOP): 700 us, 1060 TFLOP/s, where a large library product
-//     reaches 1364.  Nothing alone bounds it: with its products only, it takes 565
-//     us (the clock falls to 2.05 GHz under them), LDS loads add 40, operand reads
-//     60, exponentials 90.
+//   3 drafted blocks in fp32 of head size 64, up to 2049 keys: 14.4 us;
+//   prompt chunks (739 GFLOP): 694 us, 1060 TFLOP/s, where a large library product
+//     reaches 1373 (690 to 757 us on different cards).  Nothing alone bounds it: with its
+//     products only, it takes 565 us (the clock falls to 2.05 GHz under them), LDS loads
+//     add 40, operand reads 60, exponentials 90.
 #pragma once
 
 #include "common.hpp"
@@ -670,8 +669,10 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::
         } else {
             // Each product adds two terms and rounds: a chain of them over all of D puts
             // the roundings of D terms at the score's own size into its exponential.  Four
-            // sums of a quarter: outputs at scores of 50 off by 2.5e-7 to 5e-7 instead of 3e-7 to
-            // 1e-6, for a twentieth of the time of long chunks (504 us, 533).
+            // sums of a quarter (two of a half at head size 256, for their registers):
+            // outputs at scores of 50 off by 2.5e-7 to 5e-7 instead of 3e-7 to 1e-6, for a
+            // twentieth of the time of long chunks (2 of 2000 tokens after 2000, 8 / 2 heads
+            // of 128: 504 us, 533).
             static_assert(KS == 1, "one sub-tile");
             constexpr int NA = D <= 128 ? 4 : 2;
             f32x16_t part[NA];

@@ -21,8 +21,8 @@
 // the lane that has it.  A workgroup takes one token, or four neighbouring ones
 // where there are enough; with few tokens, several workgroups share one.
 //
-// Measured: 15 thousand tokens of 32 + 2 * 8 heads of 128 in bf16 87 us for 378 MB,
-// 4.3 TB/s, where a large copy reaches 5.1 (eight tokens a workgroup 120 us, one
+// Measured: 15 thousand tokens of 32 + 2 * 8 heads of 128 in bf16 85 us for 378 MB,
+// 4.4 TB/s, where a large copy reaches 5.1 (eight tokens a workgroup 120 us, one
 // 97); a block of 8 tokens 4.4 us, latency of the loads that follow one another:
 // sequence, page id, row.
 #pragma once

@@ -418,7 +418,9 @@ struct VerifyPlan {
 // Few elements: launch 1 makes the fp64 sums of all rows, so that launch 2 is one
 // short step.  Against the other way, both launches, rows of 151936 in bf16, 8 a
 // sequence: 11.7 us and 13.7 at one sequence, 17.7 and 19.6 at 8, 24.5 and 26.5 at
-// 16, 38.9 and 33.4 at 32; of 32000, 64 sequences, 22.2 and 21.7.  Segments of 2048
+// 16, 38.9 and 33.4 at 32; of 32000, 64 sequences, 22.2 and 21.7.  (So a count of
+// elements does not part the two exactly: of these, it sends the 16 sequences and the
+// 64 to the slower form, by 2 us and 0.5.)  Segments of 2048
 // elements, or longer ones where that would be more workgroups than run at once, as
 // far as a workgroup holds them.
 // Else launch 1 takes fp32 sums, about eight workgroups a compute unit over all

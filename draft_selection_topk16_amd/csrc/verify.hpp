@@ -23,12 +23,12 @@
 // chunks of a segment, the last to finish draws.  Few rows: launch 1 makes every
 // row's chunk sums in fp64 at once, launch 2 only decides and draws.
 //
-// Measured (launch 1 + launch 2, bf16): 64 sequences of 16 rows of 262144 91 + 32 us,
-// launch 1 at 5.9 TB/s; 32 of 8 rows of 151936 17 + 17 us for 78 MB; one of 8 rows,
+// Measured (launch 1 + launch 2, bf16): 64 sequences of 16 rows of 262144 87 + 26 us,
+// launch 1 at 6.2 TB/s; 32 of 8 rows of 151936 17 + 17 us for 78 MB; one of 8 rows,
 // the second form, 4.8 + 7.3 us (3.6 + 10.8 in the first).  Launch 2 of the first is
 // a chain of short steps (2.3 us to the decision, 1.7 for the segment, 1.1 to the last
-// arrival, 1.6, 0.8 and 1.9 for segment, chunk and token of one sequence) and, with
-// many sequences, the fp64 weights.
+// arrival, 1.6, 0.8 and 1.9 for segment, chunk and token of one sequence); the fp64
+// weights of 32 rows are some 2.5 of its 17 us.
 #pragma once
 
 #include "common.hpp"
