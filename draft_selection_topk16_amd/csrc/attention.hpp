@@ -218,10 +218,13 @@ __device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
     c.whole = a.whole;
     c.head_tiles = 0;
     int blocks = 0, most = 0;
-    uint64_t falls = 0;
+    bool fell = false, overlap = false;         // starts descended; sequences with tokens follow
     for (int c0 = 0; c0 < a.kv.B; c0 += 64) {
         q = lane_seq<Shape>(a, c0, c.whole);
-        falls |= __ballot(q.falls);
+        const uint64_t falls = __ballot(q.falls), live = __ballot(q.n > 0);
+        // 2 << i: the lanes behind i
+        overlap |= fell ? live != 0 : falls && (live & -(2ull << __builtin_ctzll(falls)));
+        fell |= falls != 0;
         c.head_tiles += __builtin_amdgcn_readlane(lanes_scan(q.tiles), 63);
         if (a.choose) {
             blocks += __builtin_amdgcn_readlane(lanes_scan(q.blocks), 63);
@@ -229,8 +232,8 @@ __device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
         }
     }
     // Sequences that overlap could make a line of any length, beyond what a tile's
-    // number holds: no work then, and a flag.
-    if (falls) {
+    // number holds: no work then, and a flag.  (Starts behind the last sequence may be 0.)
+    if (overlap) {
         if (lane_id() == 0) atomicOr(a.kv.err, kFlagLength);
         blocks = c.head_tiles = 0;
     }

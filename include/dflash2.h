@@ -422,6 +422,7 @@ df2_status dflash2_conv2(const void* x, const void* x_prev, const void* base,
  *                tok_start[b] .. tok_start[b + 1] - 1 of the N token rows (any
  *                count, zero too); new token j has position ctx_len[b] + j.
  *                Attention does nothing and raises flag bit 4 if it descends
+ *                before a sequence with tokens
  *   B, N         sequences, token rows (0: nothing is enqueued).  Rows that no
  *                sequence owns have no effect; outputs leave theirs as they are
  *   Hq, Hkv, D   query heads, key/value heads (Hq a multiple of Hkv; query

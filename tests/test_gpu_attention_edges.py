@@ -89,18 +89,40 @@ def test_lengths_at_the_ends_of_their_type(ctx):
     assert torch.equal(out, want if ctx > 0 else torch.cat((torch.zeros_like(want[:3]), want[3:])))
 
 
-@pytest.mark.parametrize("start", [[0, 8, 0, 8, 0, 8, 13], [13, 0, 0, 0, 0, 0, 0], [0, 2, 4, 6, 8, 13, 12]])
+DOWN = [
+    # starts, and the sequences with tokens of the same batch in order (None: refused)
+    ([0, 8, 0, 8, 0, 8, 13], None), ([13, 0, 2, 4, 6, 8, 10], None), ([0, 2, 4, 6, 8, 7, 9], None),
+    ([0, 2, 4, 6, 0, 0, 0], [0, 2, 4, 6, 6, 6, 6]), ([13, 0, 0, 0, 0, 0, 0], [0] * 7), ([0, 2, 4, 6, 8, 13, 12], [0, 2, 4, 6, 8, 13, 13]),
+]
+
+
+@pytest.mark.parametrize("start,same", DOWN)
 @pytest.mark.parametrize("B", [6, 150])
-def test_descending_token_starts_do_nothing(start, B):
+def test_descending_token_starts(start, same, B):
     """Overlapping sequences could ask for more work than there are tokens: outputs stay
-    and flag bit 4 is raised."""
+    and flag bit 4 is raised.  Starts that fall where no tokens follow, as zeros behind
+    the last sequence, leave the batch as it is."""
     say("attention descending starts", start, B)
     c = paged_case(72, BF, 128, 8, 2, 16, [2, 2, 2, 2, 2, 3], [500, 3, 0, 70, 9, 40])
     good = attend(c)
-    s = torch.tensor(start, dtype=torch.int32, device="cuda")
-    reps = -(-B // 6)
-    bad = dict(c, table=c["table"].repeat(reps, 1), ctx=c["ctx"].repeat(reps), start=torch.cat([s[:-1].repeat(reps), s[-1:]]))
+
+    def with_starts(s, more):
+        """B sequences: these, and empty ones that begin at `more`."""
+        wide = torch.cat((c["table"], c["table"][:1].expand(B - 6, -1)))
+        return dict(c, table=wide, ctx=torch.cat((c["ctx"], c["ctx"][:1].expand(B - 6))),
+                    start=torch.tensor(s + [more] * (B - 6), dtype=torch.int32, device="cuda"))
     out = torch.full_like(good, -7.0)
-    assert attend(bad, out=out) is out
-    assert bool((out == -7.0).all()) and df2.device_error() == 16
+    attend(with_starts(start, start[-1]), out=out)
+    if same is None:
+        assert bool((out == -7.0).all()) and df2.device_error() == 16
+        # seen from the next wave of sequences too
+        late = with_starts([0] * 7, 0)
+        if B > 64:
+            late["start"][7:] = torch.tensor([13] * 80 + [3] * (B - 6 - 81) + [5], dtype=torch.int32, device="cuda")
+            attend(late, out=out)
+            assert bool((out == -7.0).all()) and df2.device_error() == 16
+    else:
+        want = torch.full_like(good, -7.0)
+        attend(with_starts(same, same[-1]), out=want)
+        assert torch.equal(out, want) and df2.device_error() == 0
     assert torch.equal(attend(c), good) and df2.device_error() == 0
