@@ -2,7 +2,8 @@
 
 The compute path is the HIP library libdflash2.so (C ABI: include/dflash2.h);
 `binding` marshals torch tensors into it, `target` those of the target's side
-(paged cache, attention over it, verification of drafts).  `synth` draws seeded synthetic
+(paged cache, attention over it, verification of drafts), `steps` what stands between
+its steps (pages of the next one, penalties and masks on rows).  `synth` draws seeded synthetic
 inputs.  Importing the package does not load the library: the first call
 does, and raises if it has not been built.
 """
@@ -10,11 +11,12 @@ from .binding import (PreparedSelect, SelectorError, conv2, device_error, draft_
                       pair_scores, philox_uniforms, philox_uniforms_next, plan,
                       plan_override, project, release, sample_walk, select, select_sample, topk, version,
                       viterbi, walk)
+from .steps import PreparedAdjust, PreparedPages, adjust_logits, plan_pages
 from .target import (PreparedAppend, PreparedAttention, PreparedVerify, kv_append, paged_attention, rope_freqs,
                      verify)
 
-__all__ = ["PreparedAppend", "PreparedAttention", "PreparedSelect", "PreparedVerify", "SelectorError", "conv2",
+__all__ = ["PreparedAdjust", "PreparedAppend", "PreparedAttention", "PreparedPages", "PreparedSelect", "PreparedVerify", "SelectorError", "adjust_logits", "conv2",
            "device_error", "draft_rows", "kv_append", "lmhead_topk", "load", "paged_attention", "rope_freqs", "verify",
            "pair_scores", "philox_uniforms", "philox_uniforms_next", "plan",
-           "plan_override", "project", "release", "sample_walk", "select", "select_sample", "topk", "version",
+           "plan_override", "plan_pages", "project", "release", "sample_walk", "select", "select_sample", "topk", "version",
            "viterbi", "walk"]

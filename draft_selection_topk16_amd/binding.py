@@ -69,6 +69,23 @@ class VerifyDims(ctypes.Structure):
                 ("dtype", ctypes.c_int), ("kind", ctypes.c_int)]
 
 
+class PagePool(ctypes.Structure):
+    """df2_page_pool."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("block_table", "held", "free_list", "free_count")]
+                + [("table_stride", ctypes.c_int64)]
+                + [(n, ctypes.c_int32) for n in ("B", "N", "page_size", "num_pages", "table_width")])
+
+
+class Adjust(ctypes.Structure):
+    """df2_adjust."""
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "R", "V", "L", "M")] + [("dtype", ctypes.c_int)]
+                + [(n, ctypes.c_int64) for n in ("seq_stride", "row_stride", "out_seq_stride", "out_row_stride")]
+                + [("history", ctypes.c_void_p), ("history_stride", ctypes.c_int64)]
+                + [(n, ctypes.c_void_p) for n in ("history_len", "prompt_len", "path", "repetition", "frequency",
+                                                  "presence", "bias_token", "bias", "mask")]
+                + [("mask_seq_stride", ctypes.c_int64), ("mask_row_stride", ctypes.c_int64)])
+
+
 _lib = None
 
 
@@ -108,6 +125,8 @@ def load() -> ctypes.CDLL:
         "dflash2_paged_attention": [kvp, vp, i64, ctypes.c_float, i32, i32, i32, vp, i64, vp, ctypes.c_size_t,
                                     vp],
         "dflash2_verify": [vdp, vp, vp, vp, vp, vp, ctypes.c_double, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+        "dflash2_plan_pages": [ctypes.POINTER(PagePool), vp, vp, vp, vp, vp, vp, vp, vp],
+        "dflash2_adjust_logits": [ctypes.POINTER(Adjust), vp, vp, vp],
         "dflash2_plan_override": [ctypes.c_int, i32],
         "dflash2_release": [],
     }

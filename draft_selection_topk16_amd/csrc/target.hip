@@ -22,105 +22,12 @@
 #include "attention.hpp"
 #include "kvappend.hpp"
 #include "verify.hpp"
+#include "target_host.hpp"
 
 using namespace df2;
 using namespace df2::host;
 
 namespace {
-
-// Threads of a launch along one dimension.
-constexpr int64_t kMostThreads = 0xFFFFFFFF;
-
-bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-
-df2_status launched(const char* what) {
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? DF2_OK : hip_failed(e, what);
-}
-
-// Checks the sizes of a cache descriptor.
-df2_status check_kv_sizes(const df2_paged_kv* kv) {
-    if (!kv) return fail_with(DF2_EINVAL, "the cache descriptor is NULL");
-    if (kv->dtype != DF2_F32 && kv->dtype != DF2_BF16) return fail_with(DF2_EINVAL, "unknown dtype");
-    if (kv->B < 0 || kv->N < 0) return fail_with(DF2_EINVAL, "B and N must be >= 0");
-    if (kv->Hkv < 1 || kv->Hq < 1 || kv->Hq % kv->Hkv != 0)
-        return fail_with(DF2_EINVAL, "Hq must be a positive multiple of Hkv");
-    if (kv->D != 64 && kv->D != 128 && kv->D != 256)
-        return fail_with(DF2_EUNSUPPORTED, "D must be 64, 128 or 256");
-    if (kv->page_size < 1 || (kv->page_size & (kv->page_size - 1)) || kv->page_size > 65536)
-        return fail_with(DF2_EUNSUPPORTED, "page_size must be a power of two up to 65536");
-    if (kv->num_pages < 1) return fail_with(DF2_EINVAL, "num_pages < 1");
-    if (kv->table_width < 1 || kv->table_stride < kv->table_width)
-        return fail_with(DF2_EINVAL, "table_width must be >= 1 and at most table_stride");
-    if ((int64_t)kv->table_width * kv->page_size > (1 << 30))
-        return fail_with(DF2_EUNSUPPORTED, "table_width * page_size above 2^30");
-    if ((int64_t)kv->N * kv->Hq > 0x7FFFFFFF) return fail_with(DF2_EUNSUPPORTED, "N * Hq too large");
-    const int64_t page = (int64_t)kv->Hkv * kv->page_size * kv->D;
-    if (kv->page_stride < page) return fail_with(DF2_EINVAL, "page_stride below Hkv * page_size * D");
-    const int per16 = kv->dtype == DF2_BF16 ? 8 : 4;
-    if (kv->page_stride % per16 != 0) return fail_with(DF2_EINVAL, "page_stride must be a multiple of 16 bytes");
-    return DF2_OK;
-}
-
-// Checks a cache descriptor and fills what the kernels read of it.
-df2_status read_kv(const df2_paged_kv* kv, PagedKv* out) {
-    const df2_status st = check_kv_sizes(kv);
-    if (st != DF2_OK || kv->B == 0 || kv->N == 0) return st;
-    if (!kv->k_cache || !kv->v_cache || !kv->block_table || !kv->ctx_len || !kv->tok_start)
-        return fail_with(DF2_EINVAL, "NULL pointer in the cache descriptor");
-    if (!aligned(kv->k_cache, 16) || !aligned(kv->v_cache, 16))
-        return fail_with(DF2_EINVAL, "k_cache and v_cache must be 16-byte aligned");
-    if (!aligned(kv->block_table, 4) || !aligned(kv->ctx_len, 4) || !aligned(kv->tok_start, 4))
-        return fail_with(DF2_EINVAL, "block_table, ctx_len and tok_start must be 4-byte aligned");
-    out->table = kv->block_table;
-    out->ctx = kv->ctx_len;
-    out->start = kv->tok_start;
-    out->page_stride = kv->page_stride;
-    out->B = kv->B;
-    out->N = kv->N;
-    out->Hq = kv->Hq;
-    out->Hkv = kv->Hkv;
-    out->page_shift = __builtin_ctz((unsigned)kv->page_size);
-    out->num_pages = kv->num_pages;
-    out->table_width = kv->table_width;
-    out->table_stride = kv->table_stride;
-    return DF2_OK;
-}
-
-// A token's row of `heads` heads: 16-byte aligned and long enough.
-df2_status check_rows(const df2_paged_kv* kv, const void* p, int64_t stride, int heads, const char* name) {
-    const int per16 = kv->dtype == DF2_BF16 ? 8 : 4;
-    if (!aligned(p, 16)) return fail_with(DF2_EINVAL, std::string(name) + " must be 16-byte aligned");
-    if (stride < (int64_t)heads * kv->D || stride % per16 != 0)
-        return fail_with(DF2_EINVAL, std::string(name) + ": the token stride must hold the heads and be a multiple of 16 bytes");
-    return DF2_OK;
-}
-
-// Token rows as the arguments give them: stride and heads * D in elements.
-struct TokenRows {
-    const void* p;
-    int64_t stride;
-    int heads;
-};
-// Whether some row of one shares memory with a row of the other.  (Rows of both may
-// be parts of the same wider rows.)
-bool rows_meet(const df2_paged_kv* kv, const TokenRows& a, const TokenRows& b) {
-    const int64_t size = kv->dtype == DF2_BF16 ? 2 : 4, last = kv->N - 1;
-    const int64_t sa = a.stride * size, wa = (int64_t)a.heads * kv->D * size;
-    const int64_t sb = b.stride * size, wb = (int64_t)b.heads * kv->D * size;
-    const int64_t d = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p);
-    if (d >= last * sa + wa || -d >= last * sb + wb) return false;
-    if (sa == sb) {
-        const int64_t m = ((d % sa) + sa) % sa;         // where b's rows begin within a's stride
-        return m < wa || sa - m < wb;
-    }
-    for (int64_t i = 0; i <= last; ++i) {
-        const int64_t x = i * sa - d;                   // a's row against b's first
-        const int64_t j = x < wb ? 0 : (x - wb) / sb + 1;       // b's first row that ends behind its beginning
-        if (j <= last && j * sb < x + wa) return true;
-    }
-    return false;
-}
 
 // ----------------------------------------------------------------------------
 // Attention.
@@ -167,19 +74,6 @@ auto with_shape(int wr, F&& f) {
     } else {
         return f(AttnShape<BF16, D, 4, 1, 1, 2>());
     }
-}
-
-template <typename F>
-auto with_type(const df2_paged_kv* kv, F&& f) {
-    using std::integral_constant;
-    if (kv->dtype == DF2_BF16) {
-        if (kv->D == 64) return f(integral_constant<bool, true>(), integral_constant<int, 64>());
-        if (kv->D == 128) return f(integral_constant<bool, true>(), integral_constant<int, 128>());
-        return f(integral_constant<bool, true>(), integral_constant<int, 256>());
-    }
-    if (kv->D == 64) return f(integral_constant<bool, false>(), integral_constant<int, 64>());
-    if (kv->D == 128) return f(integral_constant<bool, false>(), integral_constant<int, 128>());
-    return f(integral_constant<bool, false>(), integral_constant<int, 256>());
 }
 
 // Blocks of as many rows as a sequence has on average, but smaller ones where a
@@ -230,14 +124,6 @@ AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
     pl.part = (size_t)2 * pl.wgs * pl.bm * kv->D;
     pl.bytes = pl.wgs > 1 ? (pl.part + (size_t)(4 * pl.bm + 8) * pl.wgs) * sizeof(float) : 0;
     return pl;
-}
-
-// max_len as the plan takes it: 0 means what the page table holds.
-df2_status plan_length(const df2_paged_kv* kv, int32_t max_len, int* out) {
-    if (max_len < 0) return fail_with(DF2_EINVAL, "max_len < 0");
-    const int cap = kv->table_width * kv->page_size;
-    *out = max_len == 0 ? cap : std::min(max_len, cap);
-    return DF2_OK;
 }
 
 template <bool BF16, int D>

@@ -568,14 +568,106 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
                           void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Pages of a paged cache for the next step, made on the device from the lengths of
+ * the requests, so that a draft-verify cycle never waits for the host: what
+ * dflash2_verify counts goes in as `advance`, and the block table and token starts
+ * come out as the paged operators take them.
+ *   block_table [B, table_width] int32, rows table_stride apart: pages of each
+ *               request in order of position, its first held[b] entries
+ *   held        [B] int32   pages that each request holds
+ *   free_list   [num_pages] int32, free_count [1] int32: the ids of the free pages.
+ *               A page is in the list's first free_count entries or held once
+ *   B           requests (0: nothing is enqueued), at most 2^20
+ *   N           token rows of the step, at most 2^30
+ *   page_size, num_pages, table_width as in df2_paged_kv
+ * These four arrays are updated in place.
+ */
+typedef struct df2_page_pool {
+    int32_t* block_table;
+    int32_t* held;
+    int32_t* free_list;
+    int32_t* free_count;
+    int64_t table_stride;
+    int32_t B, N, page_size, num_pages, table_width;
+} df2_page_pool;
+
+/*
+ *   ctx_len     [B] int32   tokens that each request had in the cache before the last
+ *               step, or what is left of them
+ *   advance     [B] int32   tokens that have joined them since, or NULL: none; a sum
+ *               below 0 counts as 0
+ *   n_new       [B] int32   new tokens it brings; negative: the request has ended
+ * A request wants ceil((ctx_len + advance + n_new) / page_size) pages, one that has
+ * ended none.  First pages beyond that (after refused drafts, say) go to the end of the free
+ * list, in the order of the requests and positions, and their table entries become
+ * -1.  Then missing pages are taken, in the same order, each from the list's end.
+ * A request is served while all pages and rows that it and those before it ask for
+ * are there; one that is not, or whose table is too narrow, keeps what it has and
+ * gets no new tokens, and device flag bit 7 (bit 4: the table) is raised.
+ *   ctx_out     [B] int32   ctx_len + advance (0: ended); may be ctx_len itself
+ *   tok_start   [B + 1] int32  first row of each request's new tokens
+ *   slots       [N] int64   page id * page_size + place in the page of each row, or NULL
+ *   positions   [N] int32   its position, or NULL; both are -1 in rows of no request
+ * Outputs must not overlap one another or the inputs (but for ctx_out).  The result
+ * is the same whenever the inputs are.
+ */
+df2_status dflash2_plan_pages(const df2_page_pool* pool, const int32_t* ctx_len, const int32_t* advance,
+                              const int32_t* n_new, int32_t* ctx_out, int32_t* tok_start,
+                              int64_t* slots, int32_t* positions, hipStream_t stream);
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on rows of logits: the
+ * target's rows before dflash2_verify, or the drafter's before the selection.  Of
+ * token v's value x in row t of sequence b:
+ *     y = x;  if v was seen before the row:  y = x > 0 ? x / repetition : x * repetition
+ *     y -= frequency * c + presence * [c > 0]    (one after the other)
+ *     y += bias of v;  v not allowed: y = -inf
+ * Seen: v stands in the first history_len tokens of the history, or among the drafts
+ * path[b][0 .. t - 1]; c: how often it stands in the history from prompt_len on, and
+ * among those drafts.  fp32 arithmetic, one rounding at the store; values that nothing
+ * happens to keep their bits.
+ *   logits, out  rows of V values (dtype), row t of sequence b at b * seq_stride +
+ *                t * row_stride elements; out may be logits itself with the same
+ *                strides (then only what changes is touched), else must not overlap it
+ *   history      [B, L] int32, rows history_stride apart, or NULL; history_len [B]
+ *                int32, clamped to [0, L]; prompt_len [B] int32, or NULL: 0
+ *   path         [B, R - 1] int32, or NULL: no drafts
+ *   repetition, frequency, presence  [B] float each, or NULL: 1, 0, 0
+ *   bias_token   [B, M] int32, bias [B, M] float; of a token given twice the last counts
+ *   mask         ceil(V / 32) words a row, bit v % 32 of word v / 32 set where token v
+ *                is allowed; mask_seq_stride and mask_row_stride in words, 0: one row
+ *                for all; or NULL
+ * Ids outside [0, V) in the lists are left out (-1 fills them up).  B or R 0: nothing
+ * is enqueued.  V <= 2^29, L < 2^29.
+ */
+typedef struct df2_adjust {
+    int32_t B, R, V, L, M;
+    df2_dtype dtype;
+    int64_t seq_stride, row_stride, out_seq_stride, out_row_stride;
+    const int32_t* history;
+    int64_t history_stride;
+    const int32_t* history_len;
+    const int32_t* prompt_len;
+    const int32_t* path;
+    const float* repetition;
+    const float* frequency;
+    const float* presence;
+    const int32_t* bias_token;
+    const float* bias;
+    const int32_t* mask;
+    int64_t mask_seq_stride, mask_row_stride;
+} df2_adjust;
+df2_status dflash2_adjust_logits(const df2_adjust* adjust, const void* logits, void* out, hipStream_t stream);
+
+/*
  * Waits for `stream`, then reports and clears the device-side flags of its
  * scratch buffer and of the current device's no-allocation scratch: *flags
  * receives a bit mask (bit 0: a prev_tok outside
  * [0, V) was replaced by 0; bit 1: a cand_idx entry outside [0, V) was
  * replaced by 0; bit 2: a row merge of dflash2_select gave up waiting for
  * its gate rows (launches 1 or 2 only), which only a fault elsewhere can
- * cause, and its scores are then unreliable; bits 3 to 6: the paged operators
- * and dflash2_verify, see there; theirs, and those of dflash2_select_noalloc,
+ * cause, and its scores are then unreliable; bits 3 to 7: the paged operators,
+ * dflash2_plan_pages and dflash2_verify, see there; theirs, and those of dflash2_select_noalloc,
  * are kept once a device and reported on any of its streams: work that still
  * runs on another stream may raise some that a later call reports).  A raised
  * flag can leave a late gate arrival counted in the stream's scratch, so after
