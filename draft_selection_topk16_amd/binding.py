@@ -32,7 +32,7 @@ EXPORTED = (
     "dflash2_sample_walk", "dflash2_philox_uniforms", "dflash2_philox_uniforms_next",
     "dflash2_select_sample_rows", "dflash2_draft_rows",
     "dflash2_kv_append", "dflash2_paged_attention", "dflash2_paged_attention_workspace",
-    "dflash2_verify", "dflash2_verify_workspace",
+    "dflash2_verify", "dflash2_verify_workspace", "dflash2_plan_pages", "dflash2_adjust_logits",
     "dflash2_conv2", "dflash2_device_error",
     "dflash2_plan_override",
     "dflash2_release",
