@@ -11,7 +11,7 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", f) for f in ("dflash2.hip", "target.hip", "steps.hip")]
+SOURCES = [os.path.join(PKG, "csrc", f) for f in ("dflash2.hip", "target.hip", "steps.hip", "fp4.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdflash2.so")
 ARCH = "gfx950"

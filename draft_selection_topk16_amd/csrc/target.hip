@@ -226,51 +226,9 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
                              int32_t interleaved, void* out_q, int64_t out_q_stride, hipStream_t stream) {
     clear_error();
     AppendArgs a;
-    std::memset(&a, 0, sizeof(a));
-    df2_status st = read_kv(kv, &a.kv);
-    if (st != DF2_OK) return st;
-    if (rot < 0 || rot > kv->D || rot % 16 != 0)
-        return fail_with(DF2_EUNSUPPORTED, "rot must be a multiple of 16 in [0, D]");
-    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail_with(DF2_EINVAL, "eps must be finite and >= 0");
-    if (kv->B == 0 || kv->N == 0) return DF2_OK;
-    if (((int64_t)kv->N + 3) / 4 * 256 > kMostThreads) return fail_with(DF2_EUNSUPPORTED, "N above 2^26 - 4");
-    if (!k || !v || (rot > 0 && !rope_freq)) return fail_with(DF2_EINVAL, "NULL pointer argument");
-    if (!q != !out_q) return fail_with(DF2_EINVAL, "q and out_q come together");
-    if (!q && q_norm) return fail_with(DF2_EINVAL, "q_norm without q");
-    if ((st = check_rows(kv, k, k_stride, kv->Hkv, "k")) != DF2_OK) return st;
-    if ((st = check_rows(kv, v, v_stride, kv->Hkv, "v")) != DF2_OK) return st;
-    if (q) {
-        if ((st = check_rows(kv, q, q_stride, kv->Hq, "q")) != DF2_OK) return st;
-        if ((st = check_rows(kv, out_q, out_q_stride, kv->Hq, "out_q")) != DF2_OK) return st;
-        if (q == out_q && q_stride != out_q_stride)
-            return fail_with(DF2_EINVAL, "out_q in place of q needs the same stride");
-    }
-    if (!aligned(q_norm, 16) || !aligned(k_norm, 16))
-        return fail_with(DF2_EINVAL, "q_norm and k_norm must be 16-byte aligned");
-    if (!aligned(rope_freq, 8)) return fail_with(DF2_EINVAL, "rope_freq must be 8-byte aligned");
-    if (q) {
-        const TokenRows out = {out_q, out_q_stride, kv->Hq};
-        if ((q != out_q && rows_meet(kv, {q, q_stride, kv->Hq}, out)) || rows_meet(kv, {k, k_stride, kv->Hkv}, out) ||
-            rows_meet(kv, {v, v_stride, kv->Hkv}, out))
-            return fail_with(DF2_EINVAL, "out_q must not overlap q (unless it is q), k or v");
-    }
-    if ((st = device_flag_word(&a.kv.err)) != DF2_OK) return st;
-    a.q = q;
-    a.k = k;
-    a.v = v;
-    a.k_cache = kv->k_cache;
-    a.v_cache = kv->v_cache;
-    a.out_q = out_q;
-    a.q_norm = q_norm;
-    a.k_norm = k_norm;
-    a.freq = rope_freq;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.out_stride = out_q_stride;
-    a.rot = rot;
-    a.interleaved = interleaved ? 1 : 0;
-    a.eps = eps;
+    const df2_status st = read_append(kv, false, q, q_stride, k, k_stride, v, v_stride, q_norm, k_norm, eps, rope_freq, rot,
+                                      interleaved, out_q, out_q_stride, &a);
+    if (st != DF2_OK || kv->B == 0 || kv->N == 0) return st;
     return with_type(kv, [&](auto bf16, auto d) {
         constexpr int D = decltype(d)::value, heads = 256 / (D / (decltype(bf16)::value ? 8 : 4));
         const int units = (q ? kv->Hq : 0) + 2 * kv->Hkv;

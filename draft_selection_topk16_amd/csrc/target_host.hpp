@@ -4,12 +4,15 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
+#include <cstring>
 #include <string>
 #include <type_traits>
 
 #include "dflash2.h"
 #include "host.hpp"
 #include "attention.hpp"
+#include "kvappend.hpp"
 
 namespace df2 {
 namespace host {
@@ -24,8 +27,8 @@ inline df2_status launched(const char* what) {
     return e == hipSuccess ? DF2_OK : hip_failed(e, what);
 }
 
-// Checks the sizes of a cache descriptor.
-inline df2_status check_kv_sizes(const df2_paged_kv* kv) {
+// Checks the sizes of a cache descriptor; fp4: of 4-bit values, whose stride is in bytes.
+inline df2_status check_kv_sizes(const df2_paged_kv* kv, bool fp4 = false) {
     if (!kv) return fail_with(DF2_EINVAL, "the cache descriptor is NULL");
     if (kv->dtype != DF2_F32 && kv->dtype != DF2_BF16) return fail_with(DF2_EINVAL, "unknown dtype");
     if (kv->B < 0 || kv->N < 0) return fail_with(DF2_EINVAL, "B and N must be >= 0");
@@ -41,6 +44,13 @@ inline df2_status check_kv_sizes(const df2_paged_kv* kv) {
     if ((int64_t)kv->table_width * kv->page_size > (1 << 30))
         return fail_with(DF2_EUNSUPPORTED, "table_width * page_size above 2^30");
     if ((int64_t)kv->N * kv->Hq > 0x7FFFFFFF) return fail_with(DF2_EUNSUPPORTED, "N * Hq too large");
+    if (fp4) {
+        if (kv->page_size < 16) return fail_with(DF2_EUNSUPPORTED, "page_size of a 4-bit cache must be at least 16");
+        if (kv->page_stride < (int64_t)kv->Hkv * kv->page_size * (kv->D / 2 + kv->D / 32))
+            return fail_with(DF2_EINVAL, "page_stride below Hkv * page_size * (D / 2 + D / 32)");
+        if (kv->page_stride % 16 != 0) return fail_with(DF2_EINVAL, "page_stride must be a multiple of 16 bytes");
+        return DF2_OK;
+    }
     const int64_t page = (int64_t)kv->Hkv * kv->page_size * kv->D;
     if (kv->page_stride < page) return fail_with(DF2_EINVAL, "page_stride below Hkv * page_size * D");
     const int per16 = kv->dtype == DF2_BF16 ? 8 : 4;
@@ -49,8 +59,8 @@ inline df2_status check_kv_sizes(const df2_paged_kv* kv) {
 }
 
 // Checks a cache descriptor and fills what the kernels read of it.
-inline df2_status read_kv(const df2_paged_kv* kv, PagedKv* out) {
-    const df2_status st = check_kv_sizes(kv);
+inline df2_status read_kv(const df2_paged_kv* kv, PagedKv* out, bool fp4 = false) {
+    const df2_status st = check_kv_sizes(kv, fp4);
     if (st != DF2_OK || kv->B == 0 || kv->N == 0) return st;
     if (!kv->k_cache || !kv->v_cache || !kv->block_table || !kv->ctx_len || !kv->tok_start)
         return fail_with(DF2_EINVAL, "NULL pointer in the cache descriptor");
@@ -106,6 +116,59 @@ inline bool rows_meet(const df2_paged_kv* kv, const TokenRows& a, const TokenRow
         if (j <= last && j * sb < x + wa) return true;
     }
     return false;
+}
+
+// Checks the arguments of an append and fills what its kernels read.
+inline df2_status read_append(const df2_paged_kv* kv, bool fp4, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const void* q_norm, const void* k_norm,
+                              float eps, const double* rope_freq, int32_t rot, int32_t interleaved, void* out_q,
+                              int64_t out_q_stride, AppendArgs* a) {
+    std::memset(a, 0, sizeof(*a));
+    df2_status st = read_kv(kv, &a->kv, fp4);
+    if (st != DF2_OK) return st;
+    if (rot < 0 || rot > kv->D || rot % 16 != 0)
+        return fail_with(DF2_EUNSUPPORTED, "rot must be a multiple of 16 in [0, D]");
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail_with(DF2_EINVAL, "eps must be finite and >= 0");
+    if (kv->B == 0 || kv->N == 0) return DF2_OK;
+    if (((int64_t)kv->N + 3) / 4 * 256 > kMostThreads) return fail_with(DF2_EUNSUPPORTED, "N above 2^26 - 4");
+    if (!k || !v || (rot > 0 && !rope_freq)) return fail_with(DF2_EINVAL, "NULL pointer argument");
+    if (!q != !out_q) return fail_with(DF2_EINVAL, "q and out_q come together");
+    if (!q && q_norm) return fail_with(DF2_EINVAL, "q_norm without q");
+    if ((st = check_rows(kv, k, k_stride, kv->Hkv, "k")) != DF2_OK) return st;
+    if ((st = check_rows(kv, v, v_stride, kv->Hkv, "v")) != DF2_OK) return st;
+    if (q) {
+        if ((st = check_rows(kv, q, q_stride, kv->Hq, "q")) != DF2_OK) return st;
+        if ((st = check_rows(kv, out_q, out_q_stride, kv->Hq, "out_q")) != DF2_OK) return st;
+        if (q == out_q && q_stride != out_q_stride)
+            return fail_with(DF2_EINVAL, "out_q in place of q needs the same stride");
+    }
+    if (!aligned(q_norm, 16) || !aligned(k_norm, 16))
+        return fail_with(DF2_EINVAL, "q_norm and k_norm must be 16-byte aligned");
+    if (!aligned(rope_freq, 8)) return fail_with(DF2_EINVAL, "rope_freq must be 8-byte aligned");
+    if (q) {
+        const TokenRows out = {out_q, out_q_stride, kv->Hq};
+        if ((q != out_q && rows_meet(kv, {q, q_stride, kv->Hq}, out)) || rows_meet(kv, {k, k_stride, kv->Hkv}, out) ||
+            rows_meet(kv, {v, v_stride, kv->Hkv}, out))
+            return fail_with(DF2_EINVAL, "out_q must not overlap q (unless it is q), k or v");
+    }
+    if ((st = device_flag_word(&a->kv.err)) != DF2_OK) return st;
+    a->q = q;
+    a->k = k;
+    a->v = v;
+    a->k_cache = kv->k_cache;
+    a->v_cache = kv->v_cache;
+    a->out_q = out_q;
+    a->q_norm = q_norm;
+    a->k_norm = k_norm;
+    a->freq = rope_freq;
+    a->q_stride = q_stride;
+    a->k_stride = k_stride;
+    a->v_stride = v_stride;
+    a->out_stride = out_q_stride;
+    a->rot = rot;
+    a->interleaved = interleaved ? 1 : 0;
+    a->eps = eps;
+    return DF2_OK;
 }
 
 // Calls f with the cache's type and head size as constants.

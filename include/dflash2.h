@@ -508,6 +508,44 @@ df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_
                                    int32_t max_len, void* out, int64_t out_stride,
                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * A paged cache of 4-bit values (a quarter of the bytes that attention reads of a
+ * bf16 one, and a thirteenth more for the scales).  Its descriptor is df2_paged_kv with
+ *   k_cache, v_cache  pages of Hkv heads; a head of a page holds its tokens' codes,
+ *                page_size rows of D / 2 bytes (the first of two elements in the low
+ *                half), then their scales, page_size rows of D / 32 bytes
+ *   page_stride  in bytes, a multiple of 16
+ *   page_size    16 at least
+ *   dtype        of the token rows (queries, keys, values, outputs)
+ * Each block of 32 neighbouring elements of a head has one scale, a power of two held
+ * as its exponent plus 127, and codes of a sign and one of the magnitudes 0, 1/2, 1,
+ * 3/2, 2, 3, 4, 6 (4-bit floats of the microscaling formats).  The append chooses the
+ * smallest power, from 2^-120 to 2^120, of which the block's largest magnitude is at
+ * most 7, and the nearest codes, ties to the even one; a block with an infinity or NaN
+ * gets scale 255, which makes all of it NaN.  Scales 0 to 254 are read as 2^(byte - 127).
+ */
+
+/*
+ * dflash2_kv_append into a 4-bit cache: same arguments, same queries.  Keys are normed
+ * and rotated in fp64 and rounded once, to their codes, so that a cache depends on
+ * nothing but its tokens.
+ */
+df2_status dflash2_kv_append_fp4(const df2_paged_kv* kv, const void* q, int64_t q_stride,
+                                 const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                 const void* q_norm, const void* k_norm, float eps,
+                                 const double* rope_freq, int32_t rot, int32_t interleaved,
+                                 void* out_q, int64_t out_q_stride, hipStream_t stream);
+
+/*
+ * What all pages of a 4-bit cache hold, as numbers (exact in either type but for
+ * magnitudes outside its range): out_k, out_v [num_pages, Hkv, page_size, D] (dtype), a
+ * cache as the other paged operators take it, 16-byte aligned; they must not overlap
+ * the cache or each other.  Of the descriptor, the tables and lengths and N and B's values are not
+ * used.  Up to 2^34 values in each.
+ */
+df2_status dflash2_kv_unpack_fp4(const df2_paged_kv* kv, void* out_k, void* out_v,
+                                 hipStream_t stream);
+
 /* What the rows given to dflash2_verify hold. */
 typedef enum { DF2_TARGET_LOGITS = 0, DF2_TARGET_PROBS = 1 } df2_target_kind;
 
