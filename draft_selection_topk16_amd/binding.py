@@ -33,7 +33,8 @@ EXPORTED = (
     "dflash2_select_sample_rows", "dflash2_draft_rows",
     "dflash2_kv_append", "dflash2_paged_attention", "dflash2_paged_attention_workspace",
     "dflash2_verify", "dflash2_verify_workspace", "dflash2_plan_pages", "dflash2_adjust_logits",
-    "dflash2_kv_append_fp4", "dflash2_kv_unpack_fp4",
+    "dflash2_kv_append_fp4", "dflash2_kv_unpack_fp4", "dflash2_paged_attention_fp4",
+    "dflash2_paged_attention_fp4_workspace",
     "dflash2_conv2", "dflash2_device_error",
     "dflash2_plan_override",
     "dflash2_release",
@@ -127,6 +128,8 @@ def load() -> ctypes.CDLL:
                                     vp],
         "dflash2_verify": [vdp, vp, vp, vp, vp, vp, ctypes.c_double, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
         "dflash2_kv_append_fp4": [kvp, vp, i64, vp, i64, vp, i64, vp, vp, ctypes.c_float, vp, i32, i32, vp, i64, vp],
+        "dflash2_paged_attention_fp4": [kvp, vp, i64, ctypes.c_float, i32, i32, i32, vp, i64, vp, ctypes.c_size_t,
+                                        vp],
         "dflash2_kv_unpack_fp4": [kvp, vp, vp, vp],
         "dflash2_plan_pages": [ctypes.POINTER(PagePool), vp, vp, vp, vp, vp, vp, vp, vp],
         "dflash2_adjust_logits": [ctypes.POINTER(Adjust), vp, vp, vp],
@@ -137,7 +140,9 @@ def load() -> ctypes.CDLL:
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = ctypes.c_int
-    for name, args in {"dflash2_paged_attention_workspace": [kvp, i32], "dflash2_verify_workspace": [vdp]}.items():
+    for name, args in {"dflash2_paged_attention_workspace": [kvp, i32],
+                       "dflash2_paged_attention_fp4_workspace": [kvp, i32],
+                       "dflash2_verify_workspace": [vdp]}.items():
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = ctypes.c_size_t
     for name in ("dflash2_status_string",):

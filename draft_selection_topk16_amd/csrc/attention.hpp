@@ -45,6 +45,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "fp4.hpp"
 #include "lanes.hpp"
 
 namespace df2 {
@@ -427,6 +428,13 @@ __device__ __forceinline__ void load_to_lds(const void* base, const uint32_t* of
 #undef DF2_TO_LDS_2
 #undef DF2_TO_LDS_4
 
+// x * c - m with the product rounded.
+__device__ __forceinline__ float scaled_minus(float x, float c, float m) {
+#pragma clang fp contract(off)
+    const float y = x * c;
+    return y - m;
+}
+
 template <bool BF16, int D>
 struct AttnTile {
     static constexpr int kEsz = BF16 ? 2 : 4;
@@ -449,13 +457,15 @@ struct AttnTile {
 // a wave in each tile, NS stages of tiles in LDS.  More than two stages, with as
 // many bytes in flight, were slower wherever they were tried (one row block on
 // 131 thousand keys: 262 us with three, 349 with five).
-template <bool BF16, int D, int WR, int WK, int KS, int NS>
+// FP4: the cache holds 4-bit values (fp4.hpp), which become BF16's type on their way
+// into the tiles.
+template <bool BF16, int D, int WR, int WK, int KS, int NS, bool FP4>
 __global__ void k_attend(AttnArgs a);
 
-template <bool BF16, int D, int WR, int WK, int KS, int NS>
+template <bool BF16, int D, int WR, int WK, int KS, int NS, bool FP4 = false>
 struct AttnShape {
     using Tile = AttnTile<BF16, D>;
-    static constexpr auto kernel() { return &k_attend<BF16, D, WR, WK, KS, NS>; }
+    static constexpr auto kernel() { return &k_attend<BF16, D, WR, WK, KS, NS, FP4>; }
     static constexpr int kWaves = WR * WK;
     static constexpr int kThreads = 64 * kWaves;
     static constexpr int BM = 32 * WR;
@@ -499,9 +509,9 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float (&x)[4
     }
 }
 
-template <bool BF16, int D, int WR, int WK, int KS, int NS>
-__global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::kSimdWaves)) void k_attend(AttnArgs a) {
-    using Shape = AttnShape<BF16, D, WR, WK, KS, NS>;
+template <bool BF16, int D, int WR, int WK, int KS, int NS, bool FP4>
+__global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, FP4>::kSimdWaves)) void k_attend(AttnArgs a) {
+    using Shape = AttnShape<BF16, D, WR, WK, KS, NS, FP4>;
     using Tile = AttnTile<BF16, D>;
     constexpr int RB = Tile::kRow, CH = Tile::kChunks, KT = Shape::KT, BM = Shape::BM;
     constexpr int NL = Shape::kLoads, DB = D / 32;
@@ -645,6 +655,61 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::
         load_tile(a.v, k0, lds0 + (NS + slot) * Shape::kTileBytes, page0, at_v);
     };
 
+    // A 4-bit cache: a thread brings whole blocks of 32 codes and their scales into
+    // registers, a tile ahead, and puts them into the tile as the products take them.
+    // A page has 16 keys at least, so neighbouring threads read neighbouring bytes.
+    constexpr int NB = D / kFp4Block, NI = (KT * NB + Shape::kThreads - 1) / Shape::kThreads;
+    u32x4_t codes_k[FP4 ? NI : 1], codes_v[FP4 ? NI : 1];
+    uint32_t scale_k[FP4 ? NI : 1], scale_v[FP4 ? NI : 1];
+    auto fetch = [&](int k0, int page0) {
+        if constexpr (FP4) {
+            const int64_t head_at = head_kv * Fp4Page<D>::bytes(kv.page_shift);
+            const int64_t scales_at = Fp4Page<D>::scales(kv.page_shift);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int x = i * Shape::kThreads + threadIdx.x;
+                if (KT * NB % Shape::kThreads != 0 && x >= KT * NB) break;
+                const int key = min(max(k0 + x / NB, klo), khi - 1), slot = key & page_mask;
+                const int64_t at = (int64_t)ids[(key >> kv.page_shift) - page0] * kv.page_stride + head_at;
+                const int64_t code = at + slot * Fp4Page<D>::kCodes + x % NB * (kFp4Block / 2);
+                const int64_t scale = at + scales_at + slot * NB + x % NB;
+                codes_k[i] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint8_t*>(a.k) + code);
+                codes_v[i] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint8_t*>(a.v) + code);
+                scale_k[i] = reinterpret_cast<const uint8_t*>(a.k)[scale];
+                scale_v[i] = reinterpret_cast<const uint8_t*>(a.v)[scale];
+            }
+        }
+    };
+    auto put = [&](int slot) {
+        if constexpr (FP4) {
+            constexpr int BC = CH / NB;         // chunks of a block
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int x = i * Shape::kThreads + threadIdx.x;
+                if (KT * NB % Shape::kThreads != 0 && x >= KT * NB) break;
+                const int row = x / NB, first = x % NB * BC;
+                unsigned char* to_k = lds + slot * Shape::kTileBytes + row * RB;
+                unsigned char* to_v = to_k + NS * Shape::kTileBytes;
+                const float sk = fp4_scale(scale_k[i]), sv = fp4_scale(scale_v[i]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if constexpr (BF16) {
+                        *reinterpret_cast<u32x4_t*>(to_k + ((first + c) ^ Tile::swz_k(row)) * 16) = fp4_to_bf16(codes_k[i][c], sk);
+                        *reinterpret_cast<u32x4_t*>(to_v + ((first + c) ^ Tile::swz_v(row)) * 16) = fp4_to_bf16(codes_v[i][c], sv);
+                    } else {
+                        f32x4_t lo, hi;
+                        fp4_to_f32(codes_k[i][c], sk, lo, hi);
+                        *reinterpret_cast<f32x4_t*>(to_k + ((first + 2 * c) ^ Tile::swz_k(row)) * 16) = lo;
+                        *reinterpret_cast<f32x4_t*>(to_k + ((first + 2 * c + 1) ^ Tile::swz_k(row)) * 16) = hi;
+                        fp4_to_f32(codes_v[i][c], sv, lo, hi);
+                        *reinterpret_cast<f32x4_t*>(to_v + ((first + 2 * c) ^ Tile::swz_v(row)) * 16) = lo;
+                        *reinterpret_cast<f32x4_t*>(to_v + ((first + 2 * c + 1) ^ Tile::swz_v(row)) * 16) = hi;
+                    }
+                }
+            }
+        }
+    };
+
     // The first product of a tile, the scores of its keys for this wave's rows:
     // product u = q * KS + ks takes chunk q of sub-tile ks (neighbouring products
     // add to different sums).
@@ -731,8 +796,18 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::
     // rounding of the output alone, with it.
     constexpr bool kLow = BF16 && WR <= 2;
     constexpr int PN = BF16 ? (kLow ? 16 : 8) : 16;
-    auto weights = [&](const f32x16_t (&x)[KS], uint32_t (&p)[KS][PN]) {
-        const float ms = m == -INFINITY ? 0.f : m;
+    bool huge = false;                  // some row's maximum is beyond 2^26
+    auto weights = [&](f32x16_t (&x)[KS], uint32_t (&p)[KS][PN]) {
+        float ms = m == -INFINITY ? 0.f : m;
+        // m is rounded and x * c below is not: from 2^26 on they differ by more than 1, and
+        // from 2^31 on the exponential of the difference overflows.  There, both rounded.
+        if (huge) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) x[ks][v] = scaled_minus(x[ks][v], a.c, ms) / a.c;
+            ms = 0.f;
+        }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             float e[16];
@@ -763,6 +838,7 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::
             const float mn = fmaxf(m, mx);
             const float f = m == mn ? 1.f : __builtin_amdgcn_exp2f(m - mn);
             m = mn;
+            huge = __any(fabsf(m) > 0x1p26f && m != -INFINITY);
             l *= f;
 #pragma unroll
             for (int d = 0; d < DB; ++d)
@@ -836,29 +912,48 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS>::
 #pragma unroll
         for (int q = 0; q < QN; ++q) asm volatile("" : "+v"(qf[q]));
         uint32_t p[KS][PN];
-        // A ring of NS tiles, NS - 1 of them in flight or waiting.
+        if constexpr (FP4) {
+            // two tiles in LDS, one more in registers
+            static_assert(NS == 2, "two stages");
+            fetch(k_win, page0);
+            put(0);
+            if (ntile > 1) fetch(k_win + KT, page0);
+            for (int it = 0; it < ntile; ++it) {
+                const int k0 = k_win + it * KT;
+                // the tile is whole, and nobody reads the one before it any more
+                __syncthreads();
+                if (it + 1 < ntile) put((it + 1) & 1);
+                if (it + 2 < ntile) fetch(k0 + 2 * KT, page0);
+                scores(it & 1, s);
+                move_max(mask_and_max(k0, s));
+                weights(s, p);
+                add_values(it & 1, p);
+            }
+        } else {
+            // A ring of NS tiles, NS - 1 of them in flight or waiting.
 #pragma unroll
-        for (int i = 0; i < NS - 1; ++i)
-            if (i < ntile) {
-                load_k(k_win + i * KT, i, page0);
-                load_v(k_win + i * KT, i, page0);
+            for (int i = 0; i < NS - 1; ++i)
+                if (i < ntile) {
+                    load_k(k_win + i * KT, i, page0);
+                    load_v(k_win + i * KT, i, page0);
+                }
+            int slot = 0;
+            for (int it = 0; it < ntile; ++it) {
+                const int k0 = k_win + it * KT;
+                // this wave's part of the oldest tile is in LDS; then everyone's is,
+                // and nobody reads the tile before it any more
+                wait_and_meet<NS - 2, 2 * NL>(ntile - 1 - it);
+                if (it + NS - 1 < ntile) {
+                    const int free = slot == 0 ? NS - 1 : slot - 1;
+                    load_k(k0 + (NS - 1) * KT, free, page0);
+                    load_v(k0 + (NS - 1) * KT, free, page0);
+                }
+                scores(slot, s);
+                move_max(mask_and_max(k0, s));
+                weights(s, p);
+                add_values(slot, p);
+                slot = slot == NS - 1 ? 0 : slot + 1;
             }
-        int slot = 0;
-        for (int it = 0; it < ntile; ++it) {
-            const int k0 = k_win + it * KT;
-            // this wave's part of the oldest tile is in LDS; then everyone's is,
-            // and nobody reads the tile before it any more
-            wait_and_meet<NS - 2, 2 * NL>(ntile - 1 - it);
-            if (it + NS - 1 < ntile) {
-                const int free = slot == 0 ? NS - 1 : slot - 1;
-                load_k(k0 + (NS - 1) * KT, free, page0);
-                load_v(k0 + (NS - 1) * KT, free, page0);
-            }
-            scores(slot, s);
-            move_max(mask_and_max(k0, s));
-            weights(s, p);
-            add_values(slot, p);
-            slot = slot == NS - 1 ? 0 : slot + 1;
         }
         k_win += ntile * KT;
     }

@@ -14,6 +14,7 @@
 #include "host.hpp"
 #include "target_host.hpp"
 #include "append_fp4.hpp"
+#include "attention_host.hpp"
 #include "fp4.hpp"
 
 using namespace df2;
@@ -78,6 +79,17 @@ df2_status dflash2_kv_unpack_fp4(const df2_paged_kv* kv, void* out_k, void* out_
                            stream, a);
         return launched("dflash2_kv_unpack_fp4 launch");
     });
+}
+
+size_t dflash2_paged_attention_fp4_workspace(const df2_paged_kv* kv, int32_t max_len) {
+    return attend_workspace<true>(kv, max_len);
+}
+
+df2_status dflash2_paged_attention_fp4(const df2_paged_kv* kv, const void* q, int64_t q_stride, float scale,
+                                       int32_t causal, int32_t window, int32_t max_len, void* out, int64_t out_stride,
+                                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    return attend<true>(kv, q, q_stride, scale, causal, window, max_len, out, out_stride, workspace, workspace_bytes,
+                        stream);
 }
 
 }  // extern "C"

@@ -106,6 +106,36 @@ class PreparedAppendFp4(_Prepared):
                     out_q)
 
 
+class PreparedAttentionFp4(_Prepared):
+    """dflash2_paged_attention_fp4: as PreparedAttention, over a 4-bit cache (k_cache,
+    v_cache uint8 [num_pages, Hkv, page_size * (D / 2 + D / 32)])."""
+
+    def __init__(self, q, k_cache, v_cache, block_table, ctx_len, tok_start, scale: Optional[float] = None,
+                 causal: bool = True, window: int = 0, max_len: Optional[int] = None,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+        lib = load()
+        length = min(int(max_len), 2**31 - 1) if max_len is not None else 0
+        _int32(window=int(window), max_len=length)
+        if q.dim() != 3:
+            raise ValueError("q must be [N, Hq, D]")
+        N, Hq, D = q.shape
+        self.kv = kv = _fp4_descriptor(k_cache, v_cache, block_table, ctx_len, tok_start, N, Hq, D, q)
+        q_stride = _rows(q, "q", N, Hq, D, q.dtype)
+        if out is None:
+            out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+        out_stride = _rows(out, "out", N, Hq, D, q.dtype)
+        need = lib.dflash2_paged_attention_fp4_workspace(ctypes.byref(kv), length)
+        if workspace is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+        elif workspace.dtype != torch.uint8:
+            raise ValueError("workspace must be uint8")
+        args = (ctypes.byref(kv), q.data_ptr(), q_stride, float(D ** -0.5 if scale is None else scale),
+                int(causal), int(window), length, out.data_ptr(), out_stride,
+                _dev(workspace, "workspace") if workspace.numel() else None, workspace.numel())
+        self._ready(lib.dflash2_paged_attention_fp4, args, k_cache.device,
+                    (q, k_cache, v_cache, block_table, ctx_len, tok_start, out, workspace), out)
+
+
 class PreparedUnpackFp4(_Prepared):
     """dflash2_kv_unpack_fp4: what all pages of a 4-bit cache of head size D hold.
     Calling it returns (keys, values) [num_pages, Hkv, page_size, D] in `dtype`, a cache
@@ -133,6 +163,15 @@ def kv_append_fp4(k, v, k_cache, v_cache, block_table, ctx_len, tok_start, q=Non
     the way (see PreparedAppendFp4): the queries, or None without q."""
     return PreparedAppendFp4(k, v, k_cache, v_cache, block_table, ctx_len, tok_start, q, q_norm, k_norm, eps, rope_freq,
                              interleaved, out_q)()
+
+
+def paged_attention_fp4(q, k_cache, v_cache, block_table, ctx_len, tok_start, scale: Optional[float] = None,
+                        causal: bool = True, window: int = 0, max_len: Optional[int] = None,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of the new tokens over their sequences' positions in a 4-bit cache (see
+    PreparedAttentionFp4): [N, Hq, D]."""
+    return PreparedAttentionFp4(q, k_cache, v_cache, block_table, ctx_len, tok_start, scale, causal, window, max_len,
+                                out)()
 
 
 def kv_unpack_fp4(k_cache, v_cache, D: int, dtype: torch.dtype = torch.bfloat16) -> Tuple[torch.Tensor, torch.Tensor]:

@@ -537,11 +537,26 @@ df2_status dflash2_kv_append_fp4(const df2_paged_kv* kv, const void* q, int64_t 
                                  void* out_q, int64_t out_q_stride, hipStream_t stream);
 
 /*
- * What all pages of a 4-bit cache hold, as numbers (exact in either type but for
- * magnitudes outside its range): out_k, out_v [num_pages, Hkv, page_size, D] (dtype), a
- * cache as the other paged operators take it, 16-byte aligned; they must not overlap
- * the cache or each other.  Of the descriptor, the tables and lengths and N and B's values are not
- * used.  Up to 2^34 values in each.
+ * dflash2_paged_attention over a 4-bit cache: same arguments, and the softmax over the
+ * values that the codes stand for.  bf16 calls multiply them as bf16, which they are exactly;
+ * scores, statistics, sums and probabilities as there.  Scales of positions that a
+ * token of the batch sees must be 7 to 247, as the append makes them for finite numbers;
+ * a sequence's values, added up with weights of up to 2^8 before they are divided by the
+ * sum, must stay finite in fp32 (any scale up to 2^90 will do).
+ */
+size_t dflash2_paged_attention_fp4_workspace(const df2_paged_kv* kv, int32_t max_len);
+df2_status dflash2_paged_attention_fp4(const df2_paged_kv* kv, const void* q, int64_t q_stride,
+                                       float scale, int32_t causal, int32_t window,
+                                       int32_t max_len, void* out, int64_t out_stride,
+                                       void* workspace, size_t workspace_bytes,
+                                       hipStream_t stream);
+
+/*
+ * What all pages of a 4-bit cache hold, as numbers (dtype; exact but for scales whose
+ * values leave its range): out_k, out_v [num_pages, Hkv, page_size, D], 16-byte aligned, a
+ * cache as the operators over one of that type take it.  They must not overlap the cache
+ * or each other.  block_table, ctx_len and tok_start may be NULL, B and N 0.  Up to 2^34
+ * values in each.
  */
 df2_status dflash2_kv_unpack_fp4(const df2_paged_kv* kv, void* out_k, void* out_v,
                                  hipStream_t stream);
