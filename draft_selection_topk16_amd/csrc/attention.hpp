@@ -87,7 +87,7 @@ struct AttnArgs {
     int bm;                 // rows of a block
     int wgs, whole;         // workgroups that take stretches; 1: each takes a whole block
     int cus;                // compute units
-    int join;               // there may be parts, and a workspace for them
+    int join;               // workgroups that join the parts at a boundary; 0: there are none
     int choose;             // blocks enough for the kernel to choose whole ones
     double inv_g;           // 1 / G
     float c;                // scale * log2(e)
@@ -475,7 +475,7 @@ struct AttnShape {
     static constexpr int kLoads = kTileBytes / (1024 * kWaves);     // of a wave for K, and for V
     static constexpr int kRows = KT / kWaves;                       // keys that they bring
     static constexpr int kGroup = kLoads % 4 == 0 && Tile::kRow >= 256 ? 4 : kLoads % 2 == 0 ? 2 : 1;
-    static constexpr int kGroupKeys = kGroup * (64 / Tile::kChunks);
+    static constexpr int kGroupKeys = FP4 ? 16 : kGroup * (64 / Tile::kChunks);
     // loads that may be in flight while the oldest stage is complete
     static constexpr int kAhead = (NS - 2) * 2 * kLoads;
     static constexpr int kMergeBytes = WK > 1 ? kWaves * (32 * D * 4 + 256) + BM * 8 : 0;
@@ -657,26 +657,55 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
 
     // A 4-bit cache: a thread brings whole blocks of 32 codes and their scales into
     // registers, a tile ahead, and puts them into the tile as the products take them.
-    // A page has 16 keys at least, so neighbouring threads read neighbouring bytes.
-    constexpr int NB = D / kFp4Block, NI = (KT * NB + Shape::kThreads - 1) / Shape::kThreads;
+    // Tiles start at multiples of 16 keys, which share a page, so a wave's load has one
+    // address but for its lanes' offsets (head size 64: two).  Keys outside the stretch may
+    // hold anything: their scores are masked, the scales of their values made 1.
+    constexpr int NB = D / kFp4Block, KL = 64 / NB;     // blocks of a key, keys of a wave's load
+    constexpr int FL = KT / KL, NI = (FL + Shape::kWaves - 1) / Shape::kWaves;      // loads of a tile, of a wave
     u32x4_t codes_k[FP4 ? NI : 1], codes_v[FP4 ? NI : 1];
     uint32_t scale_k[FP4 ? NI : 1], scale_v[FP4 ? NI : 1];
     auto fetch = [&](int k0, int page0) {
         if constexpr (FP4) {
             const int64_t head_at = head_kv * Fp4Page<D>::bytes(kv.page_shift);
             const int64_t scales_at = Fp4Page<D>::scales(kv.page_shift);
+            // codes and scales of key k's group of 16, from its page's head on
+            const auto group = [&](int k, int64_t& code, int64_t& scale) {
+                k = min(max(k, klo & ~15), (khi - 1) & ~15);
+                const int64_t at = (int64_t)__builtin_amdgcn_readfirstlane(ids[(k >> kv.page_shift) - page0]) * kv.page_stride + head_at;
+                code = at + (k & page_mask) * (D / 2);
+                scale = at + scales_at + (k & page_mask) * NB;
+            };
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int x = i * Shape::kThreads + threadIdx.x;
-                if (KT * NB % Shape::kThreads != 0 && x >= KT * NB) break;
-                const int key = min(max(k0 + x / NB, klo), khi - 1), slot = key & page_mask;
-                const int64_t at = (int64_t)ids[(key >> kv.page_shift) - page0] * kv.page_stride + head_at;
-                const int64_t code = at + slot * Fp4Page<D>::kCodes + x % NB * (kFp4Block / 2);
-                const int64_t scale = at + scales_at + slot * NB + x % NB;
-                codes_k[i] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint8_t*>(a.k) + code);
-                codes_v[i] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const uint8_t*>(a.v) + code);
-                scale_k[i] = reinterpret_cast<const uint8_t*>(a.k)[scale];
-                scale_v[i] = reinterpret_cast<const uint8_t*>(a.v)[scale];
+                const int li = i * Shape::kWaves + w;
+                if (FL % Shape::kWaves != 0 && li >= FL) break;
+                int64_t code, scale;
+                uint32_t key = lane / NB;       // in the group
+                if constexpr (KL == 32) {
+                    int64_t code2, scale2;
+                    group(k0 + li * KL, code, scale);
+                    group(k0 + li * KL + 16, code2, scale2);
+                    code = lane < 32 ? code : code2;
+                    scale = lane < 32 ? scale : scale2;
+                    key &= 15;
+                } else {
+                    group((k0 + li * KL) & ~15, code, scale);
+                    key += li * KL & 15;
+                }
+                const uint8_t* const ck = reinterpret_cast<const uint8_t*>(a.k) + code;
+                const uint8_t* const cv = reinterpret_cast<const uint8_t*>(a.v) + code;
+                const uint32_t off = key * (D / 2) + lane % NB * (kFp4Block / 2), off_s = key * NB + lane % NB;
+                codes_k[i] = *reinterpret_cast<const u32x4_t*>(ck + off);
+                codes_v[i] = *reinterpret_cast<const u32x4_t*>(cv + off);
+                scale_k[i] = (reinterpret_cast<const uint8_t*>(a.k) + scale)[off_s];
+                scale_v[i] = (reinterpret_cast<const uint8_t*>(a.v) + scale)[off_s];
+            }
+            if (k0 < klo || k0 + KT > khi) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int k = k0 + (i * Shape::kWaves + w) * KL + lane / NB;
+                    scale_v[i] = k >= klo && k < khi ? scale_v[i] : (uint32_t)kFp4Bias;
+                }
             }
         }
     };
@@ -685,9 +714,9 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
             constexpr int BC = CH / NB;         // chunks of a block
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int x = i * Shape::kThreads + threadIdx.x;
-                if (KT * NB % Shape::kThreads != 0 && x >= KT * NB) break;
-                const int row = x / NB, first = x % NB * BC;
+                const int li = i * Shape::kWaves + w;
+                if (FL % Shape::kWaves != 0 && li >= FL) break;
+                const int row = li * KL + lane / NB, first = lane % NB * BC;
                 unsigned char* to_k = lds + slot * Shape::kTileBytes + row * RB;
                 unsigned char* to_v = to_k + NS * Shape::kTileBytes;
                 const float sk = fp4_scale(scale_k[i]), sv = fp4_scale(scale_v[i]);
@@ -801,11 +830,12 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
         float ms = m == -INFINITY ? 0.f : m;
         // m is rounded and x * c below is not: from 2^26 on they differ by more than 1, and
         // from 2^31 on the exponential of the difference overflows.  There, both rounded.
-        if (huge) {
+        if (__builtin_expect(huge, 0)) {
+            const float back = 1.f / a.c;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int v = 0; v < 16; ++v) x[ks][v] = scaled_minus(x[ks][v], a.c, ms) / a.c;
+                for (int v = 0; v < 16; ++v) x[ks][v] = scaled_minus(x[ks][v], a.c, ms) * back;
             ms = 0.f;
         }
 #pragma unroll
@@ -1056,27 +1086,27 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
 
 // Joins the parts of the blocks that lie across workgroups:
 //     sum_s 2^(m_s - m) (o_s, l_s)
-// over the parts s of a row.  kJoinWgs workgroups for each boundary of stretches, of
+// over the parts s of a row.  Some workgroups (a.join) for each boundary of stretches, of
 // which the first inside a block does the block.  D / 4 lanes take a row, four parts
 // at a time; with more parts several such groups share the row and meet in LDS, so
 // that a hundred parts of a few rows are a few loads one after another.
-constexpr int kJoinWgs = 16, kJoinThreads = 256;
+constexpr int kJoinThreads = 256;
 template <bool BF16, int D>
 __global__ __launch_bounds__(kJoinThreads) void k_attend_join(AttnArgs a) {
     constexpr int L = D / 4, NG = kJoinThreads / L;
     __shared__ f32x4_t lds_y[kJoinThreads];
     __shared__ float lds_m[NG], lds_l[NG];
-    const int slice = blockIdx.x % kJoinWgs, boundary = 1 + blockIdx.x / kJoinWgs;
+    const int slice = blockIdx.x % (unsigned)a.join, boundary = 1 + blockIdx.x / (unsigned)a.join;
     const int32_t* split = a.split + 8 * boundary;
-    const int w0 = boundary - 1, w1 = min(split[0], (int)(gridDim.x / kJoinWgs));
+    const int w0 = boundary - 1, w1 = min(split[0], (int)(gridDim.x / (unsigned)a.join));
     const int h = split[1], s0 = split[2], r0 = split[3], M = split[4];
     if (w1 < 0) return;
     const int group = threadIdx.x / L, d = (threadIdx.x % L) * 4;
     const int live = min(a.bm, M - r0);
     int share = 1;                                      // groups of a row, as long as one go takes all rows
-    while (4 * share < w1 - w0 + 1 && share < NG && live * share * 2 <= NG * kJoinWgs) share *= 2;
+    while (4 * share < w1 - w0 + 1 && share < NG && live * share * 2 <= NG * a.join) share *= 2;
     const int at_once = NG / share;
-    for (int i0 = slice * at_once; i0 < live; i0 += kJoinWgs * at_once) {
+    for (int i0 = slice * at_once; i0 < live; i0 += a.join * at_once) {
         const int i = i0 + group / share, r = r0 + i;
         float m = -INFINITY, l = 0.f;
         f32x4_t y = {0.f, 0.f, 0.f, 0.f};

@@ -14,6 +14,7 @@
 #include "dflash2.h"
 #include "host.hpp"
 #include "attention.hpp"
+#include "attention_fp4.hpp"
 #include "target_host.hpp"
 
 namespace df2 {
@@ -40,6 +41,10 @@ struct AttnPlan {
 template <bool BF16, int D, bool FP4, typename F>
 auto with_shape(int wr, F&& f) {
     constexpr int RB = AttnTile<BF16, D>::kRow;
+    if constexpr (FP4) {
+        if (wr == 0) return f(FewShape<BF16, D, 16>());
+        if (wr == 1) return f(FewShape<BF16, D, 32>());
+    }
     if constexpr (RB == 128) {
         if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2, FP4>());
         if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 2, 2, FP4>());
@@ -47,7 +52,7 @@ auto with_shape(int wr, F&& f) {
         return f(AttnShape<BF16, D, 8, 1, 2, 2, FP4>());
     } else if constexpr (RB == 256 && BF16) {
         if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2, FP4>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, 1, 2, 2, FP4>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, FP4 ? 2 : 1, FP4 ? 1 : 2, 2, FP4>());
         if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2, FP4>());
         return f(AttnShape<BF16, D, 8, 1, 4, 2, FP4>());
     } else if constexpr (RB == 256) {
@@ -82,7 +87,7 @@ AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
     const int64_t each = (rows + seqs - 1) / seqs;
     int per_cu = 1, threads = 64;
     const auto tiles = [&](int64_t len) { return (len + pl.gk + pl.kt - 1) / pl.kt; };
-    for (pl.wr = each <= 32 ? 1 : each <= 64 ? 2 : each <= 128 ? 4 : 8;; pl.wr /= 2) {
+    for (pl.wr = FP4 && each <= 16 ? 0 : each <= 32 ? 1 : each <= 64 ? 2 : each <= 128 ? 4 : 8;; pl.wr /= 2) {
         with_type(kv, [&](auto bf16, auto d) {
             return with_shape<decltype(bf16)::value, decltype(d)::value, FP4>(pl.wr, [&](auto shape) {
                 using S = decltype(shape);
@@ -94,7 +99,7 @@ AttnPlan plan_attend(const df2_paged_kv* kv, int max_len) {
                 return 0;
             });
         });
-        if (pl.wr == 1 || seqs * ((each + pl.bm - 1) / pl.bm) * kv->Hkv * tiles(max_len) >= 3 * compute_units()) break;
+        if (pl.wr <= 1 || seqs * ((each + pl.bm - 1) / pl.bm) * kv->Hkv * tiles(max_len) >= 3 * compute_units()) break;
     }
     const int64_t blocks = rows / pl.bm + seqs;     // one more in each sequence that has tokens
     const int64_t resident = (int64_t)compute_units() * per_cu;
@@ -135,7 +140,7 @@ df2_status launch_attend(const AttnPlan& pl, const AttnArgs& a, hipStream_t stre
         return launched("dflash2_paged_attention launch");
     });
     if (st != DF2_OK || !a.join) return st;
-    hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)(kJoinWgs * (pl.wgs - 1))),
+    hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)(a.join * (pl.wgs - 1))),
                        dim3(kJoinThreads), 0, stream, a);
     return launched("dflash2_paged_attention join launch");
 }
@@ -193,7 +198,7 @@ df2_status attend(const df2_paged_kv* kv, const void* q, int64_t q_stride, float
     a.wgs = pl.wgs;
     a.whole = pl.whole;
     a.cus = compute_units();
-    a.join = pl.bytes > 0;
+    a.join = pl.bytes == 0 ? 0 : FP4 && pl.wr <= 1 ? 4 : 16;
     a.choose = pl.choose;
     a.inv_g = 1.0 / a.G;
     a.c = (float)((double)scale * 1.4426950408889634);
