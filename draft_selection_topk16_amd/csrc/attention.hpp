@@ -435,19 +435,26 @@ __device__ __forceinline__ float scaled_minus(float x, float c, float m) {
     return y - m;
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool FP4 = false>
 struct AttnTile {
     static constexpr int kEsz = BF16 ? 2 : 4;
     static constexpr int kRow = D * kEsz;       // bytes of a key
     static constexpr int kChunks = kRow / 16;
+    // From 4-bit values: both, and 16 lanes write whole blocks of four chunks of rows that
+    // are four apart.
+    static __device__ __forceinline__ int swz_fp4(int row) {
+        return kChunks >= 16 ? (row & 3) << 2 | ((row >> 2) & 3) : ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
+    }
     // Permutation of a row's chunks.  K: 16 keys read one chunk each in one go,
     // so they get 16 different places of the 256 bytes that the banks span.
     static __device__ __forceinline__ int swz_k(int row) {
+        if constexpr (FP4 && BF16) return swz_fp4(row);
         return kChunks >= 16 ? (row & 15) : ((row >> 1) & 7);
     }
     // V: bf16, four keys of 64 bytes are read in one go; fp32, 128 bytes of
     // two keys that are four apart.
     static __device__ __forceinline__ int swz_v(int row) {
+        if constexpr (FP4 && BF16) return swz_fp4(row);
         if constexpr (!BF16) return ((row >> 2) & 1) << 3;
         return kChunks >= 16 ? ((row & 3) << 2) : (((row >> 1) & 1) << 2);
     }
@@ -464,7 +471,7 @@ __global__ void k_attend(AttnArgs a);
 
 template <bool BF16, int D, int WR, int WK, int KS, int NS, bool FP4 = false>
 struct AttnShape {
-    using Tile = AttnTile<BF16, D>;
+    using Tile = AttnTile<BF16, D, FP4>;
     static constexpr auto kernel() { return &k_attend<BF16, D, WR, WK, KS, NS, FP4>; }
     static constexpr int kWaves = WR * WK;
     static constexpr int kThreads = 64 * kWaves;
@@ -477,7 +484,7 @@ struct AttnShape {
     static constexpr int kGroup = kLoads % 4 == 0 && Tile::kRow >= 256 ? 4 : kLoads % 2 == 0 ? 2 : 1;
     static constexpr int kGroupKeys = FP4 ? 16 : kGroup * (64 / Tile::kChunks);
     // loads that may be in flight while the oldest stage is complete
-    static constexpr int kAhead = (NS - 2) * 2 * kLoads;
+    static constexpr int kAhead = NS > 2 ? (NS - 2) * 2 * kLoads : 0;
     static constexpr int kMergeBytes = WK > 1 ? kWaves * (32 * D * 4 + 256) + BM * 8 : 0;
     static constexpr int kLds = NS * kStage > kMergeBytes ? NS * kStage : kMergeBytes;   // tiles, or the merge
     static constexpr int kAllLds = kLds + 4 * kPageIds;
@@ -512,7 +519,7 @@ __device__ __forceinline__ void store4(void* out, int64_t at, const float (&x)[4
 template <bool BF16, int D, int WR, int WK, int KS, int NS, bool FP4>
 __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, FP4>::kSimdWaves)) void k_attend(AttnArgs a) {
     using Shape = AttnShape<BF16, D, WR, WK, KS, NS, FP4>;
-    using Tile = AttnTile<BF16, D>;
+    using Tile = AttnTile<BF16, D, FP4>;
     constexpr int RB = Tile::kRow, CH = Tile::kChunks, KT = Shape::KT, BM = Shape::BM;
     constexpr int NL = Shape::kLoads, DB = D / 32;
     extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
@@ -664,6 +671,8 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
     constexpr int FL = KT / KL, NI = (FL + Shape::kWaves - 1) / Shape::kWaves;      // loads of a tile, of a wave
     u32x4_t codes_k[FP4 ? NI : 1], codes_v[FP4 ? NI : 1];
     uint32_t scale_k[FP4 ? NI : 1], scale_v[FP4 ? NI : 1];
+    // this lane's key of a load: with 16 keys, four lanes of a row, then rows that are four apart
+    const int load_key = KL == 16 && BF16 ? (lane / NB & 3) * 4 + lane / (4 * NB) : lane / NB;
     auto fetch = [&](int k0, int page0) {
         if constexpr (FP4) {
             const int64_t head_at = head_kv * Fp4Page<D>::bytes(kv.page_shift);
@@ -680,7 +689,7 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
                 const int li = i * Shape::kWaves + w;
                 if (FL % Shape::kWaves != 0 && li >= FL) break;
                 int64_t code, scale;
-                uint32_t key = lane / NB;       // in the group
+                uint32_t key = load_key;        // in the group
                 if constexpr (KL == 32) {
                     int64_t code2, scale2;
                     group(k0 + li * KL, code, scale);
@@ -703,7 +712,7 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
             if (k0 < klo || k0 + KT > khi) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const int k = k0 + (i * Shape::kWaves + w) * KL + lane / NB;
+                    const int k = k0 + (i * Shape::kWaves + w) * KL + load_key;
                     scale_v[i] = k >= klo && k < khi ? scale_v[i] : (uint32_t)kFp4Bias;
                 }
             }
@@ -716,7 +725,7 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
             for (int i = 0; i < NI; ++i) {
                 const int li = i * Shape::kWaves + w;
                 if (FL % Shape::kWaves != 0 && li >= FL) break;
-                const int row = li * KL + lane / NB, first = lane % NB * BC;
+                const int row = li * KL + load_key, first = lane % NB * BC;
                 unsigned char* to_k = lds + slot * Shape::kTileBytes + row * RB;
                 unsigned char* to_v = to_k + NS * Shape::kTileBytes;
                 const float sk = fp4_scale(scale_k[i]), sv = fp4_scale(scale_v[i]);
@@ -822,8 +831,9 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
     // 16 after 1000 23.3 and 23.6, head size 256 61.5 and 64.2); blocks of 128 rows lose a
     // tenth by it (79 and 87) and prompt chunks more (690 and 940), so there the weights
     // are rounded.  Outputs against fp64, relative: 2.1e-3 without it, 1.7e-3, the
-    // rounding of the output alone, with it.
-    constexpr bool kLow = BF16 && WR <= 2;
+    // rounding of the output alone, with it.  Over a 4-bit cache blocks of 64 rows are bound
+    // by the products too, and do without (32 contexts: 119 us with it, 103; 2.1e-3).
+    constexpr bool kLow = BF16 && WR <= 2 && !FP4;
     constexpr int PN = BF16 ? (kLow ? 16 : 8) : 16;
     bool huge = false;                  // some row's maximum is beyond 2^26
     auto weights = [&](f32x16_t (&x)[KS], uint32_t (&p)[KS][PN]) {
@@ -884,10 +894,11 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
     auto value_operand = [&](int slot, int u) {
         typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
         const int d = u % DB, keys = u / DB * 16;       // 16 rows on: the same permutation
-        const unsigned char* from = lds + (NS + slot) * Shape::kTileBytes + keys * RB + v_row * RB + (lane & 1) * 8 +
-                                    ((4 * d + v_chunk) ^ Tile::swz_v(v_row)) * 16;
-        const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)from);
-        const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(from + 8 * RB));
+        const unsigned char* from = lds + (NS + slot) * Shape::kTileBytes + keys * RB + v_row * RB + (lane & 1) * 8;
+        const s16x4_t v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)(from + ((4 * d + v_chunk) ^ Tile::swz_v(v_row)) * 16));
+        const s16x4_t v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)(from + 8 * RB + ((4 * d + v_chunk) ^ Tile::swz_v(v_row + 8)) * 16));
         return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
     };
     auto value_product = [&](int u, u32x4_t vf, const uint32_t (&p)[KS][PN]) {
@@ -943,21 +954,24 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
         for (int q = 0; q < QN; ++q) asm volatile("" : "+v"(qf[q]));
         uint32_t p[KS][PN];
         if constexpr (FP4) {
-            // two tiles in LDS, one more in registers
-            static_assert(NS == 2, "two stages");
+            // NS tiles in LDS, one more in registers
+            static_assert(NS <= 2, "one stage or two");
             fetch(k_win, page0);
-            put(0);
-            if (ntile > 1) fetch(k_win + KT, page0);
+            if constexpr (NS == 2) {
+                put(0);
+                if (ntile > 1) fetch(k_win + KT, page0);
+            }
             for (int it = 0; it < ntile; ++it) {
-                const int k0 = k_win + it * KT;
-                // the tile is whole, and nobody reads the one before it any more
+                const int k0 = k_win + it * KT, slot = it & (NS - 1);
+                // two: the tile is whole, and nobody reads the one before it any more
                 __syncthreads();
-                if (it + 1 < ntile) put((it + 1) & 1);
-                if (it + 2 < ntile) fetch(k0 + 2 * KT, page0);
-                scores(it & 1, s);
+                if (it + NS - 1 < ntile) put((it + NS - 1) & (NS - 1));
+                if (it + NS < ntile) fetch(k0 + NS * KT, page0);
+                if constexpr (NS == 1) __syncthreads();
+                scores(slot, s);
                 move_max(mask_and_max(k0, s));
                 weights(s, p);
-                add_values(it & 1, p);
+                add_values(slot, p);
             }
         } else {
             // A ring of NS tiles, NS - 1 of them in flight or waiting.

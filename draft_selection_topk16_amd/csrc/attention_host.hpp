@@ -29,6 +29,32 @@ struct AttnPlan {
     size_t part = 0, bytes = 0; // workspace: the parts' outputs, all of it
 };
 
+// Over a 4-bit cache: blocks of 16 and 32 rows (wr 0 and 1) have a kernel of their own.
+// Blocks of 64 rows are bound by the products and the instructions around them, not by
+// the bytes, and want two waves a SIMD: four waves a workgroup, two workgroups a compute
+// unit (32 contexts of 301 to 12007 tokens, 8 new, 64 / 8 heads: two waves 147 us, four
+// 116, with one stage of 128 keys and weights of one bf16 part 100).
+template <bool BF16, int D, typename F>
+auto with_fp4_shape(int wr, F&& f) {
+    constexpr int RB = AttnTile<BF16, D>::kRow;
+    if (wr == 0) return f(FewShape<BF16, D, 16>());
+    if (wr == 1) return f(FewShape<BF16, D, 32>());
+    if constexpr (RB == 128) {
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 2, 2, true>());
+        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2, true>());
+        return f(AttnShape<BF16, D, 8, 1, 2, 2, true>());
+    } else if constexpr (RB == 256 && BF16) {
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 2, 1, true>());
+        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2, true>());
+        return f(AttnShape<BF16, D, 8, 1, 4, 2, true>());
+    } else if constexpr (RB <= 512) {
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2, true>());
+        return f(AttnShape<BF16, D, 4, 1, 1, 2, true>());
+    } else {
+        return f(AttnShape<BF16, D, 4, 1, 1, 2, true>());
+    }
+}
+
 // The kernels there are: rows (WR waves of 32), key groups, 32-key steps.  A block
 // of few rows gets its waves from groups of keys (one row after 1003 tokens, event
 // times: 9.7 us and 6.0 for the join with four groups, 8.8 and 7.4 with one, which
@@ -42,29 +68,27 @@ template <bool BF16, int D, bool FP4, typename F>
 auto with_shape(int wr, F&& f) {
     constexpr int RB = AttnTile<BF16, D>::kRow;
     if constexpr (FP4) {
-        if (wr == 0) return f(FewShape<BF16, D, 16>());
-        if (wr == 1) return f(FewShape<BF16, D, 32>());
-    }
-    if constexpr (RB == 128) {
-        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2, FP4>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 2, 2, FP4>());
-        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2, FP4>());
-        return f(AttnShape<BF16, D, 8, 1, 2, 2, FP4>());
+        return with_fp4_shape<BF16, D>(wr, f);
+    } else if constexpr (RB == 128) {
+        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 2, 2>());
+        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2>());
+        return f(AttnShape<BF16, D, 8, 1, 2, 2>());
     } else if constexpr (RB == 256 && BF16) {
-        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2, FP4>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, FP4 ? 2 : 1, FP4 ? 1 : 2, 2, FP4>());
-        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2, FP4>());
-        return f(AttnShape<BF16, D, 8, 1, 4, 2, FP4>());
+        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 1, 2, 2>());
+        if (wr == 4) return f(AttnShape<BF16, D, 4, 1, 2, 2>());
+        return f(AttnShape<BF16, D, 8, 1, 4, 2>());
     } else if constexpr (RB == 256) {
-        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2, FP4>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2, FP4>());
-        return f(AttnShape<BF16, D, 4, 1, 1, 2, FP4>());
+        if (wr == 1) return f(AttnShape<BF16, D, 1, 4, 1, 2>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2>());
+        return f(AttnShape<BF16, D, 4, 1, 1, 2>());
     } else if constexpr (RB == 512) {
-        if (wr == 1) return f(AttnShape<BF16, D, 1, 2, 1, 2, FP4>());
-        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2, FP4>());
-        return f(AttnShape<BF16, D, 4, 1, 1, 2, FP4>());
+        if (wr == 1) return f(AttnShape<BF16, D, 1, 2, 1, 2>());
+        if (wr == 2) return f(AttnShape<BF16, D, 2, 2, 1, 2>());
+        return f(AttnShape<BF16, D, 4, 1, 1, 2>());
     } else {
-        return f(AttnShape<BF16, D, 4, 1, 1, 2, FP4>());
+        return f(AttnShape<BF16, D, 4, 1, 1, 2>());
     }
 }
 
