@@ -11,11 +11,17 @@
 //
 // A workgroup takes a segment of the vocabulary and some rows of one sequence.  It
 // goes through the history once and counts in LDS the tokens that fall into its
-// segment (integer sums, so their order does not matter); a bitmap of the tokens that
-// anything happens to lets the rows pass by eight elements at a time, of which most
-// are copied (or, in place, not even read: a vector is loaded only if one of its
-// tokens is touched, and a vector of forbidden ones is only stored).  Nothing is kept
-// between calls, so a sequence's history may be edited at will.
+// segment (integer sums, so their order does not matter), and lists those that anything
+// happens to.  Two passes over the rows follow: all of their vectors are copied, with -inf
+// for the forbidden (in place only vectors with forbidden tokens are touched, and one
+// that has no others is not read); then the listed tokens are adjusted one by one, a
+// thread to a token for all rows.  (With both in one pass nearly every wave went through
+// the arithmetic for all eight elements of its vectors, for a token here and there: 512
+// rows in place 136 us.)  Nothing is kept between calls, so a history may be edited at will.
+//
+// Every load waits for most of a microsecond, so they go out several at a time: four
+// vectors of the history, the masks of all rows into LDS at once, four vectors or elements of
+// rows.
 #pragma once
 
 #include "common.hpp"
@@ -44,9 +50,12 @@ struct AdjustArgs {
     int B, R, V, L, M;
     int seg, nseg;              // tokens of a segment (a multiple of 32), segments
     int rows, row_groups;       // rows of a workgroup
+    int max_words;              // mask words of a segment, all rows of the workgroup; 0: no masks
+    int table;                  // biases have a word for each token of the segment; 0: a list of M
 };
 
-constexpr uint32_t kTokenSeen = 1u << 31, kTokenDrafted = 1u << 30, kTokenCount = kTokenDrafted - 1;
+constexpr uint32_t kTokenSeen = 1u << 31, kTokenDrafted = 1u << 30, kTokenBiased = 1u << 29, kTokenCount = kTokenBiased - 1;
+constexpr int kBiasList = 512;      // biases that are listed: each is looked for in the list of its segment
 constexpr int kAdjustThreads = 256;
 
 // `count` bits (up to 8) from bit p of the words on; words behind `last` are not read.
@@ -62,21 +71,37 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
     using Elem = std::conditional_t<BF16, uint16_t, uint32_t>;
     constexpr int E = BF16 ? 8 : 4;             // elements of 16 bytes
     constexpr uint32_t ALL = (1u << E) - 1;
+    constexpr int U = 4;                        // vectors of a thread at a time
     constexpr Elem kLow = BF16 ? 0xFF80u : 0xFF800000u;     // -inf
     extern __shared__ __attribute__((aligned(16))) uint32_t adjust_lds[];
+    __shared__ int listed, biased;
     uint32_t* const count = adjust_lds;                     // [seg]
     uint32_t* const touched = count + a.seg;                // [seg / 32]
-    uint32_t* const from = touched + a.seg / 32;            // [seg] bias entry + 1 (M > 0)
+    uint16_t* const list = reinterpret_cast<uint16_t*>(touched + a.seg / 32);       // [seg] touched tokens
+    uint32_t* const allowed = touched + a.seg / 32 + a.seg / 2;     // [rows, seg / 32] (with masks)
+    // biases: of each token its entry + 1, or (a few) a list of token and entry
+    uint32_t* const from = allowed + a.max_words;
     const int tid = threadIdx.x;
     const int s = blockIdx.x % a.nseg, rg = blockIdx.x / a.nseg % a.row_groups, b = blockIdx.x / a.nseg / a.row_groups;
     const int v0 = s * a.seg, len = min(a.seg, a.V - v0);
     const int t0 = rg * a.rows, t1 = min(t0 + a.rows, a.R);
 
     const bool lists = a.history || a.path || a.M > 0;
+    const int seg_words = a.seg >> 5, words = (len + 31) >> 5;      // mask words of the segment
     if (lists) {
-        for (int i = tid; i < a.seg + a.seg / 32 + (a.M > 0 ? a.seg : 0); i += kAdjustThreads) adjust_lds[i] = 0;
-        __syncthreads();
+        if (tid == 0) listed = biased = 0;
+        for (int i = tid; i < a.seg + seg_words; i += kAdjustThreads) adjust_lds[i] = 0;
+        if (a.table)
+            for (int i = tid; i < a.seg; i += kAdjustThreads) from[i] = 0;
     }
+    if (a.mask) {
+        const uint32_t* row = a.mask + b * a.mask_seq_stride + (v0 >> 5);
+        for (int i = tid; i < (t1 - t0) * seg_words; i += kAdjustThreads) {
+            const int t = (int)((unsigned)i / (unsigned)seg_words), w = i - t * seg_words;
+            if (w < words) allowed[i] = row[(t0 + t) * a.mask_row_stride + w];
+        }
+    }
+    __syncthreads();
     const auto touch = [&](uint32_t v) { atomicOr(&touched[v >> 5], 1u << (v & 31)); };
     if (a.history) {
         const int n = min(max(a.history_len[b], 0), a.L), prompt = a.prompt_len ? a.prompt_len[b] : 0;
@@ -91,10 +116,16 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
         const int head = min((int)((16 - ((uintptr_t)text & 15)) & 15) / 4, n);     // up to the first 16 bytes in line
         if (tid < head) take(tid, text[tid]);
         const int vectors = (n - head) / 4;
-        for (int i = tid; i < vectors; i += kAdjustThreads) {
-            const u32x4_t ids = *reinterpret_cast<const u32x4_t*>(text + head + 4 * i);
+        for (int i = tid; i < vectors; i += 4 * kAdjustThreads) {
+            u32x4_t ids[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) take(head + 4 * i + k, (int)ids[k]);
+            for (int j = 0; j < 4; ++j)
+                ids[j] = *reinterpret_cast<const u32x4_t*>(text + head + 4 * min(i + j * kAdjustThreads, vectors - 1));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + j * kAdjustThreads < vectors)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) take(head + 4 * (i + j * kAdjustThreads) + k, (int)ids[j][k]);
         }
         for (int i = head + 4 * vectors + tid; i < n; i += kAdjustThreads) take(i, text[i]);
     }
@@ -110,86 +141,177 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
         const int id = a.bias_token[(int64_t)b * a.M + i];
         const uint32_t v = (uint32_t)id - (uint32_t)v0;
         if (id < 0 || v >= (uint32_t)len) continue;
-        atomicMax(&from[v], (uint32_t)i + 1);       // of a token given twice, the last
+        if (a.table) atomicMax(&from[v], (uint32_t)i + 1);      // of a token given twice, the last
+        else from[atomicAdd(&biased, 1)] = v << 16 | (uint32_t)(i + 1);
+        atomicOr(&count[v], kTokenBiased);
         touch(v);
     }
-    if (lists) __syncthreads();
+    if (lists) {
+        __syncthreads();
+        for (int i = tid; i < seg_words; i += kAdjustThreads) {
+            uint32_t bits = touched[i];
+            int to = bits ? atomicAdd(&listed, __popc(bits)) : 0;
+            for (; bits; bits &= bits - 1) list[to++] = (uint16_t)(32 * i + __builtin_ctz(bits));
+        }
+    }
+    __syncthreads();
+
+    // all vectors of the rows
+    const bool in_line = (((uintptr_t)a.out | a.out_seq_stride * sizeof(Elem) | a.out_row_stride * sizeof(Elem)) & 15) == 0 &&
+                         (PLACE || (((uintptr_t)a.logits | a.seq_stride * sizeof(Elem) | a.row_stride * sizeof(Elem)) & 15) == 0);
+    if ((!PLACE || a.mask) && in_line) {
+        // rows begin in line: a vector's mask is a byte of the words, or half of one
+        const auto forbidden = [&](int t, int x) {
+            if (!a.mask) return 0u;
+            const uint8_t* bytes = reinterpret_cast<const uint8_t*>(allowed + (t - t0) * seg_words);
+            return E == 8 ? ~bytes[x] & 0xFFu : ~(bytes[x >> 1] >> (4 * (x & 1))) & 0xFu;
+        };
+        const Elem* in = reinterpret_cast<const Elem*>(a.logits) + b * a.seq_stride + v0;
+        Elem* const out = reinterpret_cast<Elem*>(a.out) + b * a.out_seq_stride + v0;
+        const int whole = len / E;
+        constexpr int RU = 2, XU = 2;                       // rows and vectors of a thread at a time
+        for (int t = t0; t < t1; t += RU)
+            for (int x0 = tid; x0 < whole; x0 += XU * kAdjustThreads) {
+                u32x4_t data[RU][XU];
+                uint32_t gone[RU][XU];
+#pragma unroll
+                for (int j = 0; j < RU * XU; ++j) {
+                    const int r = min(t + j / XU, t1 - 1), x = min(x0 + j % XU * kAdjustThreads, whole - 1);
+                    gone[j / XU][j % XU] = forbidden(r, x);
+                    if (!PLACE || (gone[j / XU][j % XU] && gone[j / XU][j % XU] != ALL))
+                        data[j / XU][j % XU] = *reinterpret_cast<const u32x4_t*>(in + r * a.row_stride + x * E);
+                }
+#pragma unroll
+                for (int j = 0; j < RU * XU; ++j) {
+                    const int r = t + j / XU, x = x0 + j % XU * kAdjustThreads;
+                    const uint32_t bad = gone[j / XU][j % XU];
+                    if (r >= t1 || x >= whole || (PLACE && !bad)) continue;
+                    u32x4_t y = data[j / XU][j % XU];
+                    if (bad) {
+                        __attribute__((aligned(16))) Elem e[E];
+                        *reinterpret_cast<u32x4_t*>(e) = y;
+#pragma unroll
+                        for (int k = 0; k < E; ++k) e[k] = bad >> k & 1 ? kLow : e[k];
+                        y = *reinterpret_cast<const u32x4_t*>(e);
+                    }
+                    *reinterpret_cast<u32x4_t*>(out + r * a.out_row_stride + x * E) = y;
+                }
+            }
+        // the elements behind the last whole vector
+        const int rest = len - whole * E;
+        for (int i = tid; i < (t1 - t0) * rest; i += kAdjustThreads) {
+            const int t = t0 + i / rest, k = i % rest;
+            const bool bad = forbidden(t, whole) >> k & 1;
+            if (!PLACE || bad)
+                out[t * a.out_row_stride + whole * E + k] = bad ? kLow : in[t * a.row_stride + whole * E + k];
+        }
+    } else if (!PLACE || a.mask) {
+        const int slots = (a.seg + E - 1) / E + 1;          // vectors of a row that meet the segment
+        const int items = (t1 - t0) * slots;
+        int t = t0, x = tid;                                // row and vector of this thread's next item
+        for (int i0 = 0; i0 < items; i0 += U * kAdjustThreads) {
+            // which elements of U vectors are theirs to write, and to forbid
+            const Elem* src[U];
+            Elem* to[U];
+            uint32_t own[U], gone[U];
+            u32x4_t data[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                while (x >= slots) {
+                    x -= slots;
+                    ++t;
+                }
+                own[j] = gone[j] = 0;
+                if (t < t1) {
+                    // vectors begin where the row's store address is in line
+                    Elem* const out = reinterpret_cast<Elem*>(a.out) + b * a.out_seq_stride + t * a.out_row_stride + v0;
+                    const int p = x * E - (int)(((uintptr_t)out & 15) / sizeof(Elem));      // its first token in the segment
+                    const int lo = max(p, 0), hi = min(p + E, len);
+                    if (lo < hi) {
+                        own[j] = (ALL >> (E - (hi - lo))) << (lo - p);
+                        gone[j] = a.mask ? ~(bits_at(allowed + (t - t0) * seg_words, lo, words - 1) << (lo - p)) & own[j] : 0u;
+                        if (PLACE && !gone[j]) own[j] = 0;
+                        src[j] = reinterpret_cast<const Elem*>(a.logits) + b * a.seq_stride + t * a.row_stride + v0 + p;
+                        to[j] = out + p;
+                        if (own[j] == ALL && gone[j] != ALL && (PLACE || ((uintptr_t)src[j] & 15) == 0))
+                            data[j] = *reinterpret_cast<const u32x4_t*>(src[j]);
+                    }
+                }
+                x += kAdjustThreads;
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (own[j] == ALL) {
+                    __attribute__((aligned(16))) Elem e[E];
+                    if (PLACE || gone[j] == ALL || ((uintptr_t)src[j] & 15) == 0) {
+                        *reinterpret_cast<u32x4_t*>(e) = data[j];
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < E; ++k) e[k] = src[j][k];
+                    }
+#pragma unroll
+                    for (int k = 0; k < E; ++k) e[k] = gone[j] >> k & 1 ? kLow : e[k];
+                    *reinterpret_cast<u32x4_t*>(to[j]) = *reinterpret_cast<const u32x4_t*>(e);
+                } else if (own[j]) {
+                    for (int k = 0; k < E; ++k)
+                        if (own[j] >> k & 1) to[j][k] = gone[j] >> k & 1 ? kLow : src[j][k];
+                }
+            }
+        }
+    }
+    if (!lists || listed == 0) return;
+    // their stores are done: elements of the same vectors follow
+    __syncthreads();
+
     const float rep = a.repetition ? a.repetition[b] : 1.f;
     const float freq = a.frequency ? a.frequency[b] : 0.f, pres = a.presence ? a.presence[b] : 0.f;
-
-    // token v0 + v of row t
-    const auto adjusted = [&](float x, int v, int t) {
-#pragma clang fp contract(off)
-        const uint32_t w = count[v];
-        uint32_t c = w & kTokenCount;
-        bool seen = w & kTokenSeen;
-        if (w & kTokenDrafted)
-            for (int j = 0; j < t; ++j)
-                if (path[j] == v0 + v) {
-                    ++c;
-                    seen = true;
-                }
-        if (seen) x = x > 0.f ? x / rep : x * rep;
-        if (c > 0) {
-            const float often = freq * (float)c;
-            x = x - often;
-            x = x - pres;
-        }
-        if (a.M > 0 && from[v]) x = x + a.bias[(int64_t)b * a.M + from[v] - 1];
-        return x;
-    };
     const auto number = [](Elem e) { return BF16 ? bf16_lo(e) : __uint_as_float(e); };
     const auto element = [](float x) -> Elem {
         if constexpr (BF16) return __builtin_bit_cast(uint16_t, (__bf16)x);
         else return __float_as_uint(x);
     };
-
-    const int last_word = (a.V - 1) >> 5;
-    const int slots = (a.seg + E - 1) / E + 1;              // vectors of a row that meet the segment
-    for (int i = tid; i < (t1 - t0) * slots; i += kAdjustThreads) {
-        const int t = t0 + i / slots;
-        const Elem* row = reinterpret_cast<const Elem*>(a.logits) + b * a.seq_stride + t * a.row_stride;
-        Elem* to = reinterpret_cast<Elem*>(a.out) + b * a.out_seq_stride + t * a.out_row_stride;
-        const uint32_t* allowed = a.mask ? a.mask + b * a.mask_seq_stride + t * a.mask_row_stride : nullptr;
-        // vectors begin where the row's store address is in line
-        const int off = (int)(((uintptr_t)(to + v0) & 15) / sizeof(Elem));
-        const int p = (i % slots) * E - off;                // first token of the vector in the segment
-        const int lo = max(p, 0), hi = min(p + E, len);
-        if (lo >= hi) continue;
-        const uint32_t own = (ALL >> (E - (hi - lo))) << (lo - p);     // its elements inside the segment
-        uint32_t change = lists ? (bits_at(touched, lo, (a.seg >> 5) - 1) << (lo - p)) & own : 0u;
-        const uint32_t gone = allowed ? ~(bits_at(allowed, v0 + lo, last_word) << (lo - p)) & own : 0u;
-        change &= ~gone;
-        if (PLACE && !(change | gone)) continue;
-        if (own == ALL) {
-            __attribute__((aligned(16))) Elem e[E];
-            if (gone == ALL) {
+    // U rows of a token at a time
+    const int quads = (t1 - t0 + U - 1) / U;
+    for (int i = tid; i < listed * quads; i += kAdjustThreads) {
+        const int quad = (int)((unsigned)i / (unsigned)listed), v = list[i - quad * listed], t = t0 + quad * U;
+        const Elem* src = reinterpret_cast<const Elem*>(a.logits) + b * a.seq_stride + v0 + v;
+        Elem* to = reinterpret_cast<Elem*>(a.out) + b * a.out_seq_stride + v0 + v;
+        Elem e[U];
 #pragma unroll
-                for (int k = 0; k < E; ++k) e[k] = kLow;
-            } else {
-                const Elem* src = row + v0 + p;
-                if (PLACE || ((uintptr_t)src & 15) == 0) {
-                    *reinterpret_cast<u32x4_t*>(e) = *reinterpret_cast<const u32x4_t*>(src);
-                } else {
+        for (int j = 0; j < U; ++j) e[j] = src[(int64_t)min(t + j, t1 - 1) * a.row_stride];
+        const uint32_t w = count[v];
+        const bool bias_it = w & kTokenBiased;
+        float bias = 0.f;
+        if (bias_it) {
+            uint32_t entry = a.table ? from[v] : 0u;
+            if (!a.table)
+                for (int k = 0; k < biased; ++k)
+                    if (from[k] >> 16 == (uint32_t)v) entry = max(entry, from[k] & 0xFFFFu);
+            bias = a.bias[(int64_t)b * a.M + entry - 1];
+        }
+        int c = (int)(w & kTokenCount), drafted = 0;        // generated before row t; drafts gone through
+        bool seen = w & kTokenSeen;
 #pragma unroll
-                    for (int k = 0; k < E; ++k) e[k] = src[k];
-                }
-                if (change | gone) {
-#pragma unroll
-                    for (int k = 0; k < E; ++k) {
-                        if (change >> k & 1) e[k] = element(adjusted(number(e[k]), p + k, t));
-                        if (gone >> k & 1) e[k] = kLow;
+        for (int j = 0; j < U; ++j) {
+#pragma clang fp contract(off)
+            if (t + j >= t1) break;
+            if (w & kTokenDrafted)
+                for (; drafted < t + j; ++drafted)
+                    if (path[drafted] == v0 + v) {
+                        ++c;
+                        seen = true;
                     }
-                }
+            if (a.mask && !(allowed[(t + j - t0) * seg_words + (v >> 5)] >> (v & 31) & 1)) continue;
+            if (!seen && !bias_it) continue;        // a draft of this row or one behind it
+            float x = number(e[j]);
+            if (seen) x = x > 0.f ? x / rep : x * rep;
+            if (c > 0) {
+                const float often = freq * (float)c;
+                x = x - often;
+                x = x - pres;
             }
-            *reinterpret_cast<u32x4_t*>(to + v0 + p) = *reinterpret_cast<const u32x4_t*>(e);
-        } else {
-            for (int k = lo - p; k < hi - p; ++k) {
-                Elem x = row[v0 + p + k];
-                if (change >> k & 1) x = element(adjusted(number(x), p + k, t));
-                if (gone >> k & 1) x = kLow;
-                to[v0 + p + k] = x;
-            }
+            if (bias_it) x = x + bias;
+            to[(int64_t)(t + j) * a.out_row_stride] = element(x);
         }
     }
 }

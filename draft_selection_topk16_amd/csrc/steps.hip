@@ -193,7 +193,7 @@ df2_status dflash2_adjust_logits(const df2_adjust* d, const void* logits, void* 
     // there are two workgroups a compute unit.
     const int64_t want = 2 * (int64_t)compute_units();
     a.seg = 4096;
-    a.rows = d->R;
+    a.rows = d->mask ? std::min(d->R, 16) : d->R;       // the masks of 16 rows are 8 KB of LDS
     const auto count = [&] {
         a.nseg = (int)(((int64_t)d->V + a.seg - 1) / a.seg);
         a.row_groups = (d->R + a.rows - 1) / a.rows;
@@ -203,7 +203,11 @@ df2_status dflash2_adjust_logits(const df2_adjust* d, const void* logits, void* 
     while (a.seg > 1024 && count() < want) a.seg /= 2;
     const int64_t groups = count();
     if (groups * kAdjustThreads > kMostThreads) return fail_with(DF2_EUNSUPPORTED, "B * R * V too large");
-    const size_t lds = ((size_t)a.seg + a.seg / 32 + (biases ? a.seg : 0)) * 4;
+    a.max_words = d->mask ? a.rows * (a.seg / 32) : 0;
+    // A list of biases is short LDS and a search for each biased token; with many a word for
+    // each token (512 rows in place with 16 biases: a table costs 22 us).
+    a.table = d->M > kBiasList;
+    const size_t lds = ((size_t)a.seg + a.seg / 32 + a.seg / 2 + a.max_words + (a.table ? a.seg : d->M)) * 4;
     const auto go = [&](auto bf16, auto in_place) {
         hipLaunchKernelGGL((k_adjust<decltype(bf16)::value, decltype(in_place)::value>), dim3((unsigned)groups),
                            dim3(kAdjustThreads), lds, stream, a);
