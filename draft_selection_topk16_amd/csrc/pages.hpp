@@ -8,12 +8,13 @@
 // sums of what the requests ask for, so the result does not depend on how the work
 // is divided, and there are no atomics.
 //
-// One workgroup does this for all requests: three passes over them (what goes
-// back; who is served; tables and starts), kPageThreads at a time, prefix sums by
-// lanes and then over the waves in LDS.  It is bound by latency: a pass is a few
-// loads and a scan one after the other.  What follows per row (slots and positions)
-// is work for the whole chip where there are many rows, in a second launch; with up
-// to kPageRows rows the same workgroup does it.
+// One workgroup does this for all requests: two passes over them (what goes back; who
+// is served, with tables and starts), K neighbouring requests a thread, prefix sums by
+// lanes and then over the waves in LDS.  It is bound by latency: a pass is a few loads and
+// scans one after the other, so with up to 4096 requests they are read once (3000 of them
+// with 93 thousand rows, a thousand at a time: 42 us).  What follows per row (slots and
+// positions) is work for the whole chip where there are many rows, in a second launch;
+// with up to kPageRows rows the same workgroup does it.
 #pragma once
 
 #include "attention.hpp"
@@ -81,11 +82,11 @@ __device__ __forceinline__ double pages_scan(double x, double* waves, double& al
 }
 
 // The request that has item i of a chunk's items, from the sums up to each request.
-template <int NT>
+template <int N>
 __device__ __forceinline__ int item_owner(const int* upto, int i) {
     int lo = 0;
 #pragma unroll
-    for (int step = NT / 2; step > 0; step /= 2)
+    for (int step = N / 2; step > 0; step /= 2)
         if (upto[lo + step - 1] <= i) lo += step;
     return lo;
 }
@@ -100,37 +101,68 @@ __device__ __forceinline__ void write_idle_row(const PagesArgs& a, int row) {
     if (a.pos) a.pos[row] = -1;
 }
 
-template <int NT>
+template <int NT, int K>
 __global__ __launch_bounds__(NT) void k_plan_pages(PagesArgs a) {
+    constexpr int CH = NT * K;              // requests of a chunk
     __shared__ double waves[NT / 64];
-    __shared__ int upto[NT], base[NT], first[NT];
+    __shared__ int upto[CH], base[CH], many[CH];
     const int tid = threadIdx.x;
-    const int chunks = (a.B + NT - 1) / NT;
-    PageRequest r = page_request(a, tid);
+    const int chunks = (a.B + CH - 1) / CH;
+    PageRequest r[K];
+    const auto read = [&](int c) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) r[k] = page_request(a, c * CH + tid * K + k);
+    };
+    read(0);
     int count = min(max(*a.free_count, 0), a.num_pages);
+    // sums up to each of this thread's requests, and of all
+    const auto scan = [&](const int (&x)[K], double (&sum)[K]) {
+        double mine = 0.0, all;
+#pragma unroll
+        for (int k = 0; k < K; ++k) mine += x[k];
+        double before = pages_scan<NT>(mine, waves, all) - mine;
+#pragma unroll
+        for (int k = 0; k < K; ++k) sum[k] = before += x[k];
+        return all;
+    };
+    // a chunk's items one by one: item i is number j of request q's n, which begin at `first`
+    const auto each_item = [&](const int (&n)[K], const double (&sum)[K], const int (&first)[K], int items, auto&& f) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            upto[tid * K + k] = (int)fmin(sum[k], 2147483647.0);
+            base[tid * K + k] = first[k];
+            many[tid * K + k] = n[k];
+        }
+        __syncthreads();
+        for (int i = tid; i < items; i += NT) {
+            const int q = item_owner<CH>(upto, i);
+            f(i, q, base[q] + (i - (upto[q] - many[q])));
+        }
+        __syncthreads();
+    };
 
     // what goes back
     for (int c = 0; c < chunks; ++c) {
-        if (c > 0) r = page_request(a, c * NT + tid);
-        const int gone = max(r.held - r.want, 0);
-        double all;
-        const double sum = pages_scan<NT>(gone, waves, all);
+        if (c > 0) read(c);
+        int gone[K], first[K];
+        double sum[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            gone[k] = max(r[k].held - r[k].want, 0);
+            first[k] = r[k].want;
+        }
+        const double all = scan(gone, sum);
         if (all == 0.0) continue;
         const int items = (int)fmin(all, 2147483647.0);
-        upto[tid] = (int)fmin(sum, 2147483647.0);
-        base[tid] = r.want;
-        first[tid] = gone;
-        __syncthreads();
-        for (int i = tid; i < items; i += NT) {
-            const int q = item_owner<NT>(upto, i);
-            int32_t* entry = a.table + (int64_t)(c * NT + q) * a.table_stride + base[q] + (i - (upto[q] - first[q]));
+        each_item(gone, sum, first, items, [&](int i, int q, int at) {
+            int32_t* entry = a.table + (int64_t)(c * CH + q) * a.table_stride + at;
             const int id = *entry;
             *entry = -1;
             if (i < a.num_pages - count) a.free_list[count + i] = id;
             else atomicOr(a.err, kFlagPage);        // more than there are: a page held twice
-        }
+        });
         count += min(items, a.num_pages - count);
-        __syncthreads();
     }
 
     // who is served; their pages, starts and rows
@@ -138,50 +170,53 @@ __global__ __launch_bounds__(NT) void k_plan_pages(PagesArgs a) {
     int taken = 0, start = 0;
     if (tid == 0) a.start[0] = 0;
     for (int c = 0; c < chunks; ++c) {
-        const int b = c * NT + tid;
-        if (chunks > 1) r = page_request(a, b);
-        int ask = max(r.want - r.held, 0), n = r.n;
-        double all_pages, all_rows;
-        const double pages = asked_pages + pages_scan<NT>(ask, waves, all_pages);
-        const double rows = asked_rows + pages_scan<NT>(n, waves, all_rows);
+        if (chunks > 1) read(c);
+        int ask[K], n[K], first[K];
+        double pages[K], rows[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            ask[k] = max(r[k].want - r[k].held, 0);
+            n[k] = r[k].n;
+        }
+        const double all_pages = scan(ask, pages), all_rows = scan(n, rows);
+        bool some = false;              // somebody is not served: the sums change
+        if (asked_pages + all_pages > count || asked_rows + all_rows > a.N) {
+            some = true;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (asked_pages + pages[k] > count || asked_rows + rows[k] > a.N) {
+                    if (n[k] > 0 || ask[k] > 0) atomicOr(a.err, kFlagServed);
+                    n[k] = ask[k] = 0;
+                }
+        }
         asked_pages += all_pages;
         asked_rows += all_rows;
-        if (pages > count || rows > a.N) {
-            if (n > 0 || ask > 0) atomicOr(a.err, kFlagServed);
-            n = ask = 0;
+        double all_taken = all_pages, all_n = all_rows;
+        if (some) {
+            all_taken = scan(ask, pages);
+            all_n = scan(n, rows);
         }
-        if (r.wide) atomicOr(a.err, kFlagLength);
-        double all_taken, all_n;
-        const int page_sum = (int)pages_scan<NT>(ask, waves, all_taken);
-        const int row_sum = (int)pages_scan<NT>(n, waves, all_n);
-        if (b < a.B) {
-            a.held[b] = min(r.held, r.want) + ask;
-            a.ctx_out[b] = r.ctx;
-            a.start[b + 1] = start + row_sum;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int b = c * CH + tid * K + k;
+            if (r[k].wide) atomicOr(a.err, kFlagLength);
+            first[k] = r[k].held;
+            if (b < a.B) {
+                a.held[b] = min(r[k].held, r[k].want) + ask[k];
+                a.ctx_out[b] = r[k].ctx;
+                a.start[b + 1] = start + (int)rows[k];
+            }
         }
         if (all_taken > 0.0) {
-            upto[tid] = page_sum;
-            base[tid] = r.held;
-            first[tid] = ask;
-            __syncthreads();
-            for (int i = tid; i < (int)all_taken; i += NT) {
-                const int q = item_owner<NT>(upto, i);
-                a.table[(int64_t)(c * NT + q) * a.table_stride + base[q] + (i - (upto[q] - first[q]))] =
-                    a.free_list[count - 1 - taken - i];
-            }
+            each_item(ask, pages, first, (int)all_taken, [&](int i, int q, int at) {
+                a.table[(int64_t)(c * CH + q) * a.table_stride + at] = a.free_list[count - 1 - taken - i];
+            });
             taken += (int)all_taken;
-            __syncthreads();
         }
         if (a.rows_here) {
-            upto[tid] = row_sum;
-            base[tid] = r.ctx;
-            first[tid] = n;
-            __syncthreads();
-            for (int i = tid; i < (int)all_n; i += NT) {
-                const int q = item_owner<NT>(upto, i);
-                write_row(a, start + i, c * NT + q, base[q] + (i - (upto[q] - first[q])));
-            }
-            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < K; ++k) first[k] = r[k].ctx;
+            each_item(n, rows, first, (int)all_n, [&](int i, int q, int at) { write_row(a, start + i, c * CH + q, at); });
         }
         start += (int)all_n;
     }

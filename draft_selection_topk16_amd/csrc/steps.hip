@@ -111,9 +111,11 @@ df2_status dflash2_plan_pages(const df2_page_pool* pool, const int32_t* ctx_len,
     const bool rows = slots || positions;
     a.rows_here = rows && pool->N <= kPageRows;
     if (pool->B <= 256 && (!a.rows_here || pool->N <= 1024))
-        hipLaunchKernelGGL(k_plan_pages<256>, dim3(1), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_plan_pages<256, 1>), dim3(1), dim3(256), 0, stream, a);
+    else if (pool->B <= kPageThreads)
+        hipLaunchKernelGGL((k_plan_pages<kPageThreads, 1>), dim3(1), dim3(kPageThreads), 0, stream, a);
     else
-        hipLaunchKernelGGL(k_plan_pages<kPageThreads>, dim3(1), dim3(kPageThreads), 0, stream, a);
+        hipLaunchKernelGGL((k_plan_pages<kPageThreads, 4>), dim3(1), dim3(kPageThreads), 0, stream, a);
     if ((st = launched("dflash2_plan_pages launch")) != DF2_OK || !rows || a.rows_here) return st;
     // some 16 waves a compute unit over the requests' rows
     const int64_t waves = (int64_t)compute_units() * 16;

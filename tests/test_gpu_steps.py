@@ -69,6 +69,8 @@ PAGES = [
     ("past_a_workgroup", 257, 16, 40, 600, 9, 256, 2000, 0.2), ("rows_apart", 40, 16, 300, 2000, 700, 2500, 30000, 0.1),
     ("chunks", 1024, 16, 20, 300, 4, 1100, 4096, 0.1), ("past_a_chunk", 1025, 16, 20, 300, 4, 300, 4096, 0.1),
     ("three_chunks", 2500, 16, 20, 300, 8, 1500, 12000, 0.3), ("three_chunks_apart", 2500, 64, 6, 300, 40, 2500, 60000, 0.1),
+    ("four_a_thread", 4096, 16, 20, 300, 4, 4100, 12000, 0.2), ("past_four_a_thread", 4097, 16, 20, 300, 4, 1000, 4096, 0.2),
+    ("many_chunks", 9000, 32, 8, 200, 9, 4000, 40000, 0.3),
 ]
 
 
