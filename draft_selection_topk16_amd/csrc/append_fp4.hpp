@@ -81,8 +81,12 @@ __global__ __launch_bounds__(256) void k_append_fp4(AppendArgs a) {
             if (placed) page = kv.table[(int64_t)q.b * kv.table_stride + (pos >> kv.page_shift)];
         }
         for (int i = lane; i < half; i += 64) {
+            // whole turns drop out; 1 / (2 pi) in two parts, so that what is left of the angle
+            // is as exact as the angle
+            constexpr double kTurn = 0.15915494309189535, kTurnLow = -9.839338337591243e-18;
+            const double angle = (double)pos * a.freq[i], whole = rint(angle * kTurn);
             double s, c;
-            sincos((double)pos * a.freq[i], &s, &c);
+            sincospi(2.0 * (__builtin_fma(angle, kTurn, -whole) + angle * kTurnLow), &s, &c);
             turn[j][i] = c;
             turn[j][half + i] = s;
         }
