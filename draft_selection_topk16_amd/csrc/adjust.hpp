@@ -54,6 +54,8 @@ struct AdjustArgs {
     int table;                  // biases have a word for each token of the segment; 0: a list of M
 };
 
+// What LDS holds of a token: whether the prompt has it, whether a draft is it, whether it
+// has a bias, how often it was generated.
 constexpr uint32_t kTokenSeen = 1u << 31, kTokenDrafted = 1u << 30, kTokenBiased = 1u << 29, kTokenCount = kTokenBiased - 1;
 constexpr int kBiasList = 512;      // biases that are listed: each is looked for in the list of its segment
 constexpr int kAdjustThreads = 256;
@@ -102,7 +104,10 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
         }
     }
     __syncthreads();
-    const auto touch = [&](uint32_t v) { atomicOr(&touched[v >> 5], 1u << (v & 31)); };
+    // read first: texts repeat themselves, and a wave's atomics on one word go one by one
+    const auto touch = [&](uint32_t v) {
+        if (!(touched[v >> 5] >> (v & 31) & 1)) atomicOr(&touched[v >> 5], 1u << (v & 31));
+    };
     if (a.history) {
         const int n = min(max(a.history_len[b], 0), a.L), prompt = a.prompt_len ? a.prompt_len[b] : 0;
         const int32_t* text = a.history + (int64_t)b * a.history_stride;
@@ -110,7 +115,7 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
             const uint32_t v = (uint32_t)id - (uint32_t)v0;
             if (id < 0 || v >= (uint32_t)len) return;
             if (i >= prompt) atomicAdd(&count[v], 1u);
-            atomicOr(&count[v], kTokenSeen);
+            else if (!(count[v] & kTokenSeen)) atomicOr(&count[v], kTokenSeen);
             touch(v);
         };
         const int head = min((int)((16 - ((uintptr_t)text & 15)) & 15) / 4, n);     // up to the first 16 bytes in line
@@ -290,7 +295,7 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
             bias = a.bias[(int64_t)b * a.M + entry - 1];
         }
         int c = (int)(w & kTokenCount), drafted = 0;        // generated before row t; drafts gone through
-        bool seen = w & kTokenSeen;
+        bool seen = (w & kTokenSeen) || c > 0;
 #pragma unroll
         for (int j = 0; j < U; ++j) {
 #pragma clang fp contract(off)
