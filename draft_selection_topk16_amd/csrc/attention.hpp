@@ -249,7 +249,7 @@ __device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
         // 32 of a thousand 46 and 44; 128 of them 131 and 117; 64 of 500, 32 new, 66 and
         // 42; one chunk of 2048 tokens without context 95 and 58.)
         const int average = (int)((unsigned)all / (unsigned)max(a.wgs, 1));
-        if (blocks * a.kv.Hkv <= (int)gridDim.x && max(most, average + most / 2) <= average + (Shape::BM == 32 ? 5 : 16)) {
+        if (blocks * a.kv.Hkv <= (int)gridDim.x && max(most, average + most / 2) <= average + (Shape::BM <= 32 ? 5 : 16)) {
             c.whole = true;
             q.tiles = q.blocks;
             c.head_tiles = blocks;
@@ -261,8 +261,10 @@ __device__ __forceinline__ Cut cut_work(const AttnArgs& a, LaneSeq& q) {
     // stretches leave more parts than they save (event times with 512 workgroups and
     // the join, then with 256: 4 contexts of 25 thousand tokens, 8 new, 16 / 2 heads, 6
     // tiles each, 34 + 14.5 and 34 + 9.8 us; 2 of 4000, 32 new, 32 / 8 heads, 2 tiles,
-    // 29 + 16.6 and 25 + 12.8; but 16 such, 16 tiles, 68 + 12.1 and 76 + 12.0).
-    if (!c.whole && c.wgs > a.cus && all < 8 * c.wgs) c.wgs = a.cus;
+    // 29 + 16.6 and 25 + 12.8; but 16 such, 16 tiles, 68 + 12.1 and 76 + 12.0).  Parts of
+    // 16 rows are small: four tiles there (4-bit cache, 8 heads, one token after 64 thousand,
+    // 8 tiles each, 31 us with 256 and 28 with 512; 4 after 4000, 2 tiles, 14.4 and 15.7).
+    if (!c.whole && c.wgs > a.cus && all < (Shape::BM == 16 ? 4 : 8) * c.wgs) c.wgs = a.cus;
     c.each = c.wgs > 0 ? (int)((unsigned)all / (unsigned)c.wgs) : 0;
     c.more = all - c.each * c.wgs;
     return c;
