@@ -179,9 +179,9 @@ df2_status dflash2_adjust_logits(const df2_adjust* d, const void* logits, void* 
     a.bias = d->bias;
     a.mask = reinterpret_cast<const uint32_t*>(d->mask);
     a.seq_stride = seq;
-    a.row_stride = row;
+    a.row_stride = d->R > 1 ? row : 0;
     a.out_seq_stride = out_seq;
-    a.out_row_stride = out_row;
+    a.out_row_stride = d->R > 1 ? out_row : 0;
     a.history_stride = d->history_stride;
     a.mask_seq_stride = d->B > 1 ? d->mask_seq_stride : 0;
     a.mask_row_stride = d->R > 1 ? d->mask_row_stride : 0;
