@@ -24,6 +24,16 @@
 
 namespace df2 {
 
+// Where element e of a row of the form lies in LDS: lanes read LANE neighbouring elements
+// each, in 16-byte chunks, and the chunks are permuted so that those of one go lie in
+// different banks.
+template <typename F, int LANE>
+__device__ __forceinline__ int form_place(int e) {
+    constexpr int PER = 16 / (int)sizeof(F), N = LANE / PER;       // elements of a chunk, chunks of a lane
+    const int chunk = e / PER;
+    return (chunk ^ ((chunk >> 4) & (N - 1))) * PER + e % PER;
+}
+
 template <bool BF16, int D, int T>
 __global__ __launch_bounds__(256) void k_append_fp4(AppendArgs a) {
     constexpr int E = BF16 ? 8 : 4, SZ = BF16 ? 2 : 4;
@@ -128,11 +138,11 @@ __global__ __launch_bounds__(256) void k_append_fp4(AppendArgs a) {
             const double c = in ? turn[j][f] : 1.0, s = in ? turn[j][half + f] : 0.0;
             const double fa = mine * c, fb = first ? -(theirs * s) : theirs * s;
             if (is_q) {
-                form_q[j][0][e] = (float)fa;
-                form_q[j][1][e] = (float)fb;
+                form_q[j][0][form_place<float, E>(e)] = (float)fa;
+                form_q[j][1][form_place<float, E>(e)] = (float)fb;
             } else {
-                form_k[j][0][e] = fa;
-                form_k[j][1][e] = fb;
+                form_k[j][0][form_place<double, E>(e)] = fa;
+                form_k[j][1][form_place<double, E>(e)] = fb;
             }
         }
     }
@@ -175,10 +185,16 @@ __global__ __launch_bounds__(256) void k_append_fp4(AppendArgs a) {
                     r = 1.f / sqrtf(lanes_sum<L>(ss) * (1.f / D) + a.eps);
                 }
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    y.x[e] *= form_q[j][0][e0 + e];
-                    if (turned) y.x[e] = __builtin_fmaf(z.x[e], form_q[j][1][e0 + e], y.x[e]);
-                    y.x[e] *= r;
+                for (int e = 0; e < E; e += 4) {
+                    const int at = form_place<float, E>(e0 + e);
+                    const f32x4_t fa = *reinterpret_cast<const f32x4_t*>(&form_q[j][0][at]);
+                    const f32x4_t fb = *reinterpret_cast<const f32x4_t*>(&form_q[j][1][at]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y.x[e + i] *= fa[i];
+                        if (turned) y.x[e + i] = __builtin_fmaf(z.x[e + i], fb[i], y.x[e + i]);
+                        y.x[e + i] *= r;
+                    }
                 }
                 y.store(reinterpret_cast<char*>(a.out_q) + ((int64_t)tok * a.out_stride + (int64_t)h * D + e0) * SZ);
                 continue;
@@ -210,11 +226,18 @@ __global__ __launch_bounds__(256) void k_append_fp4(AppendArgs a) {
                     r = 1.0 / sqrt(lanes_sum<L>(ss) * (1.0 / D) + (double)a.eps);
                 }
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    x[e] = (double)y.x[e] * form_k[j][0][e0 + e];
-                    if (turned) x[e] = __builtin_fma((double)z.x[e], form_k[j][1][e0 + e], x[e]);
-                    x[e] *= r;
-                    most = larger(fabs(x[e]), most);
+                for (int e = 0; e < E; e += 2) {
+                    typedef double f64x2_t __attribute__((ext_vector_type(2)));
+                    const int at = form_place<double, E>(e0 + e);
+                    const f64x2_t fa = *reinterpret_cast<const f64x2_t*>(&form_k[j][0][at]);
+                    const f64x2_t fb = *reinterpret_cast<const f64x2_t*>(&form_k[j][1][at]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        x[e + i] = (double)y.x[e + i] * fa[i];
+                        if (turned) x[e + i] = __builtin_fma((double)z.x[e + i], fb[i], x[e + i]);
+                        x[e + i] *= r;
+                        most = larger(fabs(x[e + i]), most);
+                    }
                 }
                 most = lanes_reduce<LB>(most, larger);
                 top = (uint64_t)__double_as_longlong(most);
