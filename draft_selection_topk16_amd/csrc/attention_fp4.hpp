@@ -132,11 +132,12 @@ __global__ __launch_bounds__(256, (FewShape<BF16, D, R>::kResident)) void k_atte
     int32_t* const ids = reinterpret_cast<int32_t*>(lds + Shape::kLds);
     const int64_t head_bytes = Fp4Page<D>::bytes(kv.page_shift), scales_at = Fp4Page<D>::scales(kv.page_shift);
     const int page_mask = (1 << kv.page_shift) - 1;
-    // Values in LDS: a key's row of 2 D bytes, its 16-byte chunks permuted so that what is
-    // read in one go, 16 rows of two chunks or 8 of four, lies in all banks alike, and so does
-    // what is written (lane_key: 16 lanes of four rows that are four apart).
+    // Values in LDS: a key's row of 2 D bytes, its 16-byte chunks permuted so that what 32
+    // lanes read in one go, 8 rows of two chunks or 4 of four, lies in all banks, and so does
+    // what 16 lanes write (lane_key: four rows that are four apart).
     const auto swz = [](int row) {
-        return D == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
+        const int far = (row >> 3 & 1) | (row >> 1 & 2);        // bits 2 and 3 of the row, swapped
+        return D == 64 ? (row >> 1 & 1) << 2 | far : (row & 3) << 2 | far;
     };
     // the key, of the 64, and the block of load i of the values
     constexpr int KL = 64 / NB;             // keys of a load
