@@ -17,12 +17,13 @@
 // that has no others is not read); then the listed tokens are adjusted one by one, a
 // thread to a token for all rows.  (With both in one pass nearly every wave went through
 // the arithmetic for all eight elements of its vectors, for a token here and there: 512
-// rows of 151936 in place, half of them masked, 136 us, now 73, of which the single elements'
+// rows of 151936 in place, half of them masked, 136 us, now 72, of which the single elements'
 // lines are some 40.  8 rows into another tensor: 6.6 us, latency.)  Nothing is kept between calls, so a history may be edited at will.
 //
 // Every load waits for most of a microsecond, so they go out several at a time: four
 // vectors of the history, the masks of all rows into LDS at once, four vectors or elements of
-// rows.
+// rows.  A token of the history costs one atomic that nothing waits for (with a bitmap read
+// and set beside it, 2 sequences of 16 thousand tokens over 1200 words 17 us, now 10).
 #pragma once
 
 #include "common.hpp"
@@ -79,9 +80,8 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint32_t adjust_lds[];
     __shared__ int listed, biased;
     uint32_t* const count = adjust_lds;                     // [seg]
-    uint32_t* const touched = count + a.seg;                // [seg / 32]
-    uint16_t* const list = reinterpret_cast<uint16_t*>(touched + a.seg / 32);       // [seg] touched tokens
-    uint32_t* const allowed = touched + a.seg / 32 + a.seg / 2;     // [rows, seg / 32] (with masks)
+    uint16_t* const list = reinterpret_cast<uint16_t*>(count + a.seg);      // [seg] touched tokens
+    uint32_t* const allowed = count + a.seg + a.seg / 2;    // [rows, seg / 32] (with masks)
     // biases: of each token its entry + 1, or (a few) a list of token and entry
     uint32_t* const from = allowed + a.max_words;
     const int tid = threadIdx.x;
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
     const int seg_words = a.seg >> 5, words = (len + 31) >> 5;      // mask words of the segment
     if (lists) {
         if (tid == 0) listed = biased = 0;
-        for (int i = tid; i < a.seg + seg_words; i += kAdjustThreads) adjust_lds[i] = 0;
+        for (int i = tid; i < a.seg; i += kAdjustThreads) count[i] = 0;
         if (a.table)
             for (int i = tid; i < a.seg; i += kAdjustThreads) from[i] = 0;
     }
@@ -105,19 +105,15 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
         }
     }
     __syncthreads();
-    // read first: texts repeat themselves, and a wave's atomics on one word go one by one
-    const auto touch = [&](uint32_t v) {
-        if (!(touched[v >> 5] >> (v & 31) & 1)) atomicOr(&touched[v >> 5], 1u << (v & 31));
-    };
     if (a.history) {
         const int n = min(max(a.history_len[b], 0), a.L), prompt = a.prompt_len ? a.prompt_len[b] : 0;
         const int32_t* text = a.history + (int64_t)b * a.history_stride;
         const auto take = [&](int i, int id) {
             const uint32_t v = (uint32_t)id - (uint32_t)v0;
             if (id < 0 || v >= (uint32_t)len) return;
+            // nothing is read back, so nothing waits
             if (i >= prompt) atomicAdd(&count[v], 1u);
-            else if (!(count[v] & kTokenSeen)) atomicOr(&count[v], kTokenSeen);
-            touch(v);
+            else atomicOr(&count[v], kTokenSeen);
         };
         const int head = min((int)((16 - ((uintptr_t)text & 15)) & 15) / 4, n);     // up to the first 16 bytes in line
         if (tid < head) take(tid, text[tid]);
@@ -141,7 +137,6 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
             const uint32_t v = (uint32_t)path[i] - (uint32_t)v0;
             if (path[i] < 0 || v >= (uint32_t)len) continue;
             atomicOr(&count[v], kTokenDrafted);
-            touch(v);
         }
     for (int i = tid; i < a.M; i += kAdjustThreads) {
         const int id = a.bias_token[(int64_t)b * a.M + i];
@@ -150,15 +145,22 @@ __global__ __launch_bounds__(kAdjustThreads) void k_adjust(AdjustArgs a) {
         if (a.table) atomicMax(&from[v], (uint32_t)i + 1);      // of a token given twice, the last
         else from[atomicAdd(&biased, 1)] = v << 16 | (uint32_t)(i + 1);
         atomicOr(&count[v], kTokenBiased);
-        touch(v);
     }
     if (lists) {
         __syncthreads();
-        for (int i = tid; i < seg_words; i += kAdjustThreads) {
-            uint32_t bits = touched[i];
-            int to = bits ? atomicAdd(&listed, __popc(bits)) : 0;
-            for (; bits; bits &= bits - 1) list[to++] = (uint16_t)(32 * i + __builtin_ctz(bits));
+        // a thread's neighbouring words, four at a time; one place in the list a wave
+        const int each = a.seg / kAdjustThreads;
+        uint32_t bits = 0;
+        for (int i = 0; i < each; i += 4) {
+            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(count + tid * each + i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bits |= (w[k] != 0 ? 1u : 0u) << (i + k);
         }
+        const int n = __popc(bits), upto = lanes_scan(n);
+        int first = 0;
+        if (lane_id() == 63) first = atomicAdd(&listed, upto);
+        int to = __builtin_amdgcn_readlane(first, 63) + upto - n;
+        for (; bits; bits &= bits - 1) list[to++] = (uint16_t)(tid * each + __builtin_ctz(bits));
     }
     __syncthreads();
 

@@ -13,10 +13,10 @@
 // D * size / 16 lanes hold a head, 16 bytes each: a block is 4 of them (bf16) or 8, so its
 // largest magnitude is two or three register moves away.
 //
-// Measured: 15 thousand tokens of 32 + 2 * 8 heads of 128 in bf16 107 us for 331 MB (the
+// Measured: 15 thousand tokens of 32 + 2 * 8 heads of 128 in bf16 97 us for 331 MB (the
 // append of bf16 pages 85 for 378), bound by its vector instructions, a third of them the
-// keys' fp64 (with the library's sine of any angle in place of a fraction of a turn 122); a
-// batch's 539 tokens in fp32 5 us.
+// keys' fp64.  (With the form's chunks as they lie, in four banks' way, 107; with the library's
+// sine of any angle in place of a fraction of a turn 122.)  A batch's 539 tokens in fp32 5 us.
 #pragma once
 
 #include "fp4.hpp"

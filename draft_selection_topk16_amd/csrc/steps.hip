@@ -202,14 +202,14 @@ df2_status dflash2_adjust_logits(const df2_adjust* d, const void* logits, void* 
         return (int64_t)a.nseg * a.row_groups * d->B;
     };
     while (a.rows > 1 && count() < want) a.rows = (a.rows + 1) / 2;
-    while (a.seg > 1024 && count() < want) a.seg /= 2;
+    while (a.seg > 1024 && count() < want) a.seg /= 2;     // four words a thread at least
     const int64_t groups = count();
     if (groups * kAdjustThreads > kMostThreads) return fail_with(DF2_EUNSUPPORTED, "B * R * V too large");
     a.max_words = d->mask ? a.rows * (a.seg / 32) : 0;
     // A list of biases is short LDS and a search for each biased token; with many a word for
     // each token (512 rows in place with 16 biases: a table costs 22 us).
     a.table = d->M > kBiasList;
-    const size_t lds = ((size_t)a.seg + a.seg / 32 + a.seg / 2 + a.max_words + (a.table ? a.seg : d->M)) * 4;
+    const size_t lds = ((size_t)a.seg + a.seg / 2 + a.max_words + (a.table ? a.seg : d->M)) * 4;
     const auto go = [&](auto bf16, auto in_place) {
         hipLaunchKernelGGL((k_adjust<decltype(bf16)::value, decltype(in_place)::value>), dim3((unsigned)groups),
                            dim3(kAdjustThreads), lds, stream, a);
