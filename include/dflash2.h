@@ -538,11 +538,12 @@ df2_status dflash2_kv_append_fp4(const df2_paged_kv* kv, const void* q, int64_t 
 
 /*
  * dflash2_paged_attention over a 4-bit cache: same arguments, and the softmax over the
- * values that the codes stand for.  bf16 calls multiply them as bf16, which they are exactly;
- * scores, statistics, sums and probabilities as there.  Scales of positions that a
- * token of the batch sees must be 7 to 247, as the append makes them for finite numbers;
- * a sequence's values, added up with weights of up to 2^8 before they are divided by the
- * sum, must stay finite in fp32 (any scale up to 2^90 will do).
+ * values that the codes stand for.  bf16 calls multiply them as bf16, which they are
+ * exactly, and give probabilities 16 bits in blocks of up to 32 rows (above, rounded to
+ * bf16); scores, statistics and sums as there.  Scales of positions that a token of the
+ * batch sees must be 7 to 247, as the append makes them for finite numbers; a sequence's
+ * values, added up with weights of up to 2^8 before they are divided by the sum, must stay
+ * finite in fp32 (any scale up to 2^90 will do).
  */
 size_t dflash2_paged_attention_fp4_workspace(const df2_paged_kv* kv, int32_t max_len);
 df2_status dflash2_paged_attention_fp4(const df2_paged_kv* kv, const void* q, int64_t q_stride,
@@ -633,7 +634,7 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
  *   B           requests (0: nothing is enqueued), at most 2^20
  *   N           token rows of the step, at most 2^30
  *   page_size, num_pages, table_width as in df2_paged_kv
- * These four arrays are updated in place.
+ * These four arrays are updated in place; calls that share them must be ordered.
  */
 typedef struct df2_page_pool {
     int32_t* block_table;
