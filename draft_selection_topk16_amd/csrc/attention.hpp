@@ -437,6 +437,11 @@ __device__ __forceinline__ float scaled_minus(float x, float c, float m) {
     return y - m;
 }
 
+// The maximum that a row's part hands to the merges, which take -inf for a part that sees
+// nothing.  Scores of NaN raise no maximum: their row's sum is NaN, and shall stay so
+// however its keys are divided.
+__device__ __forceinline__ float stated_max(float m, float l) { return l != l && m == -INFINITY ? 0.f : m; }
+
 template <bool BF16, int D, bool FP4 = false>
 struct AttnTile {
     static constexpr int kEsz = BF16 ? 2 : 4;
@@ -1008,6 +1013,7 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
         pair_of<32>(l, lower, upper);
         l = lower + upper;
     }
+    m = stated_max(m, l);
 
     const int part0 = 2 * wg + (tile0 == 0 ? 1 : 0);    // where a part goes
     if constexpr (WK > 1) {

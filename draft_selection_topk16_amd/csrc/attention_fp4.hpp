@@ -447,6 +447,7 @@ __global__ __launch_bounds__(256, (FewShape<BF16, D, R>::kResident)) void k_atte
             pair_of<32>(l, x, y);
             l = x + y;
         }
+        m = stated_max(m, l);
 
         // The waves' results meet in LDS, scaled to the rows' common maximum, as in k_attend.
         const int part0 = 2 * wg + (tile0 == 0 ? 1 : 0);        // where a part goes

@@ -498,7 +498,8 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
  * of up to 64 rows (tokens of a sequence times Hq / Hkv, on average), and rounded
  * to bf16 in larger ones, as of prompt chunks.  Keys and values that a token of
  * the batch sees must be finite; whatever else stands in the pages is not
- * used.  The work is counted in tiles of 32 to 128 keys: (N * Hq / Hkv / 32 + B)
+ * used.  Queries must be finite or NaN: a head of a token whose query holds a NaN gives
+ * NaN, and no other output does.  The work is counted in tiles of 32 to 128 keys: (N * Hq / Hkv / 32 + B)
  * * Hkv times the tiles of a whole page table must stay below 2^31
  * (DF2_EUNSUPPORTED).
  */
@@ -543,7 +544,9 @@ df2_status dflash2_kv_append_fp4(const df2_paged_kv* kv, const void* q, int64_t 
  * bf16); scores, statistics and sums as there.  Scales of positions that a token of the
  * batch sees must be 7 to 247, as the append makes them for finite numbers; a sequence's
  * values, added up with weights of up to 2^8 before they are divided by the sum, must stay
- * finite in fp32 (any scale up to 2^90 will do).
+ * finite in fp32 (any scale up to 2^90 will do).  A block of keys with scale 255 makes the
+ * outputs of the tokens that see it NaN (of the heads that read that key head), a block of values
+ * leaves those of its sequence's tokens undefined; other sequences' are not touched.
  */
 size_t dflash2_paged_attention_fp4_workspace(const df2_paged_kv* kv, int32_t max_len);
 df2_status dflash2_paged_attention_fp4(const df2_paged_kv* kv, const void* q, int64_t q_stride,
