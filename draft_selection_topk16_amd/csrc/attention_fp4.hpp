@@ -385,13 +385,13 @@ __global__ __launch_bounds__(256, (FewShape<BF16, D, R>::kResident)) void k_atte
 #pragma unroll
                         for (int v = 0; v < AV; ++v) o[d][v] *= f;
                 }
-                float ms = m == -INFINITY ? 0.f : m;
-                if (__builtin_expect(huge, 0)) {
-                    const float back = 1.f / a.c;
+                float ms = m == -INFINITY ? 0.f : m, c = a.c;
+                if (__builtin_expect(huge, 0)) {        // as in k_attend
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
 #pragma unroll
-                        for (int v = 0; v < AV; ++v) s[i][v] = scaled_minus(s[i][v], a.c, ms) * back;
+                        for (int v = 0; v < AV; ++v) s[i][v] = scaled_minus(s[i][v], a.c, ms);
+                    c = 1.f;
                     ms = 0.f;
                 }
 
@@ -403,7 +403,7 @@ __global__ __launch_bounds__(256, (FewShape<BF16, D, R>::kResident)) void k_atte
 #pragma unroll
                     for (int i = 0; i < NE; ++i) {
                         const float x = R == 16 ? s[R == 16 ? i / 4 : 0][i % 4] : s[R == 16 ? 0 : T][R == 16 ? 0 : i];
-                        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x, a.c, -ms));
+                        e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x, c, -ms));
                         l += e[i];
                     }
                     uint32_t p[PP][NE / 2];
