@@ -87,7 +87,7 @@ struct AttnArgs {
     int bm;                 // rows of a block
     int wgs, whole;         // workgroups that take stretches; 1: each takes a whole block
     int cus;                // compute units
-    int join;               // workgroups that join the parts at a boundary; 0: there are none
+    int join;               // there may be parts, and a workspace for them
     int choose;             // blocks enough for the kernel to choose whole ones
     double inv_g;           // 1 / G
     float c;                // scale * log2(e)
@@ -848,7 +848,7 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
         // m is rounded and x * c below is not: from 2^26 on they differ by more than 1, and
         // from 2^31 on the exponential of the difference overflows.  There, both rounded, the
         // differences in x's place and a factor of 1 (scores put back in their own units
-        // here cost every tile registers: fp32 of 256 spilled 113 of them, not 75).
+        // here cost every tile registers: fp32 of 256 spilled 113 of them, not 78).
         float c = a.c;
         if (__builtin_expect(huge, 0)) {
 #pragma unroll
@@ -1111,27 +1111,27 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
 
 // Joins the parts of the blocks that lie across workgroups:
 //     sum_s 2^(m_s - m) (o_s, l_s)
-// over the parts s of a row.  Some workgroups (a.join) for each boundary of stretches, of
-// which the first inside a block does the block.  D / 4 lanes take a row, four parts
+// over the parts s of a row.  JOIN workgroups for each boundary of stretches, of which the
+// first inside a block does the block.  D / 4 lanes take a row, four parts
 // at a time; with more parts several such groups share the row and meet in LDS, so
 // that a hundred parts of a few rows are a few loads one after another.
 constexpr int kJoinThreads = 256;
-template <bool BF16, int D>
+template <bool BF16, int D, int JOIN>
 __global__ __launch_bounds__(kJoinThreads) void k_attend_join(AttnArgs a) {
     constexpr int L = D / 4, NG = kJoinThreads / L;
     __shared__ f32x4_t lds_y[kJoinThreads];
     __shared__ float lds_m[NG], lds_l[NG];
-    const int slice = blockIdx.x % (unsigned)a.join, boundary = 1 + blockIdx.x / (unsigned)a.join;
+    const int slice = blockIdx.x % JOIN, boundary = 1 + blockIdx.x / JOIN;
     const int32_t* split = a.split + 8 * boundary;
-    const int w0 = boundary - 1, w1 = min(split[0], (int)(gridDim.x / (unsigned)a.join));
+    const int w0 = boundary - 1, w1 = min(split[0], (int)(gridDim.x / JOIN));
     const int h = split[1], s0 = split[2], r0 = split[3], M = split[4];
     if (w1 < 0) return;
     const int group = threadIdx.x / L, d = (threadIdx.x % L) * 4;
     const int live = min(a.bm, M - r0);
     int share = 1;                                      // groups of a row, as long as one go takes all rows
-    while (4 * share < w1 - w0 + 1 && share < NG && live * share * 2 <= NG * a.join) share *= 2;
+    while (4 * share < w1 - w0 + 1 && share < NG && live * share * 2 <= NG * JOIN) share *= 2;
     const int at_once = NG / share;
-    for (int i0 = slice * at_once; i0 < live; i0 += a.join * at_once) {
+    for (int i0 = slice * at_once; i0 < live; i0 += JOIN * at_once) {
         const int i = i0 + group / share, r = r0 + i;
         float m = -INFINITY, l = 0.f;
         f32x4_t y = {0.f, 0.f, 0.f, 0.f};

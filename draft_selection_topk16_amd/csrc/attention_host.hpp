@@ -164,8 +164,18 @@ df2_status launch_attend(const AttnPlan& pl, const AttnArgs& a, hipStream_t stre
         return launched("dflash2_paged_attention launch");
     });
     if (st != DF2_OK || !a.join) return st;
-    hipLaunchKernelGGL((k_attend_join<BF16, D>), dim3((unsigned)(a.join * (pl.wgs - 1))),
-                       dim3(kJoinThreads), 0, stream, a);
+    // workgroups at a boundary: four for parts of up to 32 rows over a 4-bit cache, sixteen
+    const auto join = [&](auto each) {
+        constexpr int J = decltype(each)::value;
+        hipLaunchKernelGGL((k_attend_join<BF16, D, J>), dim3((unsigned)(J * (pl.wgs - 1))), dim3(kJoinThreads), 0, stream, a);
+    };
+    using std::integral_constant;
+    if constexpr (FP4) {
+        if (pl.wr <= 1) join(integral_constant<int, 4>());
+        else join(integral_constant<int, 16>());
+    } else {
+        join(integral_constant<int, 16>());
+    }
     return launched("dflash2_paged_attention join launch");
 }
 
@@ -222,7 +232,7 @@ df2_status attend(const df2_paged_kv* kv, const void* q, int64_t q_stride, float
     a.wgs = pl.wgs;
     a.whole = pl.whole;
     a.cus = compute_units();
-    a.join = pl.bytes == 0 ? 0 : FP4 && pl.wr <= 1 ? 4 : 16;
+    a.join = pl.bytes > 0;
     a.choose = pl.choose;
     a.inv_g = 1.0 / a.G;
     a.c = (float)((double)scale * 1.4426950408889634);
