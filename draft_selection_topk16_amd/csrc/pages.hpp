@@ -135,8 +135,9 @@ __global__ __launch_bounds__(NT) void k_plan_pages(PagesArgs a) {
             many[tid * K + k] = n[k];
         }
         __syncthreads();
-        for (int i = tid; i < items; i += NT) {
-            const int q = item_owner<CH>(upto, i);
+        // unsigned: `items` may be the largest int, where page counts are wrong
+        for (unsigned u = tid; u < (unsigned)items; u += NT) {
+            const int i = (int)u, q = item_owner<CH>(upto, i);
             f(i, q, base[q] + (i - (upto[q] - many[q])));
         }
         __syncthreads();

@@ -46,6 +46,7 @@ df2_status check_pool(const df2_page_pool* p) {
     if (p->page_size < 1 || (p->page_size & (p->page_size - 1)) || p->page_size > 65536)
         return fail_with(DF2_EUNSUPPORTED, "page_size must be a power of two up to 65536");
     if (p->num_pages < 1) return fail_with(DF2_EINVAL, "num_pages < 1");
+    if (p->num_pages > 1 << 30) return fail_with(DF2_EUNSUPPORTED, "num_pages above 2^30");
     if (p->table_width < 1 || p->table_stride < p->table_width)
         return fail_with(DF2_EINVAL, "table_width must be >= 1 and at most table_stride");
     if ((int64_t)p->table_width * p->page_size > (1 << 30))

@@ -636,7 +636,7 @@ df2_status dflash2_verify(const df2_verify_dims* dims, const void* target, const
  *               A page is in the list's first free_count entries or held once
  *   B           requests (0: nothing is enqueued), at most 2^20
  *   N           token rows of the step, at most 2^30
- *   page_size, num_pages, table_width as in df2_paged_kv
+ *   page_size, num_pages, table_width as in df2_paged_kv; num_pages at most 2^30
  * These four arrays are updated in place; calls that share them must be ordered.
  */
 typedef struct df2_page_pool {
@@ -657,7 +657,8 @@ typedef struct df2_page_pool {
  * A request wants ceil((ctx_len + advance + n_new) / page_size) pages, one that has
  * ended none.  First pages beyond that (after refused drafts, say) go to the end of the free
  * list, in the order of the requests and positions, and their table entries become
- * -1.  Then missing pages are taken, in the same order, each from the list's end.
+ * -1.  Then missing pages are taken, in the same order, each from the list's end. (Pages
+ * beyond what the list holds, where one was held twice, are dropped and raise bit 3.)
  * A request is served while all pages and rows that it and those before it ask for
  * are there; one that is not, or whose table is too narrow, keeps what it has and
  * gets no new tokens, and device flag bit 7 (bit 4: the table) is raised.
