@@ -86,7 +86,7 @@ df2_status dflash2_plan_pages(const df2_page_pool* pool, const int32_t* ctx_len,
             if (&o < &other && meet(o, other))
                 return fail_with(DF2_EINVAL, std::string(o.name) + " must not overlap " + other.name);
         for (const Span& in : ins)
-            if (!(o.p == ctx_out && in.p == ctx_out) && meet(o, in))
+            if (!(o.p == ctx_out && o.p == in.p && &in == ins) && meet(o, in))
                 return fail_with(DF2_EINVAL, std::string(o.name) + " must not overlap " + in.name);
     }
     PagesArgs a;

@@ -666,8 +666,8 @@ typedef struct df2_page_pool {
  *   tok_start   [B + 1] int32  first row of each request's new tokens
  *   slots       [N] int64   page id * page_size + place in the page of each row, or NULL
  *   positions   [N] int32   its position, or NULL; both are -1 in rows of no request
- * Outputs must not overlap one another or the inputs (but for ctx_out).  The result
- * is the same whenever the inputs are.
+ * Outputs must not overlap one another or the inputs, but for ctx_out in ctx_len's place
+ * (DF2_EINVAL).  The result is the same whenever the inputs are.
  */
 df2_status dflash2_plan_pages(const df2_page_pool* pool, const int32_t* ctx_len, const int32_t* advance,
                               const int32_t* n_new, int32_t* ctx_out, int32_t* tok_start,

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import draft_selection_topk16_amd as df2
-from test_steps_host import EUNSUPPORTED, plan
+from test_steps_host import EINVAL, EUNSUPPORTED, plan, spot
 
 
 @pytest.fixture(scope="module")
@@ -20,3 +20,14 @@ def test_pools_whose_pages_a_number_of_32_bits_cannot_step_through(lib):
     for pages in ((1 << 30) + 1, (1 << 31) - 1):
         assert plan(lib, num_pages=pages) == EUNSUPPORTED
         assert "num_pages above 2^30" in lib.dflash2_last_error().decode()
+
+
+def test_lengths_go_in_place_of_lengths_only(lib):
+    """ctx_out may be ctx_len; in place of the advances or the requests it would undo them for
+    the next call of a loop."""
+    for name, at in (("advance", spot(5)), ("n_new", spot(6))):
+        assert plan(lib, ctx_out=at) == EINVAL
+        assert "ctx_out must not overlap " + name in lib.dflash2_last_error().decode()
+    # nor where the advances are given as the lengths too
+    assert plan(lib, ctx_out=spot(4), advance=spot(4)) == EINVAL
+    assert "ctx_out must not overlap advance" in lib.dflash2_last_error().decode()
