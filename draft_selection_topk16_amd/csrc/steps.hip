@@ -31,6 +31,34 @@ bool meet(const Span& a, const Span& b) {
     return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
 }
 
+// Rows that are written (bytes; sequences hold their rows, which do not meet), and a list of
+// words in rows of its own: either may lie between rows of the other.
+struct OutRows {
+    uintptr_t at;
+    int64_t B, R, seq, row, bytes;
+};
+struct List {
+    const void* p;
+    int64_t B, R, seq, row, words;
+    const char* name;
+};
+bool rows_meet_list(const OutRows& o, const List& l) {
+    if (!l.p || l.words <= 0) return false;
+    const int64_t d = (int64_t)((uintptr_t)l.p - o.at);
+    const int64_t all = (o.B - 1) * o.seq + (o.R - 1) * o.row + o.bytes;
+    const int64_t list = ((l.B - 1) * l.seq + (l.R - 1) * l.row + l.words) * 4;
+    if (d >= all || d + list <= 0) return false;
+    for (int64_t i = 0; i < (l.seq ? l.B : 1); ++i)
+        for (int64_t j = 0; j < (l.row ? l.R : 1); ++j) {
+            // the row that its beginning is in or behind, and the next one
+            const int64_t x = d + (i * l.seq + j * l.row) * 4, end = x + l.words * 4;
+            for (int64_t b = o.seq && x > 0 ? std::min(x / o.seq, o.B - 1) : 0, b1 = std::min(b + 2, o.B); b < b1; ++b)
+                for (int64_t y = x - b * o.seq, t = y > 0 ? std::min(y / o.row, o.R - 1) : 0, t1 = std::min(t + 2, o.R); t < t1; ++t)
+                    if (x < b * o.seq + t * o.row + o.bytes && end > b * o.seq + t * o.row) return true;
+        }
+    return false;
+}
+
 // ----------------------------------------------------------------------------
 // Pages.
 // ----------------------------------------------------------------------------
@@ -163,6 +191,20 @@ df2_status dflash2_adjust_logits(const df2_adjust* d, const void* logits, void* 
     if (d->mask && ((d->R > 1 && d->mask_row_stride != 0 && d->mask_row_stride < words) ||
                     (d->B > 1 && d->mask_seq_stride != 0 && d->mask_seq_stride < words)))
         return fail_with(DF2_EINVAL, "mask strides must be 0 or hold a row");
+    // what is read of the lists while rows are written
+    const OutRows rows = {(uintptr_t)out, d->B, d->R, out_seq * size, out_row * size, (int64_t)d->V * size};
+    const List lists[] = {{history ? d->history : nullptr, d->B, 1, d->history_stride, 0, d->L, "history"},
+                          {history ? d->history_len : nullptr, 1, 1, 0, 0, d->B, "history_len"},
+                          {history ? d->prompt_len : nullptr, 1, 1, 0, 0, d->B, "prompt_len"},
+                          {path ? d->path : nullptr, 1, 1, 0, 0, (int64_t)d->B * (d->R - 1), "path"},
+                          {d->repetition, 1, 1, 0, 0, d->B, "repetition"},
+                          {d->frequency, 1, 1, 0, 0, d->B, "frequency"},
+                          {d->presence, 1, 1, 0, 0, d->B, "presence"},
+                          {biases ? d->bias_token : nullptr, 1, 1, 0, 0, (int64_t)d->B * d->M, "bias_token"},
+                          {biases ? d->bias : nullptr, 1, 1, 0, 0, (int64_t)d->B * d->M, "bias"},
+                          {d->mask, d->B, d->R, d->mask_seq_stride, d->mask_row_stride, words, "mask"}};
+    for (const List& l : lists)
+        if (rows_meet_list(rows, l)) return fail_with(DF2_EINVAL, std::string("out must not overlap ") + l.name);
     if (place && !history && !path && !biases && !d->mask) return DF2_OK;
 
     AdjustArgs a;

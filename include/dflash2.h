@@ -687,6 +687,7 @@ df2_status dflash2_plan_pages(const df2_page_pool* pool, const int32_t* ctx_len,
  *   logits, out  rows of V values (dtype), row t of sequence b at b * seq_stride +
  *                t * row_stride elements; out may be logits itself with the same
  *                strides (then only what changes is touched), else must not overlap it
+ *                (DF2_EINVAL); nor may a row of out overlap the lists, penalties or masks
  *   history      [B, L] int32, rows history_stride apart, or NULL; history_len [B]
  *                int32, clamped to [0, L]; prompt_len [B] int32, or NULL: 0
  *   path         [B, R - 1] int32, or NULL: no drafts

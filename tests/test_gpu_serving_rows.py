@@ -5,7 +5,7 @@ import torch
 
 import draft_selection_topk16_amd as df2
 from gpu_util import say
-from test_gpu_steps import i32
+from test_gpu_steps import check_rows, i32, on_gpu, rows_case
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,25 @@ def test_pages_given_back_beyond_the_list_are_dropped():
         assert df2.device_error() == 8 and count.item() == B + 1 and start.tolist() == [0] * (B + 1)
         assert free.tolist() == [-9, -9] + list(range(B - 1)) and bool((store[B + 1:] == -9).all())
         assert bool((table == -1).all()) and bool((held == 0).all())
+
+
+@pytest.mark.parametrize("place", [False, True])
+def test_rows_lists_and_masks_in_one_region_a_sequence(place):
+    """Histories behind each sequence's rows and masks behind each row of them: none of it
+    overlaps, and what lies between the rows stays."""
+    say("adjust regions", place)
+    x, c = rows_case(71, torch.float32, 3, 4, 1003, 70, 6, "half")
+    d, words = on_gpu(c), (1003 + 31) // 32
+    region = torch.zeros((3, 4 * 1100 + 80), dtype=torch.int32, device="cuda")
+    rows = region[:, :4400].unflatten(1, (4, 1100))
+    mask, history = rows[:, :, 1040:1040 + words], region[:, 4400:4470]
+    mask.copy_(d["mask"])
+    history.copy_(d["history"])
+    view = rows.view(torch.float32)[:, :, :1003]
+    src = x.cuda()
+    if place:
+        view.copy_(src)
+    got = df2.adjust_logits(view if place else src, **dict(d, history=history, mask=mask), out=view)
+    check_rows(x, c, got)
+    assert torch.equal(mask, d["mask"]) and torch.equal(history, d["history"])
+    assert bool((rows[:, :, 1003:1040] == 0).all()) and bool((rows[:, :, 1040 + words:] == 0).all())

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import draft_selection_topk16_amd as df2
-from test_steps_host import EINVAL, EUNSUPPORTED, plan, spot
+from test_steps_host import EINVAL, EUNSUPPORTED, OK, adjust, plan, spot
 
 
 @pytest.fixture(scope="module")
@@ -31,3 +31,28 @@ def test_lengths_go_in_place_of_lengths_only(lib):
     # nor where the advances are given as the lengths too
     assert plan(lib, ctx_out=spot(4), advance=spot(4)) == EINVAL
     assert "ctx_out must not overlap advance" in lib.dflash2_last_error().decode()
+
+
+SPOTS = dict(history=1, history_len=2, path=3, bias_token=4, bias=5, mask=6, prompt_len=7, repetition=8, frequency=9, presence=10)
+
+
+@pytest.mark.parametrize("name", sorted(SPOTS))
+def test_rows_must_not_be_written_over_what_is_read(lib, name):
+    """Two sequences of three rows of 100 bf16: 200 bytes each, 600 a sequence.  Lists that a
+    row of out begins or ends in, or that lie in a row."""
+    for at in (spot(64), spot(64) + 1196, spot(64) + 700, spot(64) - 4):
+        assert adjust(lib, **{"prompt_len": spot(7), "repetition": spot(8), "frequency": spot(9), "presence": spot(10), name: at}) == EINVAL
+        said = lib.dflash2_last_error().decode()
+        assert said == "out must not overlap " + name, said
+    # and in place
+    assert adjust(lib, out=spot(0), **{"prompt_len": spot(7), name: spot(0) + 400}) == EINVAL
+    assert "out must not overlap " + name in lib.dflash2_last_error().decode()
+
+
+def test_lists_may_lie_between_rows(lib):
+    """Rows of 100 bf16 that are 256 bytes apart, sequences 1024: penalties of two sequences
+    (8 bytes) in every place of four bytes, in a call in place that has nothing else to do."""
+    kw = dict(out=spot(0), row_stride=128, out_row_stride=128, seq_stride=512, out_seq_stride=512, history=None, path=None, M=0, mask=None)
+    for at in range(-16, 2048, 4):
+        hit = any(at < b * 1024 + t * 256 + 200 and at + 8 > b * 1024 + t * 256 for b in range(2) for t in range(3))
+        assert adjust(lib, repetition=spot(0) + at, **kw) == (EINVAL if hit else OK), at
