@@ -170,6 +170,8 @@ df2_status dflash2_adjust_logits(const df2_adjust* d, const void* logits, void* 
     const int size = d->dtype == DF2_BF16 ? 2 : 4;
     if (!aligned(logits, size) || !aligned(out, size)) return fail_with(DF2_EINVAL, "logits or out misaligned for the dtype");
     const bool history = d->history && d->L > 0, path = d->path && d->R > 1, biases = d->M > 0;
+    if ((history ? d->L : 0) + (path ? (int64_t)d->R - 1 : 0) >= 1 << 29)
+        return fail_with(DF2_EUNSUPPORTED, "L and the drafts together must be below 2^29");
     if (history && !d->history_len) return fail_with(DF2_EINVAL, "history without history_len");
     if (history && d->history_stride < d->L) return fail_with(DF2_EINVAL, "history_stride below L");
     if (biases && (!d->bias_token || !d->bias)) return fail_with(DF2_EINVAL, "M > 0 without bias_token and bias");

@@ -697,7 +697,7 @@ df2_status dflash2_plan_pages(const df2_page_pool* pool, const int32_t* ctx_len,
  *                is allowed; mask_seq_stride and mask_row_stride in words, 0: one row
  *                for all; or NULL
  * Ids outside [0, V) in the lists are left out (-1 fills them up).  B or R 0: nothing
- * is enqueued.  V <= 2^29, L < 2^29.
+ * is enqueued.  V <= 2^29, L (with path, L + R - 1) < 2^29.
  */
 typedef struct df2_adjust {
     int32_t B, R, V, L, M;

@@ -55,3 +55,15 @@ def test_rows_lists_and_masks_in_one_region_a_sequence(place):
     check_rows(x, c, got)
     assert torch.equal(mask, d["mask"]) and torch.equal(history, d["history"])
     assert bool((rows[:, :, 1003:1040] == 0).all()) and bool((rows[:, :, 1040 + words:] == 0).all())
+
+
+@pytest.mark.parametrize("R,V", [(37, 70001), (300, 4099), (700, 40)])
+@pytest.mark.parametrize("place", [False, True])
+def test_drafts_before_and_between_the_rows_of_a_workgroup(R, V, place):
+    """Many rows are divided over workgroups: a draft counts from the row behind it on, in its
+    own workgroup and in those of later rows, as often as it was drafted."""
+    say("adjust many rows", R, V, place)
+    x, c = rows_case(81 + R, torch.bfloat16, 1, R, V, 9, 4, "half")
+    c["path"] = (c["path"].long() % max(V // 50, 7)).int()              # the same few words again and again
+    d = x.cuda()
+    check_rows(x, c, df2.adjust_logits(d, **on_gpu(c), out=d if place else None))

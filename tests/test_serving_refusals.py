@@ -56,3 +56,9 @@ def test_lists_may_lie_between_rows(lib):
     for at in range(-16, 2048, 4):
         hit = any(at < b * 1024 + t * 256 + 200 and at + 8 > b * 1024 + t * 256 for b in range(2) for t in range(3))
         assert adjust(lib, repetition=spot(0) + at, **kw) == (EINVAL if hit else OK), at
+
+
+def test_tokens_beyond_what_a_count_holds(lib):
+    far = dict(B=1, R=1 << 28, V=1, row_stride=1, out_row_stride=1, history_stride=1 << 28, out=1 << 61, M=0, mask=None)
+    assert adjust(lib, L=(1 << 28) + 1, **far) == EUNSUPPORTED
+    assert "together" in lib.dflash2_last_error().decode()
