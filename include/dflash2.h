@@ -495,7 +495,8 @@ df2_status dflash2_kv_append(const df2_paged_kv* kv, const void* q, int64_t q_st
  *           NULL), 16-byte aligned
  * Scores, softmax statistics and sums are fp32.  The probabilities of bf16 calls
  * enter the second product with 16 bits (a bf16 high part and a low one) in blocks
- * of up to 64 rows (tokens of a sequence times Hq / Hkv, on average), and rounded
+ * of up to 64 rows (tokens of a sequence times Hq / Hkv, on average: N * Hq / Hkv
+ * over the smaller of B and N, rows and sequences that are idle among them), and rounded
  * to bf16 in larger ones, as of prompt chunks.  Keys and values that a token of
  * the batch sees must be finite; whatever else stands in the pages is not
  * used.  Queries must be finite or NaN: a head of a token whose query holds a NaN gives
@@ -527,9 +528,10 @@ df2_status dflash2_paged_attention(const df2_paged_kv* kv, const void* q, int64_
  */
 
 /*
- * dflash2_kv_append into a 4-bit cache: same arguments, same queries.  Keys are normed
- * and rotated in fp64 and rounded once, to their codes, so that a cache depends on
- * nothing but its tokens.
+ * dflash2_kv_append into a 4-bit cache: same arguments, and queries by the same formula in
+ * fp32 (their turns are made in fp64, so last bits may differ).  Keys are normed and
+ * rotated in fp64 and rounded once, to their codes, so that a cache depends on nothing
+ * but its tokens.
  */
 df2_status dflash2_kv_append_fp4(const df2_paged_kv* kv, const void* q, int64_t q_stride,
                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -540,11 +542,11 @@ df2_status dflash2_kv_append_fp4(const df2_paged_kv* kv, const void* q, int64_t 
 /*
  * dflash2_paged_attention over a 4-bit cache: same arguments, and the softmax over the
  * values that the codes stand for.  bf16 calls multiply them as bf16, which they are
- * exactly, and give probabilities 16 bits in blocks of up to 32 rows (above, rounded to
- * bf16); scores, statistics and sums as there.  Scales of positions that a token of the
+ * exactly, and give probabilities 16 bits in blocks of up to 32 rows (counted as there;
+ * above, rounded to bf16); scores, statistics and sums as there.  Scales of positions that a token of the
  * batch sees must be 7 to 247, as the append makes them for finite numbers; a sequence's
  * values, added up with weights of up to 2^8 before they are divided by the sum, must stay
- * finite in fp32 (any scale up to 2^90 will do).  A block of keys with scale 255 makes the
+ * finite in fp32 (any scale up to 2^87 will do: 6 * 2^(87 + 8 + 30) is below 2^128).  A block of keys with scale 255 makes the
  * outputs of the tokens that see it NaN (of the heads that read that key head), a block of values
  * leaves those of its sequence's tokens undefined; other sequences' are not touched.
  */
@@ -556,8 +558,8 @@ df2_status dflash2_paged_attention_fp4(const df2_paged_kv* kv, const void* q, in
                                        hipStream_t stream);
 
 /*
- * What all pages of a 4-bit cache hold, as numbers (dtype; exact but for scales whose
- * values leave its range): out_k, out_v [num_pages, Hkv, page_size, D], 16-byte aligned, a
+ * What all pages of a 4-bit cache hold, as numbers (dtype; exact, but infinities
+ * beyond its range: under the scales 253 and 254): out_k, out_v [num_pages, Hkv, page_size, D], 16-byte aligned, a
  * cache as the operators over one of that type take it.  They must not overlap the cache
  * or each other.  block_table, ctx_len and tok_start may be NULL, B and N 0.  Up to 2^34
  * values in each.

@@ -250,3 +250,38 @@ def test_single_tokens_beside_a_chunk_and_many_idle_rows(fp4, dtype):
             got = attend(wide, max_len=max_len, out=out.clone()).cpu().double()
             assert bool(((got[:len(ref)] - ref).abs() <= bound).all()) and bool((got[len(ref):] == -7.0).all())
     assert df2.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,D,n", [(BF, 128, 1), (BF, 128, 8), (BF, 64, 16), (BF, 128, 60), (F32, 128, 1), (F32, 256, 9)])
+def test_values_up_to_the_documented_scale(dtype, D, n):
+    """Values times 2^87: every product and sum is the same but for its exponent, up to the
+    largest values under the largest weights, so the outputs are those times 2^87, bit for bit
+    (none is near the other end of the exponents)."""
+    say("large values", dtype, D, n)
+    c = case(True, n + D, dtype, D, 8, 2, 16, [n, n], [20000, 3])
+    scales = c["v_cache"][:, :, 8 * D:]
+    scales.fill_(127)
+    want = attend(c)
+    scales.fill_(127 + 87)
+    got = attend(c)
+    assert bool(torch.isfinite(got).all()) and float(got.abs().max()) > 2.0 ** 80
+    tiny = want.abs() < 2.0 ** -60                      # weights that vanish beside the largest
+    assert torch.equal(got[~tiny], (want * 2.0 ** 87)[~tiny]) and float(tiny.double().mean()) < 0.2
+    assert df2.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_unpack_at_the_ends_of_the_scales(dtype):
+    """All codes under the smallest and the largest scales: subnormal numbers under 0, exact up
+    to the end of the range, infinities beyond it, NaN under 255."""
+    say("unpack ends", dtype)
+    which = [0, 1, 2, 6, 7, 126, 127, 128, 247, 250, 251, 252, 253, 254, 255, 0]
+    cache = torch.zeros((1, 1, 16 * 34), dtype=torch.uint8)
+    cache[..., :16 * 32] = (torch.arange(16).repeat(32) * 17).to(torch.uint8)       # both halves of byte i: code i % 16
+    cache[..., 16 * 32:] = torch.tensor(which, dtype=torch.uint8).repeat_interleave(2)
+    ref = held(cache, 16, 64)
+    most = torch.finfo(dtype).max
+    ref = torch.where(ref.abs() > most, torch.sign(ref) * float("inf"), ref)
+    assert bool(torch.isinf(ref).any()) and bool(((ref != 0) & (ref.abs() < 2.0 ** -126)).any())
+    for got in df2.kv_unpack_fp4(cache.cuda(), cache.cuda(), 64, dtype):
+        assert torch.equal(torch.nan_to_num(got.cpu().double(), 12345.0, 1e300, -1e300), torch.nan_to_num(ref, 12345.0, 1e300, -1e300))
