@@ -18,7 +18,8 @@
 // thread to a token for all rows.  (With both in one pass nearly every wave went through
 // the arithmetic for all eight elements of its vectors, for a token here and there: 512
 // rows of 151936 in place, half of them masked, 136 us, now 72, of which the single elements'
-// lines are some 40.  8 rows into another tensor: 6.6 us, latency.)  Nothing is kept between calls, so a history may be edited at will.
+// lines are some 40.  8 rows into another tensor: 6.0 us, latency.)  Nothing is kept between
+// calls, so a history may be edited at will.
 //
 // Every load waits for most of a microsecond, so they go out several at a time: four
 // vectors of the history, the masks of all rows into LDS at once, four vectors or elements of

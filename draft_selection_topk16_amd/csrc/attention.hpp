@@ -448,7 +448,8 @@ struct AttnTile {
     static constexpr int kRow = D * kEsz;       // bytes of a key
     static constexpr int kChunks = kRow / 16;
     // From 4-bit values: both, and 16 lanes write whole blocks of four chunks of rows that
-    // are four apart.
+    // are four apart (writes meet all the same, eight cycles each: 32% of the cycles that the LDS
+    // works in blocks of 64 rows).
     static __device__ __forceinline__ int swz_fp4(int row) {
         return kChunks >= 16 ? (row & 3) << 2 | ((row >> 2) & 3) : ((row >> 1) & 1) << 2 | ((row >> 2) & 3);
     }
@@ -839,7 +840,8 @@ __global__ __launch_bounds__(64 * WR * WK, (AttnShape<BF16, D, WR, WK, KS, NS, F
     // tenth by it (79 and 87) and prompt chunks more (690 and 940), so there the weights
     // are rounded.  Outputs against fp64, relative: 2.1e-3 without it, 1.7e-3, the
     // rounding of the output alone, with it.  Over a 4-bit cache blocks of 64 rows are bound
-    // by the products too, and do without (32 contexts: 119 us with it, 103; 2.1e-3).
+    // by the products too, and do without (32 contexts of 64 / 8 heads: 126 us with it, 105;
+    // of 64 elements 86 and 76, of 256 105 and 98; 2.2e-3).
     constexpr bool kLow = BF16 && WR <= 2 && !FP4;
     constexpr int PN = BF16 ? (kLow ? 16 : 8) : 16;
     bool huge = false;                  // some row's maximum is beyond 2^26

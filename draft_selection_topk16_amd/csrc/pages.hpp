@@ -13,8 +13,10 @@
 // lanes and then over the waves in LDS.  It is bound by latency: a pass is a few loads and
 // scans one after the other, so with up to 4096 requests they are read once (3000 of them
 // with 93 thousand rows, a thousand at a time: 42 us).  What follows per row (slots and
-// positions) is work for the whole chip where there are many rows, in a second launch;
-// with up to kPageRows rows the same workgroup does it.
+// positions) is work for the whole chip where there are many rows, in a second launch, waves to
+// a request; with up to kPageRows rows the same workgroup does it.  (Where one request, or the
+// idle rows behind the last, are most of a large step, its waves bound it: 3000 requests in
+// a step of 131072 rows with 3000 used 186 us.)
 #pragma once
 
 #include "attention.hpp"

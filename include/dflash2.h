@@ -653,8 +653,8 @@ typedef struct df2_page_pool {
 /*
  *   ctx_len     [B] int32   tokens that each request had in the cache before the last
  *               step, or what is left of them
- *   advance     [B] int32   tokens that have joined them since, or NULL: none; a sum
- *               below 0 counts as 0
+ *   advance     [B] int32   tokens that have joined them since (none of a request that was not
+ *               served), or NULL: none; a sum below 0 counts as 0
  *   n_new       [B] int32   new tokens it brings; negative: the request has ended
  * A request wants ceil((ctx_len + advance + n_new) / page_size) pages, one that has
  * ended none.  First pages beyond that (after refused drafts, say) go to the end of the free
